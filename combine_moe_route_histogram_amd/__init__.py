@@ -22,7 +22,8 @@ __all__ = [
     "moe_expert_ffn_bwd_weight", "moe_dispatch_bwd", "moe_route_bwd", "moe_expert_ffn_bwd_act",
     "moe_expert_ffn_bwd_input", "moe_expert_ffn_bwd_weight_gate_up", "moe_expert_ffn_bwd_weight_down",
     "moe_expert_ffn_bwd", "moe_sync_status", "moe_route_noalloc", "Tuning", "moe_get_tuning",
-    "moe_tuning_predict",
+    "moe_tuning_predict", "moe_decode_workspace_bytes", "moe_decode", "moe_decode_mx", "moe_mx_bytes",
+    "moe_mx_quantize", "moe_mx_dequantize",
 ]
 
 F32, BF16 = 0, 1
@@ -113,6 +114,12 @@ _SIGS = {
     "moe_expert_ffn_bwd_weight_down": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_dispatch_bwd": (ctypes.c_int, [_D, _P, _P, _P, _P]),
     "moe_route_bwd": (ctypes.c_int, [_D, _P, _P, _P, _P, _P]),
+    "moe_decode_workspace_bytes": (ctypes.c_size_t, [_D]),
+    "moe_decode": (ctypes.c_int, [_D] + [_P] * 13 + [ctypes.c_size_t, _P]),
+    "moe_decode_mx": (ctypes.c_int, [_D] + [_P] * 13 + [ctypes.c_size_t, _P]),
+    "moe_mx_bytes": (ctypes.c_size_t, [ctypes.c_int] * 3),
+    "moe_mx_quantize": (ctypes.c_int, [ctypes.c_int] * 4 + [_P, _P, _P]),
+    "moe_mx_dequantize": (ctypes.c_int, [ctypes.c_int] * 4 + [_P, _P, _P]),
 }
 
 _lib = None
@@ -187,6 +194,15 @@ def _ptr(t, name, dtype=None, numel=None):
     if numel is not None and t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
     return t.data_ptr()
+
+
+def _one_device(stream, **tensors):
+    """Refuse tensors of different devices, or of another one than the work runs on: a kernel
+    would read memory that its device may not reach."""
+    device = stream.device if isinstance(stream, torch.cuda.Stream) else torch.device("cuda", torch.cuda.current_device())
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
 
 
 def _stream(stream):
@@ -421,3 +437,66 @@ def moe_route_bwd(d: Dims, dtopk_w, topk_w, topk_idx, dlogits, stream=None):
     _call("moe_route_bwd", ctypes.byref(d), _ptr(dtopk_w, "dtopk_w", f32, d.T * d.K),
           _ptr(topk_w, "topk_w", f32, d.T * d.K), _ptr(topk_idx, "topk_idx", torch.int32, d.T * d.K),
           _ptr(dlogits, "dlogits", f32, d.T * d.E), _stream(stream))
+
+
+# ---------------------------------------------------------------- a few tokens, 4-bit weights
+
+def moe_decode_workspace_bytes(d: Dims) -> int:
+    return int(load().moe_decode_workspace_bytes(ctypes.byref(d)))
+
+
+def _decode(name, d, dt, numels, logits, x, weights, n_tokens, topk_idx, topk_w, out, ws, stream):
+    T, K = d.T, d.K
+    wp, wn = _ws(ws)
+    args = [_ptr(logits, "logits", torch.float32, T * d.E), _ptr(x, "x", d.torch_dtype, T * d.H),
+            *(_ptr(t, w, dt, n) for (w, t), n in zip(weights.items(), numels)),
+            _ptr(n_tokens, "n_tokens", torch.int32, 1), _ptr(topk_idx, "topk_idx", torch.int32, T * K),
+            _ptr(topk_w, "topk_w", torch.float32, T * K), _ptr(out, "out", d.torch_dtype, T * d.H), wp, wn]
+    _one_device(stream, logits=logits, x=x, **weights, n_tokens=n_tokens, topk_idx=topk_idx, topk_w=topk_w,
+                out=out, ws=ws)
+    _call(name, ctypes.byref(d), *args, _stream(stream))
+
+
+def moe_decode(d: Dims, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws,
+               stream=None):
+    n, ns = d.E * d.H * d.I, d.n_shared * d.H * d.I
+    _decode("moe_decode", d, d.torch_dtype, (n, n, n, ns, ns, ns), logits, x,
+            dict(w1=w1, w3=w3, w2=w2, ws1=ws1, ws3=ws3, ws2=ws2), n_tokens, topk_idx, topk_w, out, ws, stream)
+
+
+def moe_decode_mx(d: Dims, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws,
+                  stream=None):
+    """moe_decode on packed weights: uint8 tensors of moe_mx_bytes, as moe_mx_quantize writes them."""
+    n, ns = _mx_numel(d.E, d.H, d.I), _mx_numel(d.n_shared, d.H, d.I)
+    _decode("moe_decode_mx", d, torch.uint8, (n, n, n, ns, ns, ns), logits, x,
+            dict(w1=w1, w3=w3, w2=w2, ws1=ws1, ws3=ws3, ws2=ws2), n_tokens, topk_idx, topk_w, out, ws, stream)
+
+
+def _mx_numel(G, K, N):
+    return G * K * N // 32 * 17
+
+
+def moe_mx_bytes(G: int, K: int, N: int) -> int:
+    return int(load().moe_mx_bytes(G, K, N))
+
+
+def _mx_dtype(w):
+    """MOE_F32 or MOE_BF16 of a weight tensor (None: bf16, the call reports the NULL)."""
+    if w is None:
+        return BF16
+    for code, dt in _TORCH_DTYPE.items():
+        if w.dtype == dt:
+            return code
+    raise TypeError(f"w must be {torch.float32} or {torch.bfloat16} (got {w.dtype})")
+
+
+def moe_mx_quantize(G: int, K: int, N: int, w, mx, stream=None):
+    code, wp, mp = _mx_dtype(w), _ptr(w, "w", None, G * K * N), _ptr(mx, "mx", torch.uint8, _mx_numel(G, K, N))
+    _one_device(stream, w=w, mx=mx)
+    _call("moe_mx_quantize", G, K, N, code, wp, mp, _stream(stream))
+
+
+def moe_mx_dequantize(G: int, K: int, N: int, mx, w, stream=None):
+    code, wp, mp = _mx_dtype(w), _ptr(w, "w", None, G * K * N), _ptr(mx, "mx", torch.uint8, _mx_numel(G, K, N))
+    _one_device(stream, w=w, mx=mx)
+    _call("moe_mx_dequantize", G, K, N, code, mp, wp, _stream(stream))

@@ -1,0 +1,60 @@
+// Host-side launchers of the layer for a few tokens (decode.hip) and of the
+// 4-bit weight format (mx.hip); internal, the public ABI is moe.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// Tokens a decode call takes at most (one routing block holds them all).
+constexpr int kDecodeMaxTokens = 256;
+// Largest H and I of the decode calls (lane offsets into a matrix's rows are
+// formed in 32 bits inside a k step).
+constexpr int kDecodeMaxDim = 1 << 20;
+
+// Weights along the reduction dim that share one scale, and the bytes of
+// their codes.
+constexpr int kMxGroup = 32;
+constexpr int kMxCodeBytes = 16;
+
+// Where the down projection's partial sums are cut: S slices of `steps` k
+// steps each.
+struct DecodePlan {
+  int row_tile;     // rows of one entry at most (16 or 32)
+  int entries;      // bound on the number of entries (expert x row tile)
+  int up_tiles;     // column tiles of the gate/up projection
+  int down_tiles;   // column tiles of the down projection
+  int slices;       // k slices of the down projection
+  int slice_steps;  // k steps in each
+};
+DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I, int Ns);
+
+struct DecodeArgs {
+  int T, H, E, K, I, Ns, R;
+  const float* logits;
+  const void* x;
+  const void* w1;
+  const void* w3;
+  const void* w2;
+  const void* ws1;
+  const void* ws3;
+  const void* ws2;
+  const int32_t* n_tokens;  // null: T
+  int32_t* topk_idx;
+  float* topk_w;
+  void* out;
+  // workspace
+  int4* entries;       // {group, first row, rows, 0}
+  int32_t* n_entries;
+  int32_t* row_token;  // [R] token of each routed row
+  int32_t* slot;       // [T, K] row of each pair
+  void* h;             // [RA, I]: f32, or two bf16 planes (value, then what it left)
+  float* y;            // [slices, RA, H]
+};
+hipError_t launch_decode(bool is_bf16, bool mx, const DecodeArgs& a, const DecodePlan& p, hipStream_t st);
+
+hipError_t launch_mx_quantize(bool is_bf16, int64_t G, int K, int N, const void* w, void* mx, hipStream_t st);
+hipError_t launch_mx_dequantize(bool is_bf16, int64_t G, int K, int N, const void* mx, void* w, hipStream_t st);
+
+}  // namespace moe

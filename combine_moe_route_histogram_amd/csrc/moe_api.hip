@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/moe.h"
+#include "decode.hpp"
 #include "kernels.hpp"
 #include "tuning.hpp"
 
@@ -295,6 +296,102 @@ int fused_ws(const moe_dims* d, void* ws, FusedWs* w) {
   // depend on how many workers share the tasks
   const int n = debug_settings().fused_workers;
   if (n > 0) w->workers = n;
+  return MOE_OK;
+}
+
+// ---- the layer for a few tokens (moe_decode, moe_decode_mx)
+
+int check_decode_dims(const moe_dims* d, bool mx) {
+  MOE_TRY(check_dims(d));
+  if (d->T > kDecodeMaxTokens)
+    return fail(MOE_EUNSUPPORTED, "a decode call takes at most %d tokens (T=%d)", kDecodeMaxTokens, d->T);
+  if (d->H > kDecodeMaxDim || d->I > kDecodeMaxDim)
+    return fail(MOE_EUNSUPPORTED, "a decode call takes H and I up to %d (H=%d, I=%d)", kDecodeMaxDim, d->H, d->I);
+  if (mx && (d->H % kMxGroup || d->I % kMxGroup))
+    return fail(MOE_EUNSUPPORTED, "4-bit weights need H and I to be multiples of %d (H=%d, I=%d)", kMxGroup,
+                d->H, d->I);
+  return MOE_OK;
+}
+
+DecodePlan decode_plan_for(const moe_dims* d, bool mx) {
+  return decode_plan(d->dtype == MOE_BF16, mx, d->T, d->H, d->E, d->K, d->I, d->n_shared);
+}
+
+// Workspace sections of a decode call (byte offsets); one layout for both
+// weight forms, sized for the larger.
+struct DecodeLayout {
+  size_t entries, n_entries, row_token, slot, h, y, total;
+};
+DecodeLayout decode_layout(const moe_dims* d) {
+  const bool mx_ok = d->H % kMxGroup == 0 && d->I % kMxGroup == 0;
+  const DecodePlan a = decode_plan_for(d, false), b = mx_ok ? decode_plan_for(d, true) : a;
+  const size_t R = (size_t)d->T * d->K, RA = R + (size_t)d->n_shared * d->T;
+  const size_t entries = a.entries > b.entries ? a.entries : b.entries;
+  const size_t slices = a.slices > b.slices ? a.slices : b.slices;
+  DecodeLayout L;
+  size_t off = 0;
+  L.entries = off;   off = align_up(off + entries * 16);
+  L.n_entries = off; off = align_up(off + 16);
+  L.row_token = off; off = align_up(off + R * 4);
+  L.slot = off;      off = align_up(off + R * 4);
+  L.h = off;         off = align_up(off + RA * d->I * 4);
+  L.y = off;         off = align_up(off + slices * RA * d->H * 4);
+  L.total = off;
+  return L;
+}
+
+int decode(const moe_dims* d, bool mx, const float* logits, const void* x, const void* w1, const void* w3,
+           const void* w2, const void* ws1, const void* ws3, const void* ws2, const int32_t* n_tokens,
+           int32_t* topk_idx, float* topk_w, void* out, void* ws, size_t ws_bytes, void* stream,
+           const char* what) {
+  MOE_TRY(check_decode_dims(d, mx));
+  MOE_TRY(check_ptr(logits, "logits"));
+  MOE_TRY(check_ptr(x, "x"));
+  MOE_TRY(check_ptr(w1, "w1"));
+  MOE_TRY(check_ptr(w3, "w3"));
+  MOE_TRY(check_ptr(w2, "w2"));
+  if (d->n_shared > 0) {
+    MOE_TRY(check_ptr(ws1, "ws1"));
+    MOE_TRY(check_ptr(ws3, "ws3"));
+    MOE_TRY(check_ptr(ws2, "ws2"));
+  }
+  if (reinterpret_cast<uintptr_t>(n_tokens) % 4)
+    return fail(MOE_EINVAL, "n_tokens is not 4-byte aligned");
+  MOE_TRY(check_ptr(topk_idx, "topk_idx"));
+  MOE_TRY(check_ptr(topk_w, "topk_w"));
+  MOE_TRY(check_ptr(out, "out"));
+  const DecodeLayout L = decode_layout(d);
+  if (!ws) return fail(MOE_EWORKSPACE, "workspace is NULL (need %zu bytes)", L.total);
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign)
+    return fail(MOE_EWORKSPACE, "workspace must be %zu-byte aligned", kAlign);
+  if (ws_bytes < L.total)
+    return fail(MOE_EWORKSPACE, "workspace has %zu bytes, need %zu", ws_bytes, L.total);
+  DecodeArgs a{};
+  a.T = d->T; a.H = d->H; a.E = d->E; a.K = d->K; a.I = d->I; a.Ns = d->n_shared;
+  a.R = d->T * d->K;
+  a.logits = logits; a.x = x;
+  a.w1 = w1; a.w3 = w3; a.w2 = w2; a.ws1 = ws1; a.ws3 = ws3; a.ws2 = ws2;
+  a.n_tokens = n_tokens;
+  a.topk_idx = topk_idx; a.topk_w = topk_w; a.out = out;
+  a.entries = ws_at<int4>(ws, L.entries);
+  a.n_entries = ws_at<int32_t>(ws, L.n_entries);
+  a.row_token = ws_at<int32_t>(ws, L.row_token);
+  a.slot = ws_at<int32_t>(ws, L.slot);
+  a.h = ws_at<char>(ws, L.h);
+  a.y = ws_at<float>(ws, L.y);
+  return hip_status(launch_decode(d->dtype == MOE_BF16, mx, a, decode_plan_for(d, mx), as_stream(stream)), what);
+}
+
+int check_mx(int64_t G, int K, int N, int dtype) {
+  if (G < 1) return fail(MOE_EINVAL, "G must be >= 1 (got %lld)", (long long)G);
+  if (K <= 0 || K % kMxGroup)
+    return fail(MOE_EUNSUPPORTED, "K must be a positive multiple of %d (got %d)", kMxGroup, K);
+  if (N <= 0 || N % 8) return fail(MOE_EUNSUPPORTED, "N must be a positive multiple of 8 (got %d)", N);
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_EUNSUPPORTED, "dtype must be MOE_F32 or MOE_BF16 (got %d)", dtype);
+  // one thread takes 32 x 4 weights, and a launch holds less than 2^32 threads
+  if ((double)G * (K / kMxGroup) * (N / 4) > 4294967040.0)
+    return fail(MOE_EUNSUPPORTED, "G*K*N must be at most 2^39 (G=%lld, K=%d, N=%d)", (long long)G, K, N);
   return MOE_OK;
 }
 
@@ -762,6 +859,45 @@ int moe_route_bwd(const moe_dims* d, const float* dtopk_w, const float* topk_w,
   return hip_status(launch_route_bwd(dtopk_w, topk_w, topk_idx, dlogits, d->T, d->E, d->K,
                                      as_stream(stream)),
                     "moe_route_bwd");
+}
+
+size_t moe_decode_workspace_bytes(const moe_dims* d) {
+  if (check_decode_dims(d, false) != MOE_OK) return 0;
+  return decode_layout(d).total;
+}
+
+int moe_decode(const moe_dims* d, const float* logits, const void* x, const void* w1, const void* w3,
+               const void* w2, const void* ws1, const void* ws3, const void* ws2, const int32_t* n_tokens,
+               int32_t* topk_idx, float* topk_w, void* out, void* ws, size_t ws_bytes, void* stream) {
+  return decode(d, false, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws, ws_bytes,
+                stream, "moe_decode");
+}
+
+int moe_decode_mx(const moe_dims* d, const float* logits, const void* x, const void* w1, const void* w3,
+                  const void* w2, const void* ws1, const void* ws3, const void* ws2, const int32_t* n_tokens,
+                  int32_t* topk_idx, float* topk_w, void* out, void* ws, size_t ws_bytes, void* stream) {
+  return decode(d, true, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws, ws_bytes,
+                stream, "moe_decode_mx");
+}
+
+size_t moe_mx_bytes(int G, int K, int N) {
+  if (check_mx(G, K, N, MOE_BF16) != MOE_OK) return 0;
+  return (size_t)G * (K / kMxGroup) * N * (kMxCodeBytes + 1);
+}
+
+int moe_mx_quantize(int G, int K, int N, int dtype, const void* w, void* mx, void* stream) {
+  MOE_TRY(check_mx(G, K, N, dtype));
+  MOE_TRY(check_ptr(w, "w"));
+  MOE_TRY(check_ptr(mx, "mx"));
+  return hip_status(launch_mx_quantize(dtype == MOE_BF16, G, K, N, w, mx, as_stream(stream)), "moe_mx_quantize");
+}
+
+int moe_mx_dequantize(int G, int K, int N, int dtype, const void* mx, void* w, void* stream) {
+  MOE_TRY(check_mx(G, K, N, dtype));
+  MOE_TRY(check_ptr(mx, "mx"));
+  MOE_TRY(check_ptr(w, "w"));
+  return hip_status(launch_mx_dequantize(dtype == MOE_BF16, G, K, N, mx, w, as_stream(stream)),
+                    "moe_mx_dequantize");
 }
 
 }  // extern "C"

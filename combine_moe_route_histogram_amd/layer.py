@@ -9,10 +9,11 @@ from __future__ import annotations
 
 import torch
 
-from . import (BF16, F32, Dims, moe_combine, moe_combine_bwd, moe_dispatch, moe_dispatch_bwd,
-               moe_dispatch_ffn, moe_expert_ffn_bwd, moe_expert_ffn_bwd_data, moe_expert_ffn_bwd_weight,
-               moe_expert_ffn_down, moe_expert_ffn_up, moe_ffn_combine, moe_route, moe_route_bwd,
-               moe_sync_status, moe_workspace_bytes)
+from . import (BF16, F32, Dims, moe_combine, moe_combine_bwd, moe_decode, moe_decode_mx,
+               moe_decode_workspace_bytes, moe_dispatch, moe_dispatch_bwd, moe_dispatch_ffn,
+               moe_expert_ffn_bwd, moe_expert_ffn_bwd_data, moe_expert_ffn_bwd_weight,
+               moe_expert_ffn_down, moe_expert_ffn_up, moe_ffn_combine, moe_mx_bytes, moe_mx_quantize,
+               moe_route, moe_route_bwd, moe_sync_status, moe_workspace_bytes)
 
 
 def make_dims(T, H, E, K, I, n_shared=0, dtype="bf16", I_shared=None) -> Dims:
@@ -102,3 +103,36 @@ def check(stream=None):
     """Wait for the step's work and raise MoeError (MOE_ETIMEOUT) if a bounded
     wait inside a persistent kernel gave up, which leaves invalid results."""
     moe_sync_status(stream)
+
+
+class DecodeBuffers:
+    """Outputs and workspace of the layer for a few tokens (at most 256)."""
+
+    def __init__(self, d: Dims, device="cuda"):
+        self.d = d
+        self.ws = torch.empty(max(moe_decode_workspace_bytes(d), 256), dtype=torch.uint8, device=device)
+        self.topk_idx = torch.empty(d.T, d.K, dtype=torch.int32, device=device)
+        self.topk_w = torch.empty(d.T, d.K, dtype=torch.float32, device=device)
+        self.out = torch.empty(d.T, d.H, dtype=d.torch_dtype, device=device)
+
+
+def decode(b: DecodeBuffers, p: dict, stream=None):
+    """The whole layer for a few tokens, logits to out.  p holds the device
+    inputs as for forward(); its weights are plain matrices or packed ones
+    (quantize_weights).  p["n_tokens"], if there, is the device int32 count of
+    the rows in use: the rows behind it are neither read nor written."""
+    call = moe_decode_mx if p["w1"].dtype == torch.uint8 else moe_decode
+    call(b.d, p["logits"], p["x"], p["w1"], p["w3"], p["w2"], p.get("ws1"), p.get("ws3"), p.get("ws2"),
+         p.get("n_tokens"), b.topk_idx, b.topk_w, b.out, b.ws, stream)
+
+
+def quantize_weights(p: dict, stream=None) -> dict:
+    """A copy of p with its weight matrices packed to 4 bits (moe_mx_quantize)."""
+    q = dict(p)
+    for name in ("w1", "w3", "w2", "ws1", "ws3", "ws2"):
+        w = p.get(name)
+        if w is not None:
+            G, K, N = w.shape
+            q[name] = torch.empty(moe_mx_bytes(G, K, N), dtype=torch.uint8, device=w.device)
+            moe_mx_quantize(G, K, N, w, q[name], stream)
+    return q

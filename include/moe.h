@@ -357,6 +357,63 @@ int moe_dispatch_bwd(const moe_dims* d, const void* dx_rows, const int32_t* slot
 int moe_route_bwd(const moe_dims* d, const float* dtopk_w, const float* topk_w,
                   const int32_t* topk_idx, float* dlogits, void* stream);
 
+/* ----------------------------------------------- a few tokens, 4-bit weights */
+
+/* The whole layer for a few tokens (generation), logits to out, in one call:
+ * moe_route's top-k and weights, the experts' SwiGLU FFN for the rows each
+ * token picked, the shared experts, and moe_combine's sum.  It reads the
+ * weights of the experts that have a token, once each, and nothing of the
+ * others.  T <= 256, H and I <= 2^20 (else MOE_EUNSUPPORTED); larger batches
+ * go through the calls above.
+ *  logits [T, E] f32, x [T, H], weights as for moe_expert_ffn (ws1, ws3, ws2
+ *           NULL if n_shared = 0) in
+ *  n_tokens device int32[1] in, or NULL: the number of rows in use, for batches
+ *           padded to a fixed T (a captured graph); values outside [0, T] count
+ *           as the nearest of the two.  Rows behind it are not read, and their
+ *           topk_idx, topk_w and out stay as they were.
+ *  topk_idx [T, K] i32, topk_w [T, K] f32 out: the bits moe_route gives
+ *  out [T, H] out.  Float32 all the way, one rounding at the end: h and y are
+ *           not rounded to dtype in between as the separate calls do (h enters
+ *           the second product as two bf16 parts, 16 bits of it).
+ *  ws: device workspace of at least moe_decode_workspace_bytes(d) bytes, 256-
+ *           byte aligned, in any state; it may be shared by calls that are
+ *           ordered on one stream, by none that overlap.
+ * No output depends on the other rows of the batch or on T, but by the k
+ * slices of the down projection, which the library chooses from the dims. */
+size_t moe_decode_workspace_bytes(const moe_dims* d);
+int moe_decode(const moe_dims* d, const float* logits, const void* x, const void* w1, const void* w3,
+               const void* w2, const void* ws1, const void* ws3, const void* ws2,
+               const int32_t* n_tokens, int32_t* topk_idx, float* topk_w, void* out, void* ws,
+               size_t ws_bytes, void* stream);
+
+/* moe_decode on 4-bit weights: every weight pointer is a packed matrix set (see
+ * moe_mx_quantize; w1, w3: G = E, K = H, N = I; w2: G = E, K = I, N = H; the
+ * shared ones with G = n_shared).  x, out and the sums as above (dtype is that
+ * of x and out); the products use the codes' exact values.  H and I must be
+ * multiples of 32. */
+int moe_decode_mx(const moe_dims* d, const float* logits, const void* x, const void* w1, const void* w3,
+                  const void* w2, const void* ws1, const void* ws3, const void* ws2,
+                  const int32_t* n_tokens, int32_t* topk_idx, float* topk_w, void* out, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* Packed weight matrices: MXFP4 (OCP Microscaling), E2M1 codes with one E8M0
+ * scale for 32 weights that follow each other along the reduction dim K.
+ * G matrices [K, N] take moe_mx_bytes(G, K, N) = G*K*N*17/32 bytes: first the
+ * codes [G, K/32, N, 16] (byte j holds weight 2j of the 32 in its low half and
+ * weight 2j+1 in its high half), then the scales [G, K/32, N]; scale byte b
+ * stands for 2^(b-127), 1 <= b <= 254.  K must be a multiple of 32, N of 8.
+ * Codes quantised elsewhere can be laid out like this and used as well.
+ *  quantize:   w [G, K, N] of `dtype` in (finite), mx out.  The scale is
+ *              2^(floor(log2 max|w|) - 2), at least 2^-126; a code is the
+ *              nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 times it (ties to the even
+ *              code, magnitudes above 6 to 6).
+ *  dequantize: mx in, w [G, K, N] of `dtype` out: code * scale, exact (for the
+ *              calls that take plain matrices, such as a long prompt's).
+ * moe_mx_bytes returns 0 for sizes outside the rules above. */
+size_t moe_mx_bytes(int G, int K, int N);
+int moe_mx_quantize(int G, int K, int N, int dtype, const void* w, void* mx, void* stream);
+int moe_mx_dequantize(int G, int K, int N, int dtype, const void* mx, void* w, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
