@@ -183,6 +183,9 @@ def moe_workspace_bytes(d: Dims) -> int:
 def _ptr(t, name, dtype=None, numel=None):
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype)
+            and (numel is None or t.numel() >= numel)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor or None")
     if t.device.type != "cuda":
@@ -196,18 +199,9 @@ def _ptr(t, name, dtype=None, numel=None):
     return t.data_ptr()
 
 
-def _one_device(stream, **tensors):
-    """Refuse tensors of different devices, or of another one than the work runs on: a kernel
-    would read memory that its device may not reach."""
-    device = stream.device if isinstance(stream, torch.cuda.Stream) else torch.device("cuda", torch.cuda.current_device())
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-
-
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the current stream's handle without a Stream object around it (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -445,31 +439,41 @@ def moe_decode_workspace_bytes(d: Dims) -> int:
     return int(load().moe_decode_workspace_bytes(ctypes.byref(d)))
 
 
-def _decode(name, d, dt, numels, logits, x, weights, n_tokens, topk_idx, topk_w, out, ws, stream):
-    T, K = d.T, d.K
-    wp, wn = _ws(ws)
-    args = [_ptr(logits, "logits", torch.float32, T * d.E), _ptr(x, "x", d.torch_dtype, T * d.H),
-            *(_ptr(t, w, dt, n) for (w, t), n in zip(weights.items(), numels)),
-            _ptr(n_tokens, "n_tokens", torch.int32, 1), _ptr(topk_idx, "topk_idx", torch.int32, T * K),
-            _ptr(topk_w, "topk_w", torch.float32, T * K), _ptr(out, "out", d.torch_dtype, T * d.H), wp, wn]
-    _one_device(stream, logits=logits, x=x, **weights, n_tokens=n_tokens, topk_idx=topk_idx, topk_w=topk_w,
-                out=out, ws=ws)
-    _call(name, ctypes.byref(d), *args, _stream(stream))
+def _launch(name, stream, head, tensors, tail):
+    """The call with the tensors' pointers between `head` and `tail`; tensors: (tensor, name,
+    dtype, elements).  Tensors of another device than the one the work runs on are refused: a
+    kernel would read memory that its device may not reach."""
+    index = stream.device_index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device()
+    args = [_ptr(*t) for t in tensors]
+    for t, arg_name, _, _ in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{arg_name} is on {t.device}, the call runs on cuda:{index}")
+    _call(name, *head, *args, *tail, _stream(stream))
+
+
+def _decode(name, d, dt, n, ns, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws, stream):
+    T, H, K, act = d.T, d.H, d.K, d.torch_dtype
+    i32, f32 = torch.int32, torch.float32
+    _launch(name, stream, (ctypes.byref(d),),
+            ((logits, "logits", f32, T * d.E), (x, "x", act, T * H), (w1, "w1", dt, n), (w3, "w3", dt, n),
+             (w2, "w2", dt, n), (ws1, "ws1", dt, ns), (ws3, "ws3", dt, ns), (ws2, "ws2", dt, ns),
+             (n_tokens, "n_tokens", i32, 1), (topk_idx, "topk_idx", i32, T * K), (topk_w, "topk_w", f32, T * K),
+             (out, "out", act, T * H), (ws, "ws", torch.uint8, None)), (0 if ws is None else ws.numel(),))
 
 
 def moe_decode(d: Dims, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws,
                stream=None):
     n, ns = d.E * d.H * d.I, d.n_shared * d.H * d.I
-    _decode("moe_decode", d, d.torch_dtype, (n, n, n, ns, ns, ns), logits, x,
-            dict(w1=w1, w3=w3, w2=w2, ws1=ws1, ws3=ws3, ws2=ws2), n_tokens, topk_idx, topk_w, out, ws, stream)
+    _decode("moe_decode", d, d.torch_dtype, n, ns, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx,
+            topk_w, out, ws, stream)
 
 
 def moe_decode_mx(d: Dims, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws,
                   stream=None):
     """moe_decode on packed weights: uint8 tensors of moe_mx_bytes, as moe_mx_quantize writes them."""
     n, ns = _mx_numel(d.E, d.H, d.I), _mx_numel(d.n_shared, d.H, d.I)
-    _decode("moe_decode_mx", d, torch.uint8, (n, n, n, ns, ns, ns), logits, x,
-            dict(w1=w1, w3=w3, w2=w2, ws1=ws1, ws3=ws3, ws2=ws2), n_tokens, topk_idx, topk_w, out, ws, stream)
+    _decode("moe_decode_mx", d, torch.uint8, n, ns, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx,
+            topk_w, out, ws, stream)
 
 
 def _mx_numel(G, K, N):
@@ -491,12 +495,10 @@ def _mx_dtype(w):
 
 
 def moe_mx_quantize(G: int, K: int, N: int, w, mx, stream=None):
-    code, wp, mp = _mx_dtype(w), _ptr(w, "w", None, G * K * N), _ptr(mx, "mx", torch.uint8, _mx_numel(G, K, N))
-    _one_device(stream, w=w, mx=mx)
-    _call("moe_mx_quantize", G, K, N, code, wp, mp, _stream(stream))
+    _launch("moe_mx_quantize", stream, (G, K, N, _mx_dtype(w)),
+            ((w, "w", None, G * K * N), (mx, "mx", torch.uint8, _mx_numel(G, K, N))), ())
 
 
 def moe_mx_dequantize(G: int, K: int, N: int, mx, w, stream=None):
-    code, wp, mp = _mx_dtype(w), _ptr(w, "w", None, G * K * N), _ptr(mx, "mx", torch.uint8, _mx_numel(G, K, N))
-    _one_device(stream, w=w, mx=mx)
-    _call("moe_mx_dequantize", G, K, N, code, mp, wp, _stream(stream))
+    _launch("moe_mx_dequantize", stream, (G, K, N, _mx_dtype(w)),
+            ((mx, "mx", torch.uint8, _mx_numel(G, K, N)), (w, "w", None, G * K * N)), ())

@@ -18,9 +18,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 8;               // waves of a product block, splitting its k steps
-constexpr int kThreads = kWaves * kWave;
+constexpr int kMaxWaves = 8;            // waves of a product block: 8, or 4 side by side
+constexpr int kRedRows = 8;             // rows whose sums go through LDS at once
 constexpr int kRouteThreads = 1024;
+constexpr int kHeadTokens = 32;   // routing inside the first product's blocks up to here
+constexpr int kTailTokens = 4;    // the output's sum inside the second product up to here
+constexpr double kWideBlocks = 224;
 
 enum Fmt : int { kFmtBf16 = 0, kFmtF32 = 1, kFmtMxBf16 = 2, kFmtMxF32 = 3 };
 constexpr bool fmt_mx(int f) { return f >= kFmtMxBf16; }
@@ -44,123 +47,266 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// Wave maximum by DPP row shifts and row broadcasts (lane 63 ends with it).
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#define MOE_DPP_MAX(ctrl)                                                                    \
-  {                                                                                          \
-    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true); \
-    v = o > v ? o : v;                                                                       \
+// Wave maxima by DPP row shifts and row broadcasts (lane 63 ends with them).
+template <int N>
+__device__ __forceinline__ void wave_max_u32(uint32_t (&v)[N]) {
+#define MOE_DPP_MAX(ctrl)                                                                           \
+  _Pragma("unroll") for (int i = 0; i < N; ++i) {                                                   \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[i], ctrl, 0xF, 0xF, true);   \
+    v[i] = o > v[i] ? o : v[i];                                                                     \
   }
   MOE_DPP_MAX(0x111) MOE_DPP_MAX(0x112) MOE_DPP_MAX(0x114) MOE_DPP_MAX(0x118)   // row_shr 1, 2, 4, 8
   MOE_DPP_MAX(0x142) MOE_DPP_MAX(0x143)                                         // row_bcast 15, 31
 #undef MOE_DPP_MAX
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = (uint32_t)__builtin_amdgcn_readlane((int)v[i], 63);
 }
 
-// One wave's top-k of a token: lane l holds the logits of experts l, l + 64,
-// ... (EC chunks).  Writes the K picks and their weights; the same keys, order
-// and weight arithmetic as moe_route, hence the same bits.
-template <int EC>
-__device__ __forceinline__ void route_token(const float* __restrict__ row, int E, int K, int lane,
-                                            int32_t* __restrict__ idx, float* __restrict__ w) {
-  uint32_t key[EC];
+// One wave's top-k of TOK tokens t, t + dt, ... below T: lane l holds the
+// logits of experts l, l + 64, ... (EC chunks).  Writes the K picks and their
+// weights of the tokens below n; the same keys, order and weight arithmetic as
+// moe_route, hence the same bits.  A pick is a chain of dependent lane
+// operations, so several tokens at once hide each other's latency; the logits
+// are asked for before n is known.
+template <int EC, int TOK>
+__device__ __forceinline__ void route_tokens(const float* __restrict__ logits, int t, int dt, int T, int n, int E,
+                                             int K, int lane, int32_t* __restrict__ idx, float* __restrict__ w) {
+  uint32_t key[TOK][EC], first[TOK];
+  float pl[TOK][EC];
+  int pe[TOK][EC];
 #pragma unroll
-  for (int c = 0; c < EC; ++c) key[c] = lane + kWave * c < E ? logit_key(row[lane + kWave * c]) : 0u;
-  float l0 = 0.f, zsum = 0.f, pl[EC];
-  int pe[EC];
-#pragma unroll
-  for (int c = 0; c < EC; ++c) {
-    pl[c] = 0.f;
-    pe[c] = 0;
-  }
-  for (int k = 0; k < K; ++k) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int c = 1; c < EC; ++c) best = key[c] > best ? key[c] : best;
-    best = wave_max_u32(best);
-    int e = -1;
-#pragma unroll
-    for (int c = 0; c < EC; ++c) {   // the lowest expert that holds the maximum
-      const uint64_t m = __ballot(key[c] == best);
-      if (e < 0 && m) e = kWave * c + __builtin_ctzll(m);
-    }
-    const float l = key_logit(best);
-    if (k == 0) l0 = l;
-    zsum += expf(l - l0);
+  for (int i = 0; i < TOK; ++i) {
+    first[i] = 0u;
 #pragma unroll
     for (int c = 0; c < EC; ++c) {
-      if (lane + kWave * c == e) key[c] = 0u;
-      if (lane + kWave * c == k) {
-        pl[c] = l;
-        pe[c] = e;
+      pl[i][c] = 0.f;
+      pe[i][c] = 0;
+      key[i][c] = t + i * dt < T && lane + kWave * c < E
+                      ? logit_key(logits[(int64_t)(t + i * dt) * E + lane + kWave * c]) : 0u;
+    }
+  }
+  for (int k = 0; k < K; ++k) {
+    uint32_t best[TOK];
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+      best[i] = key[i][0];
+#pragma unroll
+      for (int c = 1; c < EC; ++c) best[i] = key[i][c] > best[i] ? key[i][c] : best[i];
+    }
+    wave_max_u32<TOK>(best);
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+      int e = -1;
+#pragma unroll
+      for (int c = 0; c < EC; ++c) {   // the lowest expert that holds the maximum
+        const uint64_t m = __ballot(key[i][c] == best[i]);
+        if (e < 0 && m) e = kWave * c + __builtin_ctzll(m);
+      }
+      if (k == 0) first[i] = best[i];
+#pragma unroll
+      for (int c = 0; c < EC; ++c) {
+        if (lane + kWave * c == e) key[i][c] = 0u;
+        if (lane + kWave * c == k) {
+          pl[i][c] = key_logit(best[i]);
+          pe[i][c] = e;
+        }
       }
     }
   }
 #pragma unroll
-  for (int c = 0; c < EC; ++c)
-    if (lane + kWave * c < K) {
-      idx[lane + kWave * c] = pe[c];
-      w[lane + kWave * c] = expf(pl[c] - l0) / zsum;
+  for (int i = 0; i < TOK; ++i) {
+    float ex[EC], sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < EC; ++c) ex[c] = expf(pl[i][c] - key_logit(first[i]));
+    for (int k = 0; k < K; ++k) {   // in the order of the picks
+      float v = lane_float(ex[0], k & (kWave - 1));
+#pragma unroll
+      for (int c = 1; c < EC; ++c)
+        if (k >= kWave * c) v = lane_float(ex[c], k & (kWave - 1));
+      sum += v;
     }
+#pragma unroll
+    for (int c = 0; c < EC; ++c)
+      if (t + i * dt < n && lane + kWave * c < K) {
+        const int64_t at = (int64_t)(t + i * dt) * K + lane + kWave * c;
+        idx[at] = pe[i][c];
+        w[at] = ex[c] / sum;
+      }
+  }
 }
 
-// One block routes all tokens and lists the work: the rows of every expert
-// that has some (expert-contiguous), cut into entries of at most row_tile
-// rows.  A row's place among its expert's rows is taken from an LDS counter;
-// no result depends on it (a row's sums do not mix with its neighbours').
-template <int EC>
+// All tokens, by the block's `waves` waves.
+__device__ __forceinline__ void route_all(const DecodeArgs& a, int n, int wave, int waves, int lane, int32_t* idx,
+                                          float* w) {
+  if (a.E > kWave) {
+    for (int t = wave; t < a.T; t += waves)
+      route_tokens<kMaxExperts / kWave, 1>(a.logits, t, waves, a.T, n, a.E, a.K, lane, idx, w);
+  } else if (a.T <= waves) {
+    if (wave < a.T) route_tokens<1, 1>(a.logits, wave, waves, a.T, n, a.E, a.K, lane, idx, w);
+  } else {
+    for (int t = wave; t < a.T; t += 4 * waves)
+      route_tokens<1, 4>(a.logits, t, waves, a.T, n, a.E, a.K, lane, idx, w);
+  }
+}
+
+__device__ __forceinline__ int tokens_in_use(const DecodeArgs& a) {
+  return a.n_tokens ? min(max(*a.n_tokens, 0), a.T) : a.T;
+}
+
+// The work is a list of entries, each some rows (at most row_tile) of one
+// expert: entries[i] = {group, rows}, their row ids at lists[i * row_tile].  A
+// row id is the pair t K + k, or R + s T + t for shared expert s.  The order
+// of an entry's rows comes from a counter; no result depends on it (a row's
+// sums do not mix with its neighbours').
+//
+// One block routes all tokens and writes the list (batches beyond what each
+// product block routes for itself, see decode_plan).
 __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(DecodeArgs a, int row_tile) {
-  __shared__ int count[kMaxExperts], start[kMaxExperts], first[kMaxExperts];
+  __shared__ int count[kMaxExperts], first[kMaxExperts], fill[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int E = a.E, K = a.K;
-  int n = a.T;
-  if (a.n_tokens) n = min(max(*a.n_tokens, 0), a.T);
-  if (tid < kMaxExperts) count[tid] = 0;
-  for (int t = wave; t < n; t += kRouteThreads / kWave)
-    route_token<EC>(a.logits + (int64_t)t * E, E, K, lane, a.topk_idx + (int64_t)t * K,
-                    a.topk_w + (int64_t)t * K);
+  const int E = a.E, K = a.K, n = tokens_in_use(a);
+  if (tid < kMaxExperts) count[tid] = fill[tid] = 0;
+  route_all(a, n, wave, kRouteThreads / kWave, lane, a.topk_idx, a.topk_w);
   __syncthreads();
   const int pairs = n * K;
-  for (int p = tid; p < pairs; p += kRouteThreads) a.slot[p] = atomicAdd(&count[a.topk_idx[p]], 1);
+  for (int p = tid; p < pairs; p += kRouteThreads) atomicAdd(&count[a.topk_idx[p]], 1);
   __syncthreads();
-  // prefix sums over the experts: rows, and entries
-  if (tid < kMaxExperts) {
-    start[tid] = count[tid];
-    first[tid] = (count[tid] + row_tile - 1) / row_tile;
-  }
+  if (tid < kMaxExperts) first[tid] = (count[tid] + row_tile - 1) / row_tile;
   __syncthreads();
-  for (int o = 1; o < kMaxExperts; o <<= 1) {
-    int s = 0, f = 0;
-    if (tid < kMaxExperts && tid >= o) {
-      s = start[tid - o];
-      f = first[tid - o];
-    }
+  for (int o = 1; o < kMaxExperts; o <<= 1) {   // entries up to each expert
+    int f = 0;
+    if (tid < kMaxExperts && tid >= o) f = first[tid - o];
     __syncthreads();
-    if (tid < kMaxExperts) {
-      start[tid] += s;
-      first[tid] += f;
-    }
+    if (tid < kMaxExperts) first[tid] += f;
     __syncthreads();
-  }
-  if (tid < kMaxExperts) {   // exclusive from here on: start[e] - count[e]
-    const int c = count[tid], s0 = start[tid] - c, m = (c + row_tile - 1) / row_tile, f0 = first[tid] - m;
-    for (int i = 0; i < m; ++i)
-      a.entries[f0 + i] = make_int4(tid, s0 + i * row_tile, min(row_tile, c - i * row_tile), 0);
-    start[tid] = s0;
   }
   const int routed = first[kMaxExperts - 1];
+  __syncthreads();
+  if (tid < kMaxExperts) {
+    const int c = count[tid], m = (c + row_tile - 1) / row_tile, f0 = first[tid] - m;
+    for (int i = 0; i < m; ++i) a.entries[f0 + i] = make_int2(tid, min(row_tile, c - i * row_tile));
+    first[tid] = f0;
+  }
   const int per = (n + row_tile - 1) / row_tile;   // entries of one shared expert
   for (int i = tid; i < a.Ns * per; i += kRouteThreads) {
     const int s = i / per, r = (i - s * per) * row_tile;
-    a.entries[routed + i] = make_int4(a.E + s, a.R + s * a.T + r, min(row_tile, n - r), 0);
+    a.entries[routed + i] = make_int2(E + s, min(row_tile, n - r));
+  }
+  for (int i = tid; i < a.Ns * n; i += kRouteThreads) {
+    const int s = i / n, t = i - s * n;
+    a.lists[(int64_t)(routed + s * per + t / row_tile) * row_tile + t % row_tile] = a.R + s * a.T + t;
   }
   if (tid == 0) *a.n_entries = routed + a.Ns * per;
   __syncthreads();
   for (int p = tid; p < pairs; p += kRouteThreads) {
-    const int row = start[a.topk_idx[p]] + a.slot[p];
-    a.slot[p] = row;
-    a.row_token[row] = p / K;
+    const int e = a.topk_idx[p], at = atomicAdd(&fill[e], 1);
+    a.lists[(int64_t)(first[e] + at / row_tile) * row_tile + at % row_tile] = p;
   }
+}
+
+// The same list, entry by entry, by every block of the first product for
+// itself (at most one pair a thread).  It costs a block the latency of one
+// load and of its picks; a launch of its own costs more, on the host too.
+// Writes what the second product and the caller need: the entry and its rows
+// by the blocks of column tile 0, the picks by the very first block.
+template <int NW>
+struct BlockRoute {
+  int32_t idx[NW * kWave];
+  float w[NW * kWave];
+  int32_t list[32];
+  int32_t count[kMaxExperts];
+  int32_t below[NW];
+};
+template <int NW>
+__device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute<NW>& r, int entry, bool write_entry,
+                                            bool write_picks, int row_tile, int tid, int& group, int& rows) {
+  const int lane = tid & (kWave - 1), wave = tid / kWave;
+  const int E = a.E, K = a.K, n = tokens_in_use(a), pairs = n * K;
+  for (int e = tid; e < kMaxExperts; e += NW * kWave) r.count[e] = 0;
+  route_all(a, n, wave, NW, lane, r.idx, r.w);
+  __syncthreads();
+  if (a.T == 1) {   // each pick is an entry of its own, and so is each shared expert
+    if (write_picks) {
+      if (tid < pairs) {
+        a.topk_idx[tid] = r.idx[tid];
+        a.topk_w[tid] = r.w[tid];
+      }
+      if (tid == 0) *a.n_entries = n * (K + a.Ns);
+    }
+    if (entry >= n * (K + a.Ns)) return false;
+    const bool pick = entry < K;
+    group = pick ? r.idx[entry] : E + entry - K;
+    rows = 1;
+    __syncthreads();
+    if (tid == 0) r.list[0] = pick ? entry : a.R + entry - K;
+    __syncthreads();
+    if (write_entry && tid == 0) {
+      a.entries[entry] = make_int2(group, 1);
+      a.lists[entry * row_tile] = r.list[0];
+    }
+    return true;
+  }
+  const int mine = tid < pairs ? r.idx[tid] : -1;
+  if (tid < pairs) atomicAdd(&r.count[mine], 1);
+  __syncthreads();
+  // the expert that holds this entry, and which of its entries it is
+  int seen = 0, e = -1, part = 0;
+  for (int c = 0; c < E; c += kWave) {
+    const int cnt = lane + c < E ? r.count[lane + c] : 0;
+    const int m = (cnt + row_tile - 1) / row_tile;
+    int before, in;   // entries of the chunk's lower experts, and of all of them
+    if (a.T <= row_tile) {
+      const uint64_t mask = __ballot(m != 0);
+      before = __popcll(mask & ((1ull << lane) - 1));
+      in = __popcll(mask);
+    } else {
+      before = m;
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1) {
+        const int v = __shfl_up(before, o, kWave);
+        if (lane >= o) before += v;
+      }
+      in = __builtin_amdgcn_readlane(before, kWave - 1);
+      before -= m;
+    }
+    const int want = entry - seen;
+    if (e < 0 && want < in) {
+      const int l = __builtin_ctzll(__ballot(want >= before && want < before + m));
+      e = c + l;
+      part = want - __builtin_amdgcn_readlane(before, l);
+      rows = min(row_tile, __builtin_amdgcn_readlane(cnt, l) - part * row_tile);
+    }
+    seen += in;
+  }
+  const int per = (n + row_tile - 1) / row_tile, total = seen + a.Ns * per;
+  if (write_picks) {
+    if (tid < pairs) {
+      a.topk_idx[tid] = mine;
+      a.topk_w[tid] = r.w[tid];
+    }
+    if (tid == 0) *a.n_entries = total;
+  }
+  if (entry >= total) return false;
+  if (e >= 0) {   // the entry's rows: the expert's pairs in order, from part * row_tile on
+    group = e;
+    const uint64_t mask = __ballot(mine == e);
+    if (lane == 0) r.below[wave] = __popcll(mask);
+    __syncthreads();
+    int rank = __popcll(mask & ((1ull << lane) - 1)) - part * row_tile;
+    for (int v = 0; v < wave; ++v) rank += r.below[v];
+    if (mine == e && rank >= 0 && rank < row_tile) r.list[rank] = tid;
+  } else {
+    const int s = (entry - seen) / per, t0 = (entry - seen - s * per) * row_tile;
+    group = E + s;
+    rows = min(row_tile, n - t0);
+    if (tid < rows) r.list[tid] = a.R + s * a.T + t0 + tid;
+  }
+  __syncthreads();
+  if (write_entry) {
+    if (tid == 0) a.entries[entry] = make_int2(group, rows);
+    if (tid < rows) a.lists[entry * row_tile + tid] = r.list[tid];
+  }
+  return true;
 }
 
 // ----------------------------------------------------------------- products
@@ -207,14 +353,14 @@ struct Stage {
   u32x4 act[NT][act_vecs(F, UP)];
 };
 
-// A lane's place: the matrix and column(s) it reads, and its rows.
+// A lane's place: its column(s) in row 0 of the matrix it reads, and its rows.
 template <int F, bool UP, int NT>
 struct Lane {
-  const char* w[fmt_mx(F) ? 2 : 1];        // mx: W1 and W3 (up) or W2 twice; else the lane's matrix
-  const char* sc[fmt_mx(F) ? 2 : 1];       // scales
-  bool col_ok[fmt_mx(F) ? fmt_groups(F) : 1];
-  int32_t col[fmt_mx(F) ? fmt_groups(F) : 1];
-  const char* act[NT];                     // null: no such row
+  const char* w[fmt_mx(F) && UP ? 2 : 1];   // 4 bit: in W1 and W3 (up) or in W2
+  const char* sc[fmt_mx(F) && UP ? 2 : 1];  // scales
+  int groups;                               // 4 bit: column groups inside the matrix (whole ones: N % 32 == 0)
+  bool col_ok;                              // else: the lane's columns are inside
+  const char* act[NT];                      // null: no such row
 };
 
 template <int F, bool UP, int NT>
@@ -222,15 +368,17 @@ __device__ __forceinline__ void load_stage(Stage<F, UP, NT>& s, const Lane<F, UP
                                            int Kd, int N, int64_t plane) {
   const u32x4 zero = {0, 0, 0, 0};
   if constexpr (fmt_mx(F)) {
-    const int kb = 4 * step + q, KB = Kd / kMxGroup;
+    const int kb = 4 * step + q;
+    const bool ok = kb < Kd / kMxGroup;
+    const int64_t at = (int64_t)kb * N;
 #pragma unroll
     for (int j = 0; j < fmt_groups(F); ++j) {
       s.w[j] = zero;
       s.s[j] = 127;
-      if (kb < KB && L.col_ok[j]) {
-        const int64_t at = (int64_t)kb * N + L.col[j];
-        s.w[j] = ld16_stream(L.w[UP ? j & 1 : 0] + at * kMxCodeBytes);
-        s.s[j] = static_cast<const uint8_t*>(static_cast<const void*>(L.sc[UP ? j & 1 : 0]))[at];
+      const int jj = UP ? j >> 1 : j;
+      if (ok && jj < L.groups) {
+        s.w[j] = ld16_stream(L.w[UP ? j & 1 : 0] + at * kMxCodeBytes + jj * 16 * kMxCodeBytes);
+        s.s[j] = static_cast<const uint8_t*>(static_cast<const void*>(L.sc[UP ? j & 1 : 0]))[at + jj * 16];
       }
     }
 #pragma unroll
@@ -238,7 +386,7 @@ __device__ __forceinline__ void load_stage(Stage<F, UP, NT>& s, const Lane<F, UP
       constexpr int V = act_vecs(F, UP);
 #pragma unroll
       for (int v = 0; v < V; ++v) s.act[nt][v] = zero;
-      if (L.act[nt] && kb < KB) {
+      if (L.act[nt] && ok) {
         if constexpr (F == kFmtMxF32) {
           const char* p = L.act[nt] + (int64_t)kb * kMxGroup * 4;
 #pragma unroll
@@ -258,7 +406,7 @@ __device__ __forceinline__ void load_stage(Stage<F, UP, NT>& s, const Lane<F, UP
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       s.w[i] = zero;
-      if (ok && L.col_ok[0]) s.w[i] = ld16_stream(p + (int64_t)i * N * B);
+      if (ok && L.col_ok) s.w[i] = ld16_stream(p + (int64_t)i * N * B);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -359,61 +507,122 @@ __device__ __forceinline__ int tile_col(int j, int m, bool& second) {
 template <int F>
 constexpr int red_stride() { return 16 * fmt_groups(F) + 4; }
 
-// One block: one entry (up to 16 NT rows of one expert) x one column tile x
-// one k slice, its k steps spread over the 8 waves and the waves' sums added
-// in wave order through LDS.
-template <int F, bool UP, int NT>
-__global__ __launch_bounds__(kThreads) void decode_ffn_kernel(DecodeArgs a, int tiles, int slice_steps) {
-  constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, COLS = UP ? 8 * G : 16 * G;
-  __shared__ float red[kWaves * 16 * red_stride<F>()];
+// out[t] of one 4-column vector: sum over the pairs k in order, then the
+// shared rows, each over its k slices; item i = (pair, slice).
+__device__ __forceinline__ int64_t item_row(const DecodeArgs& a, int t, int k) {
+  return k < a.K ? (int64_t)t * a.K + k : (int64_t)a.R + (int64_t)(k - a.K) * a.T + t;
+}
+constexpr int kItemBatch = 8;   // loads in flight per thread
+__device__ __forceinline__ f32x4 combine_items(const DecodeArgs& a, int slices, int t, int c, int first, int stride) {
+  const int64_t RA = (int64_t)a.R + (int64_t)a.Ns * a.T;
+  const int items = (a.K + a.Ns) * slices;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = first; i0 < items; i0 += stride * kItemBatch) {
+    f32x4 v[kItemBatch];
+    float w[kItemBatch];
+#pragma unroll
+    for (int u = 0; u < kItemBatch; ++u) {
+      const int i = i0 + u * stride;
+      v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      w[u] = 0.f;
+      if (i < items) {
+        const int k = i / slices, s = i - k * slices;
+        v[u] = *reinterpret_cast<const f32x4*>(a.y + ((int64_t)s * RA + item_row(a, t, k)) * a.H + c);
+        w[u] = k < a.K ? a.topk_w[(int64_t)t * a.K + k] : 1.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kItemBatch; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = fmaf(w[u], v[u][j], sum[j]);
+  }
+  return sum;
+}
+template <bool BF16>
+__device__ __forceinline__ void store_out(const DecodeArgs& a, int t, int c, const f32x4& sum) {
+  if constexpr (!BF16) {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + (int64_t)t * a.H + c) = sum;
+  } else {
+    u32x2 v;
+    v[0] = pack_bf16x2(sum[0], sum[1]);
+    v[1] = pack_bf16x2(sum[2], sum[3]);
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (int64_t)t * a.H + c) = v;
+  }
+}
+
+// One block: one entry (up to 16 NT rows of one expert) x one tile of columns x
+// one k slice.  Its NW waves are CW column tiles next to each other x NW / CW
+// shares of the k steps, whose sums are added in wave order through LDS.
+//
+// HEAD: the first product's blocks route for themselves (block_route).
+// TAIL: the second's add up the output of a column tile when they are its
+// last: a block stores its sums coherently, waits until they are written, and
+// counts itself; whoever counts last reads them all.  Nobody waits for
+// anybody.  The first product's first block clears the counters.
+template <int F, bool UP, int NT, int NW, int CW, bool FUSED>
+__global__ __launch_bounds__(NW * kWave, NT == 1 && (!fmt_mx(F) || (UP && F == kFmtMxBf16)) ? 4 : 2) void decode_ffn_kernel(DecodeArgs a, int tiles, int slices, int slice_steps) {
+  constexpr bool HEAD = UP && FUSED, TAIL = !UP && FUSED;
+  constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, KW = NW / CW, kThreads = NW * kWave;
+  constexpr int WCOLS = UP ? 8 * G : 16 * G, COLS = WCOLS * CW;   // columns of a wave, of the block
+  __shared__ __align__(16) float red[NW * kRedRows * red_stride<F>()];
+  __shared__ int last;
+  static_assert(sizeof(BlockRoute<NW>) <= sizeof(red) && kThreads * 16 <= sizeof(red), "other uses of the sums' LDS");
   const int entry = blockIdx.y;
-  if (entry >= *a.n_entries) return;
-  const int4 en = a.entries[entry];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int m = lane & 15, q = lane >> 4;
   const int tile = blockIdx.x % tiles, slice = blockIdx.x / tiles;
   const int Kd = UP ? a.H : a.I, N = UP ? a.I : a.H;
-  const bool shared = en.x >= a.E;
   const int64_t RA = (int64_t)a.R + (int64_t)a.Ns * a.T;
   const int64_t plane = RA * a.I * 2;   // bytes between h's two bf16 planes
+  int group, rows, ids[NT], n_entries = 0;   // ids: this lane's rows
+  if (UP && blockIdx.x == 0 && entry == 0)
+    for (int i = tid; i < a.n_done; i += kThreads) a.done[i * kDoneStride] = 0;
+  if constexpr (HEAD) {
+    BlockRoute<NW>& r = *reinterpret_cast<BlockRoute<NW>*>(red);
+    if (!block_route(a, r, entry, blockIdx.x == 0, blockIdx.x == 0 && entry == 0, 16 * NT, tid, group, rows)) return;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = 16 * nt + m < rows ? r.list[16 * nt + m] : 0;
+    __syncthreads();   // the list is read; its LDS becomes the sums'
+  } else {
+    n_entries = *a.n_entries;
+    const int2 en = a.entries[entry];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = a.lists[(int64_t)entry * (16 * NT) + 16 * nt + m];
+    if (entry >= n_entries) return;
+    group = en.x;
+    rows = en.y;
+  }
+  const bool shared = group >= a.E;
+  const int g = shared ? group - a.E : group;
+  const int col0 = tile * COLS + wave % CW * WCOLS;   // the wave's first column
 
   Lane<F, UP, NT> L;
   if constexpr (fmt_mx(F)) {
-    const int g = shared ? en.x - a.E : en.x, groups = shared ? a.Ns : a.E;
     const int64_t one = (int64_t)(Kd / kMxGroup) * N;   // groups of 32 of one matrix
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (UP ? 2 : 1); ++i) {
       const void* base = UP ? (i ? (shared ? a.ws3 : a.w3) : (shared ? a.ws1 : a.w1)) : (shared ? a.ws2 : a.w2);
-      L.w[i] = static_cast<const char*>(base) + g * one * kMxCodeBytes;
-      L.sc[i] = static_cast<const char*>(base) + groups * one * kMxCodeBytes + g * one;
+      L.w[i] = static_cast<const char*>(base) + (g * one + col0 + m) * kMxCodeBytes;
+      L.sc[i] = static_cast<const char*>(base) + (shared ? a.Ns : a.E) * one * kMxCodeBytes + g * one + col0 + m;
     }
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      bool second;
-      L.col[j] = tile * COLS + tile_col<F, UP>(j, m, second);
-      L.col_ok[j] = L.col[j] < N;
-    }
+    L.groups = (N - col0) / 16;
   } else {
     bool second;
-    const int col = tile * COLS + tile_col<F, UP>(0, m, second);
-    const int g = shared ? en.x - a.E : en.x;
+    const int col = col0 + tile_col<F, UP>(0, m, second);
     const void* base = UP ? (second ? (shared ? a.ws3 : a.w3) : (shared ? a.ws1 : a.w1)) : (shared ? a.ws2 : a.w2);
     L.w[0] = static_cast<const char*>(base) + ((int64_t)g * Kd * N + col) * B;
-    L.col[0] = col;
-    L.col_ok[0] = col < N;
+    L.col_ok = col < N;
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int n = 16 * nt + m;
     L.act[nt] = nullptr;
-    if (n < en.z) {
+    if (16 * nt + m < rows) {
       if constexpr (UP) {
-        const int t = shared ? en.y + n - a.R - (en.x - a.E) * a.T : a.row_token[en.y + n];
+        const int t = shared ? ids[nt] - a.R - g * a.T : ids[nt] / a.K;
         L.act[nt] = static_cast<const char*>(a.x) + (int64_t)t * a.H * B;
       } else {
-        L.act[nt] = static_cast<const char*>(a.h) + (int64_t)(en.y + n) * a.I * B;
+        L.act[nt] = static_cast<const char*>(a.h) + (int64_t)ids[nt] * a.I * B;
       }
-      // dense: a lane's k offset is added per step (8 q rows inside it)
     }
   }
 
@@ -426,38 +635,36 @@ __global__ __launch_bounds__(kThreads) void decode_ffn_kernel(DecodeArgs a, int 
   const int steps = (Kd + fmt_step(F) - 1) / fmt_step(F);
   const int begin = slice * slice_steps, end = min(steps, begin + slice_steps);
   Stage<F, UP, NT> s0, s1;
-  int k = begin + wave;
-  if (k < end) {
+  int k = begin + wave / CW;
+  if (k < end && col0 < N) {
     load_stage<F, UP, NT>(s0, L, k, q, Kd, N, plane);
     for (;;) {
-      const bool more1 = k + kWaves < end;
-      if (more1) load_stage<F, UP, NT>(s1, L, k + kWaves, q, Kd, N, plane);
+      const bool more1 = k + KW < end;
+      if (more1) load_stage<F, UP, NT>(s1, L, k + KW, q, Kd, N, plane);
       mma_stage<F, UP, NT>(s0, acc);
       if (!more1) break;
-      const bool more0 = k + 2 * kWaves < end;
-      if (more0) load_stage<F, UP, NT>(s0, L, k + 2 * kWaves, q, Kd, N, plane);
+      const bool more0 = k + 2 * KW < end;
+      if (more0) load_stage<F, UP, NT>(s0, L, k + 2 * KW, q, Kd, N, plane);
       mma_stage<F, UP, NT>(s1, acc);
       if (!more0) break;
-      k += 2 * kWaves;
+      k += 2 * KW;
     }
   }
 
   constexpr int RS = red_stride<F>();
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int rows = min(16, en.z - 16 * nt);
-    if (rows <= 0) break;
-    if (nt) __syncthreads();
-    if (m < rows) {
+  for (int r0 = 0; r0 < 16 * NT; r0 += kRedRows) {   // kRedRows rows at a time
+    const int nt = r0 / 16, n0 = r0 % 16, here = min(kRedRows, rows - r0);
+    if (here <= 0) break;
+    if (r0) __syncthreads();
+    if (m >= n0 && m < n0 + here) {
 #pragma unroll
       for (int j = 0; j < G; ++j)
-        *reinterpret_cast<f32x4*>(&red[(wave * 16 + m) * RS + 16 * j + 4 * q]) = acc[nt][j];
+        *reinterpret_cast<f32x4*>(&red[(wave * kRedRows + m - n0) * RS + 16 * j + 4 * q]) = acc[nt][j];
     }
     __syncthreads();
-    for (int o = tid; o < rows * COLS; o += kThreads) {
-      const int n = o / COLS, c = o - n * COLS;
-      if (tile * COLS + c >= N) continue;
-      const int64_t row = en.y + 16 * nt + n;
+    for (int o = tid; o < here * COLS; o += kThreads) {
+      const int n = o / COLS, bc = o - n * COLS, cw = bc / WCOLS, c = bc - cw * WCOLS;
       int at, at3 = 0;
       if constexpr (fmt_mx(F)) {
         at = UP ? 32 * (c >> 4) + (c & 15) : c;
@@ -466,13 +673,15 @@ __global__ __launch_bounds__(kThreads) void decode_ffn_kernel(DecodeArgs a, int 
         at = 16 * (c % G) + c / G;
         at3 = at + 8;
       }
+      const int64_t row = __shfl(ids[nt], n0 + n, 16);   // every group of 16 lanes holds the 16 ids
       float s = 0.f, s3 = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        s += red[(w * 16 + n) * RS + at];
-        if constexpr (UP) s3 += red[(w * 16 + n) * RS + at3];
+      for (int w = 0; w < KW; ++w) {
+        s += red[((w * CW + cw) * kRedRows + n) * RS + at];
+        if constexpr (UP) s3 += red[((w * CW + cw) * kRedRows + n) * RS + at3];
       }
-      const int64_t dst = row * N + tile * COLS + c;
+      if (tile * COLS + bc >= N) continue;
+      const int64_t dst = row * N + tile * COLS + bc;
       if constexpr (UP) {
         const float hv = silu_f(s) * s3;
         if constexpr (fmt_f32(F)) {
@@ -483,56 +692,87 @@ __global__ __launch_bounds__(kThreads) void decode_ffn_kernel(DecodeArgs a, int 
           hp[dst] = (uint16_t)hi;
           hp[RA * a.I + dst] = (uint16_t)f32_to_bf16(hv - bf16_to_f32(hi));
         }
+      } else if constexpr (TAIL) {
+        __hip_atomic_store(&a.y[(int64_t)slice * RA * N + dst], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       } else {
         a.y[(int64_t)slice * RA * N + dst] = s;
       }
     }
   }
+
+  if constexpr (TAIL) {
+    __builtin_amdgcn_s_waitcnt(0);   // this wave's sums are written
+    __syncthreads();
+    if (tid == 0)
+      last = __hip_atomic_fetch_add(&a.done[tile * kDoneStride], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+             n_entries * slices - 1;
+    __syncthreads();
+    if (!last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    // the threads = vectors of the tile x (tokens x parts of a token's items);
+    // the parts' sums are added in order
+    constexpr int VECS = COLS / 4, SLOTS = kThreads / VECS;
+    const int n = tokens_in_use(a), items = (a.K + a.Ns) * slices;
+    const int parts = max(1, min(SLOTS / a.T, items)), par = min(a.T, SLOTS);
+    const int vec = tid % VECS, slot = tid / VECS, c = tile * COLS + 4 * vec;
+    f32x4* part_sum = reinterpret_cast<f32x4*>(red);
+    for (int t0 = 0; t0 < n; t0 += par) {
+      const int t = t0 + slot / parts, part = slot % parts;
+      const bool ok = slot < par * parts && t < n && c < a.H;
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      if (ok) sum = combine_items(a, slices, t, c, part, parts);
+      if (parts > 1) {
+        __syncthreads();
+        part_sum[tid] = sum;
+        __syncthreads();
+        if (ok && part == 0) {
+          for (int i = 1; i < parts; ++i) sum += part_sum[tid + i * VECS];
+        }
+      }
+      if (ok && part == 0) store_out<!fmt_f32(F)>(a, t, c, sum);
+    }
+  }
 }
 
-// out[t] = sum_k g[t,k] (sum over slices of y[slot[t,k]]) + the shared rows',
-// in that order; one rounding.  4 columns a thread.
-template <typename S>
+template <bool BF16>
 __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int slices) {
   const int t = blockIdx.y;
-  if (a.n_tokens && t >= *a.n_tokens) return;
+  if (t >= tokens_in_use(a)) return;
   const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (c >= a.H) return;
-  const int64_t RA = (int64_t)a.R + (int64_t)a.Ns * a.T;
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < a.K + a.Ns; ++k) {
-    const int64_t row = k < a.K ? (int64_t)a.slot[(int64_t)t * a.K + k] : a.R + (int64_t)(k - a.K) * a.T + t;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < slices; ++s) v += *reinterpret_cast<const f32x4*>(a.y + ((int64_t)s * RA + row) * a.H + c);
-    const float w = k < a.K ? a.topk_w[(int64_t)t * a.K + k] : 1.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = fmaf(w, v[i], sum[i]);
-  }
-  S* out = static_cast<S*>(a.out) + (int64_t)t * a.H + c;
-  if constexpr (sizeof(S) == 4) {
-    *reinterpret_cast<f32x4*>(out) = sum;
-  } else {
-    u32x2 v;
-    v[0] = pack_bf16x2(sum[0], sum[1]);
-    v[1] = pack_bf16x2(sum[2], sum[3]);
-    *reinterpret_cast<u32x2*>(out) = v;
-  }
+  if (c < a.H) store_out<BF16>(a, t, c, combine_items(a, slices, t, c, 0, 1));
 }
 
-template <int F, int NT>
-hipError_t launch_ffn(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  decode_ffn_kernel<F, true, NT><<<dim3(p.up_tiles, p.entries), kThreads, 0, st>>>(
-      a, p.up_tiles, (a.H + fmt_step(F) - 1) / fmt_step(F));
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  decode_ffn_kernel<F, false, NT><<<dim3(p.down_tiles * p.slices, p.entries), kThreads, 0, st>>>(
-      a, p.down_tiles, p.slice_steps);
+template <int F, bool UP, int NT, int NW, int CW>
+hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
+  const int tiles = UP ? p.up_tiles : p.down_tiles, slices = UP ? 1 : p.slices;
+  const int steps = UP ? (a.H + fmt_step(F) - 1) / fmt_step(F) : p.slice_steps;
+  const dim3 grid(tiles * slices, p.entries);
+  if (UP ? p.head : p.tail)
+    decode_ffn_kernel<F, UP, NT, NW, CW, true><<<grid, NW * kWave, 0, st>>>(a, tiles, slices, steps);
+  else
+    decode_ffn_kernel<F, UP, NT, NW, CW, false><<<grid, NW * kWave, 0, st>>>(a, tiles, slices, steps);
   return hipGetLastError();
+}
+template <int F, bool UP>
+hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
+  const bool wide = (UP ? p.up_waves : p.down_waves) == 4;
+  if (p.row_tile == 16)
+    return wide ? launch_product<F, UP, 1, 4, 4>(a, p, st) : launch_product<F, UP, 1, 8, 1>(a, p, st);
+  return wide ? launch_product<F, UP, 2, 4, 4>(a, p, st) : launch_product<F, UP, 2, 8, 1>(a, p, st);
 }
 
 template <int F>
-hipError_t launch_ffn_nt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  return p.row_tile == 16 ? launch_ffn<F, 1>(a, p, st) : launch_ffn<F, 2>(a, p, st);
+hipError_t launch_fmt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
+  if (!p.head) {
+    decode_route_kernel<<<1, kRouteThreads, 0, st>>>(a, p.row_tile);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipError_t e = launch_product<F, true>(a, p, st);
+  if (e == hipSuccess) e = launch_product<F, false>(a, p, st);
+  if (p.tail || e != hipSuccess) return e;
+  decode_combine_kernel<!fmt_f32(F)><<<dim3((a.H / 4 + 255) / 256, a.T), 256, 0, st>>>(a, p.slices);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -543,16 +783,29 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
   DecodePlan p;
   p.row_tile = T <= 16 ? 16 : 32;
   const int64_t R = (int64_t)T * K;
+  p.head = R <= 4 * kWave && T <= kHeadTokens;   // a pair for every thread of the smaller blocks
+  p.tail = T <= kTailTokens;
   const int busy = (int)(R < E ? R : E);   // experts with rows, at most
   // an expert with c rows has at most 1 + (c - 1) / row_tile entries
   p.entries = busy + (int)((R - busy) / p.row_tile) + Ns * ((T + p.row_tile - 1) / p.row_tile);
-  p.up_tiles = (I + cols / 2 - 1) / (cols / 2);
-  p.down_tiles = (H + cols - 1) / cols;
+  // experts with rows as expected of even routing, and the shared ones
+  double miss = 1.0;
+  for (int t = 0; t < T; ++t) miss *= 1.0 - (double)K / E;
+  const double groups = E * (1.0 - miss) + Ns;
+  // Four column tiles side by side read 0.5 to 1 KiB of a row at once, where
+  // that leaves enough blocks for the 256 CUs.
+  const int up1 = (I + cols / 2 - 1) / (cols / 2), up4 = (I + 2 * cols - 1) / (2 * cols);
+  p.up_waves = up4 * groups >= kWideBlocks ? 4 : 1;
+  p.up_tiles = p.up_waves == 4 ? up4 : up1;
+  const int down1 = (H + cols - 1) / cols, down4 = (H + 4 * cols - 1) / (4 * cols);
   const int steps = (I + step - 1) / step;
-  // enough blocks for the 256 CUs twice over, each with work for its 8 waves
-  const int want = (int)((512 + (int64_t)p.down_tiles * (busy + Ns) - 1) / ((int64_t)p.down_tiles * (busy + Ns)));
-  int s = want < 1 ? 1 : want > 8 ? 8 : want;
-  const int most = (steps + kWaves - 1) / kWaves;
+  p.down_waves = down4 * groups * steps >= 8 * kWideBlocks ? 4 : 1;
+  p.down_tiles = p.down_waves == 4 ? down4 : down1;
+  // k slices: enough blocks for the CUs twice over, each with a step for every wave
+  const int shares = p.down_waves == 4 ? 1 : 8;
+  int s = (int)(512.0 / (p.down_tiles * groups) + 0.999);
+  const int most = (steps + shares - 1) / shares;
+  s = s < 1 ? 1 : s > 8 ? 8 : s;
   if (s > most) s = most;
   p.slice_steps = (steps + s - 1) / s;
   p.slices = (steps + p.slice_steps - 1) / p.slice_steps;
@@ -560,19 +813,8 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
 }
 
 hipError_t launch_decode(bool is_bf16, bool mx, const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if (a.E <= kWave)
-    decode_route_kernel<1><<<1, kRouteThreads, 0, st>>>(a, p.row_tile);
-  else
-    decode_route_kernel<4><<<1, kRouteThreads, 0, st>>>(a, p.row_tile);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (mx) e = is_bf16 ? launch_ffn_nt<kFmtMxBf16>(a, p, st) : launch_ffn_nt<kFmtMxF32>(a, p, st);
-  else e = is_bf16 ? launch_ffn_nt<kFmtBf16>(a, p, st) : launch_ffn_nt<kFmtF32>(a, p, st);
-  if (e != hipSuccess) return e;
-  const dim3 grid((a.H / 4 + 255) / 256, a.T);
-  if (is_bf16) decode_combine_kernel<uint16_t><<<grid, 256, 0, st>>>(a, p.slices);
-  else decode_combine_kernel<float><<<grid, 256, 0, st>>>(a, p.slices);
-  return hipGetLastError();
+  if (mx) return is_bf16 ? launch_fmt<kFmtMxBf16>(a, p, st) : launch_fmt<kFmtMxF32>(a, p, st);
+  return is_bf16 ? launch_fmt<kFmtBf16>(a, p, st) : launch_fmt<kFmtF32>(a, p, st);
 }
 
 }  // namespace moe

@@ -9,6 +9,10 @@ namespace moe {
 
 // Tokens a decode call takes at most (one routing block holds them all).
 constexpr int kDecodeMaxTokens = 256;
+// Words from one column tile's counter to the next: increments of one 64-byte
+// line follow each other every 13 ns, whichever counter they mean (512 of
+// them: 6.6 us).
+constexpr int kDoneStride = 64;
 // Largest H and I of the decode calls (lane offsets into a matrix's rows are
 // formed in 32 bits inside a k step).
 constexpr int kDecodeMaxDim = 1 << 20;
@@ -21,9 +25,13 @@ constexpr int kMxCodeBytes = 16;
 // Where the down projection's partial sums are cut: S slices of `steps` k
 // steps each.
 struct DecodePlan {
+  bool head;        // the first product's blocks route for themselves
+  bool tail;        // the second product's last blocks add up the output
   int row_tile;     // rows of one entry at most (16 or 32)
   int entries;      // bound on the number of entries (expert x row tile)
-  int up_tiles;     // column tiles of the gate/up projection
+  int up_waves;     // column tiles a block's waves span (1 or 4): gate/up projection
+  int down_waves;   // and down projection
+  int up_tiles;     // blocks' column tiles of the gate/up projection
   int down_tiles;   // column tiles of the down projection
   int slices;       // k slices of the down projection
   int slice_steps;  // k steps in each
@@ -45,10 +53,11 @@ struct DecodeArgs {
   float* topk_w;
   void* out;
   // workspace
-  int4* entries;       // {group, first row, rows, 0}
+  int2* entries;       // {group, rows}
   int32_t* n_entries;
-  int32_t* row_token;  // [R] token of each routed row
-  int32_t* slot;       // [T, K] row of each pair
+  int32_t* lists;      // [entries, row_tile] row ids
+  int32_t* done;       // [n_done], kDoneStride apart: blocks of a column tile that have stored their sums
+  int n_done;          // 0: the sum has a launch of its own
   void* h;             // [RA, I]: f32, or two bf16 planes (value, then what it left)
   float* y;            // [slices, RA, H]
 };

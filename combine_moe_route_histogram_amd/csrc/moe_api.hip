@@ -320,20 +320,21 @@ DecodePlan decode_plan_for(const moe_dims* d, bool mx) {
 // Workspace sections of a decode call (byte offsets); one layout for both
 // weight forms, sized for the larger.
 struct DecodeLayout {
-  size_t entries, n_entries, row_token, slot, h, y, total;
+  size_t entries, n_entries, lists, done, h, y, total;
 };
 DecodeLayout decode_layout(const moe_dims* d) {
   const bool mx_ok = d->H % kMxGroup == 0 && d->I % kMxGroup == 0;
   const DecodePlan a = decode_plan_for(d, false), b = mx_ok ? decode_plan_for(d, true) : a;
   const size_t R = (size_t)d->T * d->K, RA = R + (size_t)d->n_shared * d->T;
   const size_t entries = a.entries > b.entries ? a.entries : b.entries;
+  const size_t tiles = a.down_tiles > b.down_tiles ? a.down_tiles : b.down_tiles;
   const size_t slices = a.slices > b.slices ? a.slices : b.slices;
   DecodeLayout L;
   size_t off = 0;
-  L.entries = off;   off = align_up(off + entries * 16);
+  L.entries = off;   off = align_up(off + entries * 8);
   L.n_entries = off; off = align_up(off + 16);
-  L.row_token = off; off = align_up(off + R * 4);
-  L.slot = off;      off = align_up(off + R * 4);
+  L.lists = off;     off = align_up(off + entries * a.row_tile * 4);
+  L.done = off;      off = align_up(off + tiles * kDoneStride * 4);
   L.h = off;         off = align_up(off + RA * d->I * 4);
   L.y = off;         off = align_up(off + slices * RA * d->H * 4);
   L.total = off;
@@ -373,13 +374,15 @@ int decode(const moe_dims* d, bool mx, const float* logits, const void* x, const
   a.w1 = w1; a.w3 = w3; a.w2 = w2; a.ws1 = ws1; a.ws3 = ws3; a.ws2 = ws2;
   a.n_tokens = n_tokens;
   a.topk_idx = topk_idx; a.topk_w = topk_w; a.out = out;
-  a.entries = ws_at<int4>(ws, L.entries);
+  const DecodePlan p = decode_plan_for(d, mx);
+  a.entries = ws_at<int2>(ws, L.entries);
   a.n_entries = ws_at<int32_t>(ws, L.n_entries);
-  a.row_token = ws_at<int32_t>(ws, L.row_token);
-  a.slot = ws_at<int32_t>(ws, L.slot);
+  a.lists = ws_at<int32_t>(ws, L.lists);
+  a.done = ws_at<int32_t>(ws, L.done);
+  a.n_done = p.tail ? p.down_tiles : 0;
   a.h = ws_at<char>(ws, L.h);
   a.y = ws_at<float>(ws, L.y);
-  return hip_status(launch_decode(d->dtype == MOE_BF16, mx, a, decode_plan_for(d, mx), as_stream(stream)), what);
+  return hip_status(launch_decode(d->dtype == MOE_BF16, mx, a, p, as_stream(stream)), what);
 }
 
 int check_mx(int64_t G, int K, int N, int dtype) {

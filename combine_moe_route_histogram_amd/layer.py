@@ -120,7 +120,7 @@ def decode(b: DecodeBuffers, p: dict, stream=None):
     """The whole layer for a few tokens, logits to out.  p holds the device
     inputs as for forward(); its weights are plain matrices or packed ones
     (quantize_weights).  p["n_tokens"], if there, is the device int32 count of
-    the rows in use: the rows behind it are neither read nor written."""
+    the rows in use: the rows behind it have no effect and are not written."""
     call = moe_decode_mx if p["w1"].dtype == torch.uint8 else moe_decode
     call(b.d, p["logits"], p["x"], p["w1"], p["w3"], p["w2"], p.get("ws1"), p.get("ws3"), p.get("ws2"),
          p.get("n_tokens"), b.topk_idx, b.topk_w, b.out, b.ws, stream)

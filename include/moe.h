@@ -369,7 +369,7 @@ int moe_route_bwd(const moe_dims* d, const float* dtopk_w, const float* topk_w,
  *           NULL if n_shared = 0) in
  *  n_tokens device int32[1] in, or NULL: the number of rows in use, for batches
  *           padded to a fixed T (a captured graph); values outside [0, T] count
- *           as the nearest of the two.  Rows behind it are not read, and their
+ *           as the nearest of the two.  Rows behind it have no effect, and their
  *           topk_idx, topk_w and out stay as they were.
  *  topk_idx [T, K] i32, topk_w [T, K] f32 out: the bits moe_route gives
  *  out [T, H] out.  Float32 all the way, one rounding at the end: h and y are

@@ -100,11 +100,20 @@ def test_a_tensor_of_another_device_is_refused(monkeypatch):
 
     class Fake:
         def __init__(self, i):
-            self.device = torch.device("cuda", i)
+            self.i, self.device = i, torch.device("cuda", i)
+
+        def get_device(self):
+            return self.i
+    called = []
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    M._one_device(None, x=Fake(0), ws1=None)
-    with pytest.raises(ValueError, match="out is on cuda:1"):
-        M._one_device(None, x=Fake(0), out=Fake(1))
+    monkeypatch.setattr(M, "_ptr", lambda t, name, dtype, numel: None)
+    monkeypatch.setattr(M, "_stream", lambda stream: None)
+    monkeypatch.setattr(M, "_call", lambda name, *args: called.append(name))
+    M._launch("moe_decode", None, (), ((Fake(0), "x", None, 1), (None, "ws1", None, 1)), ())
+    assert called == ["moe_decode"]
+    with pytest.raises(ValueError, match="out is on cuda:1, the call runs on cuda:0"):
+        M._launch("moe_decode", None, (), ((Fake(0), "x", None, 1), (Fake(1), "out", None, 1)), ())
+    assert called == ["moe_decode"]
 
 
 def test_mx_oracle_hand_worked():

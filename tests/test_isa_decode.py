@@ -1,0 +1,20 @@
+"""Build-time check of the hand-off inside the second product of the layer for
+few tokens, on the AMD assembly of this repository's own build (gfx950): a
+block stores its sums with agent-coherent stores (sc1: written through its
+XCD's L2), waits for them, counts itself, and the last block to count
+invalidates its caches (buffer_inv sc1) before it reads all of them."""
+import re
+
+from test_isa_publish import _asm, _functions
+
+
+def test_down_projection_publishes_its_sums(tmp_path):
+    bodies = _functions(_asm("decode.hip", tmp_path), r"decode_ffn_kernelILi\dELb0ELi\dELi\dELi\dELb1E")
+    assert len(bodies) == 16                                # four weight forms, 16 and 32 rows, two block shapes
+    for body in bodies:
+        add = re.search(r"s_waitcnt vmcnt\(0\)(?:(?!s_waitcnt vmcnt).)*?global_atomic_add", body, flags=re.S)
+        assert add, "no vmcnt(0) wait ahead of the counter update"
+        stores = re.findall(r"^\s*global_store_dword\b.*$", body[:add.end()], flags=re.M)
+        assert stores and all(re.search(r"\bsc1\b", s) for s in stores)
+        assert not re.search(r"^\s*global_store_dwordx", body[:add.end()], flags=re.M)
+        assert re.search(r"^\s*buffer_inv\s+sc1\b", body[add.end():], flags=re.M)
