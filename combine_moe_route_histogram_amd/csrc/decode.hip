@@ -18,12 +18,16 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxWaves = 8;            // waves of a product block: 8, or 4 side by side
+constexpr int kWaves = 4;               // waves of a product block
+constexpr int kThreads = kWaves * kWave;
 constexpr int kRedRows = 8;             // rows whose sums go through LDS at once
 constexpr int kRouteThreads = 1024;
-constexpr int kHeadTokens = 32;   // routing inside the first product's blocks up to here
-constexpr int kTailTokens = 4;    // the output's sum inside the second product up to here
-constexpr double kWideBlocks = 224;
+constexpr int kHeadTokens = 64;         // routing inside the first product's blocks up to here
+constexpr int kTailTokens = 4;          // the output's sum inside the second product up to here
+constexpr int64_t kLongRow = 4096;      // bytes
+constexpr double kFillBlocks = 220;
+constexpr double kSliceBlocks = 400;    // the down projection is cut along k for so many blocks,
+constexpr int kMaxSlices = 8;           // into so many slices at most
 
 enum Fmt : int { kFmtBf16 = 0, kFmtF32 = 1, kFmtMxBf16 = 2, kFmtMxF32 = 3 };
 constexpr bool fmt_mx(int f) { return f >= kFmtMxBf16; }
@@ -154,14 +158,15 @@ __device__ __forceinline__ int tokens_in_use(const DecodeArgs& a) {
 }
 
 // The work is a list of entries, each some rows (at most row_tile) of one
-// expert: entries[i] = {group, rows}, their row ids at lists[i * row_tile].  A
+// expert: entries[i] = {group, rows}, their row ids at lists[i * row_tile]; the
+// entries that are not in use, up to the plan's bound, have no rows.  A
 // row id is the pair t K + k, or R + s T + t for shared expert s.  The order
 // of an entry's rows comes from a counter; no result depends on it (a row's
 // sums do not mix with its neighbours').
 //
 // One block routes all tokens and writes the list (batches beyond what each
 // product block routes for itself, see decode_plan).
-__global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(DecodeArgs a, int row_tile) {
+__global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(DecodeArgs a, int row_tile, int entries) {
   __shared__ int count[kMaxExperts], first[kMaxExperts], fill[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int E = a.E, K = a.K, n = tokens_in_use(a);
@@ -197,6 +202,7 @@ __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(DecodeArgs 
     a.lists[(int64_t)(routed + s * per + t / row_tile) * row_tile + t % row_tile] = a.R + s * a.T + t;
   }
   if (tid == 0) *a.n_entries = routed + a.Ns * per;
+  for (int i = routed + a.Ns * per + tid; i < entries; i += kRouteThreads) a.entries[i] = make_int2(0, 0);
   __syncthreads();
   for (int p = tid; p < pairs; p += kRouteThreads) {
     const int e = a.topk_idx[p], at = atomicAdd(&fill[e], 1);
@@ -209,21 +215,19 @@ __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(DecodeArgs 
 // load and of its picks; a launch of its own costs more, on the host too.
 // Writes what the second product and the caller need: the entry and its rows
 // by the blocks of column tile 0, the picks by the very first block.
-template <int NW>
 struct BlockRoute {
-  int32_t idx[NW * kWave];
-  float w[NW * kWave];
+  int32_t idx[kThreads];
+  float w[kThreads];
   int32_t list[32];
   int32_t count[kMaxExperts];
-  int32_t below[NW];
+  int32_t below[kWaves];
 };
-template <int NW>
-__device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute<NW>& r, int entry, bool write_entry,
+__device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, int entry, bool write_entry,
                                             bool write_picks, int row_tile, int tid, int& group, int& rows) {
   const int lane = tid & (kWave - 1), wave = tid / kWave;
   const int E = a.E, K = a.K, n = tokens_in_use(a), pairs = n * K;
-  for (int e = tid; e < kMaxExperts; e += NW * kWave) r.count[e] = 0;
-  route_all(a, n, wave, NW, lane, r.idx, r.w);
+  for (int e = tid; e < kMaxExperts; e += kThreads) r.count[e] = 0;
+  route_all(a, n, wave, kWaves, lane, r.idx, r.w);
   __syncthreads();
   if (a.T == 1) {   // each pick is an entry of its own, and so is each shared expert
     if (write_picks) {
@@ -233,7 +237,10 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute<NW>&
       }
       if (tid == 0) *a.n_entries = n * (K + a.Ns);
     }
-    if (entry >= n * (K + a.Ns)) return false;
+    if (entry >= n * (K + a.Ns)) {
+      if (write_entry && tid == 0) a.entries[entry] = make_int2(0, 0);
+      return false;
+    }
     const bool pick = entry < K;
     group = pick ? r.idx[entry] : E + entry - K;
     rows = 1;
@@ -286,7 +293,10 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute<NW>&
     }
     if (tid == 0) *a.n_entries = total;
   }
-  if (entry >= total) return false;
+  if (entry >= total) {
+    if (write_entry && tid == 0) a.entries[entry] = make_int2(0, 0);
+    return false;
+  }
   if (e >= 0) {   // the entry's rows: the expert's pairs in order, from part * row_tile on
     group = e;
     const uint64_t mask = __ballot(mine == e);
@@ -354,77 +364,91 @@ struct Stage {
 };
 
 // A lane's place: its column(s) in row 0 of the matrix it reads, and its rows.
+// Lanes without a column or a row of their own repeat a valid one.
 template <int F, bool UP, int NT>
 struct Lane {
   const char* w[fmt_mx(F) && UP ? 2 : 1];   // 4 bit: in W1 and W3 (up) or in W2
   const char* sc[fmt_mx(F) && UP ? 2 : 1];  // scales
   int groups;                               // 4 bit: column groups inside the matrix (whole ones: N % 32 == 0)
-  bool col_ok;                              // else: the lane's columns are inside
-  const char* act[NT];                      // null: no such row
+  const char* act[NT];
 };
 
-template <int F, bool UP, int NT>
-__device__ __forceinline__ void load_stage(Stage<F, UP, NT>& s, const Lane<F, UP, NT>& L, int step, int q,
-                                           int Kd, int N, int64_t plane) {
-  const u32x4 zero = {0, 0, 0, 0};
+// What lanes behind the matrix's end, or behind the wave's last step, take for
+// their rows' values.
+__device__ const u32x4 kZeros[8] = {};
+// A load of one of two places (a choice of pointers would make it a flat load,
+// which waits for everything).
+__device__ __forceinline__ u32x4 ld16_global(uint64_t address) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(address);
+}
+
+// Nothing here is conditional: behind a branch the compiler no longer knows
+// how many loads are in flight and waits for all of them before the next step
+// is computed.  Weights outside the matrix repeat the last ones inside: what
+// comes of such columns is not stored, and rows at or behind `limit` meet
+// zeros.
+constexpr int step_len(int f) { return fmt_mx(f) ? kMxGroup : 8; }   // a lane's rows in one k step
+template <int F, bool UP, int NT, class S>
+__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int step, int q, int Kd, int N) {
+  const int k = min(fmt_step(F) * step + step_len(F) * q, Kd - step_len(F));
   if constexpr (fmt_mx(F)) {
-    const int kb = 4 * step + q;
-    const bool ok = kb < Kd / kMxGroup;
-    const int64_t at = (int64_t)kb * N;
+    const int64_t at = (int64_t)(k / kMxGroup) * N;
 #pragma unroll
     for (int j = 0; j < fmt_groups(F); ++j) {
-      s.w[j] = zero;
-      s.s[j] = 127;
-      const int jj = UP ? j >> 1 : j;
-      if (ok && jj < L.groups) {
-        s.w[j] = ld16_stream(L.w[UP ? j & 1 : 0] + at * kMxCodeBytes + jj * 16 * kMxCodeBytes);
-        s.s[j] = static_cast<const uint8_t*>(static_cast<const void*>(L.sc[UP ? j & 1 : 0]))[at + jj * 16];
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      constexpr int V = act_vecs(F, UP);
-#pragma unroll
-      for (int v = 0; v < V; ++v) s.act[nt][v] = zero;
-      if (L.act[nt] && ok) {
-        if constexpr (F == kFmtMxF32) {
-          const char* p = L.act[nt] + (int64_t)kb * kMxGroup * 4;
-#pragma unroll
-          for (int v = 0; v < V; ++v) s.act[nt][v] = ld16(p + v * 16);
-        } else {
-          const char* p = L.act[nt] + (int64_t)kb * kMxGroup * 2;
-#pragma unroll
-          for (int v = 0; v < V; ++v) s.act[nt][v] = ld16(p + (v & 3) * 16 + (v >> 2) * plane);
-        }
-      }
+      const int i = UP ? j & 1 : 0, jj = min(UP ? j >> 1 : j, L.groups - 1);
+      s.w[j] = ld16_stream(L.w[i] + at * kMxCodeBytes + jj * 16 * kMxCodeBytes);
+      s.s[j] = static_cast<const uint8_t*>(static_cast<const void*>(L.sc[i]))[at + jj * 16];
     }
   } else {
     constexpr int B = fmt_f32(F) ? 4 : 2;
-    const int k = fmt_step(F) * step + 8 * q;
-    const bool ok = k < Kd;
     const char* p = L.w[0] + (int64_t)k * N * B;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s.w[i] = zero;
-      if (ok && L.col_ok) s.w[i] = ld16_stream(p + (int64_t)i * N * B);
+    for (int i = 0; i < 8; ++i) s.w[i] = ld16_stream(p + (int64_t)i * N * B);
+  }
+}
+
+template <int F, bool UP, int NT, int NTL>
+__device__ __forceinline__ void load_stage(Stage<F, UP, NTL>& s, const Lane<F, UP, NT>& L, int step, int q,
+                                           int Kd, int N, int limit, int64_t plane) {
+  constexpr int V = act_vecs(F, UP), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
+  constexpr int PER = LEN * B / 16;   // vectors of a lane's values from one plane
+  load_weights<F, UP, NT>(s, L, step, q, Kd, N);
+  const int at = fmt_step(F) * step + LEN * q, k = min(at, Kd - LEN);
+#pragma unroll
+  for (int nt = 0; nt < NTL; ++nt)
+#pragma unroll
+    for (int v0 = 0; v0 < V; v0 += PER) {
+      const uint64_t p = reinterpret_cast<uint64_t>(L.act[nt]) + (int64_t)k * B + v0 / PER * plane;
+      const uint64_t from = at < limit ? p : reinterpret_cast<uint64_t>(kZeros);
+#pragma unroll
+      for (int v = 0; v < PER; ++v) s.act[nt][v0 + v] = ld16_global(from + v * 16);
     }
+}
+
+// acc[nt][j] += word i of the lanes' codes (8 rows of column group j) x the
+// rows' values b of those 8; fp4 x 2^s is exact in bf16.
+template <int F, int NT, int NTL, int P>
+__device__ __forceinline__ void mma_mx(const u32x4 (&w)[fmt_groups(F)], const uint32_t (&scale)[fmt_groups(F)], int i,
+                                       const u32x4 (&b)[NTL][P], f32x4 (&acc)[NT][fmt_groups(F)]) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      constexpr int V = act_vecs(F, UP);
+  for (int j = 0; j < fmt_groups(F); ++j) {
+    const float sc = __uint_as_float(scale[j] << 23);
+    u32x4 A;
+    A[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 0));
+    A[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 1));
+    A[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 2));
+    A[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 3));
 #pragma unroll
-      for (int v = 0; v < V; ++v) s.act[nt][v] = zero;
-      if (L.act[nt] && ok) {
-        const char* r = L.act[nt] + (int64_t)k * B;
+    for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
-        for (int v = 0; v < V; ++v) s.act[nt][v] = ld16(r + (F == kFmtF32 ? (int64_t)v * 16 : v * plane));
-      }
-    }
+      for (int p = 0; p < P; ++p)
+        acc[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(A), as_bf16x8(b[nt][p]), acc[nt][j], 0, 0, 0);
   }
 }
 
 // acc[nt][j] += the step's weights (16 columns of group j) x rows (16 of tile nt).
-template <int F, bool UP, int NT>
-__device__ __forceinline__ void mma_stage(const Stage<F, UP, NT>& s, f32x4 (&acc)[NT][fmt_groups(F)]) {
+template <int F, bool UP, int NT, int NTL>
+__device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, f32x4 (&acc)[NT][fmt_groups(F)]) {
   if constexpr (F == kFmtBf16) {
     // A lane holds 8 columns of 8 rows; an operand wants 8 rows of one column:
     // halves of two rows' words are put together, one v_perm per two weights.
@@ -437,7 +461,7 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NT>& s, f32x4 (&acc
         for (int d = 0; d < 4; ++d)
           A[d] = __builtin_amdgcn_perm(s.w[2 * d + 1][r], s.w[2 * d][r], odd ? 0x07060302u : 0x05040100u);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
           for (int p = 0; p < act_parts(F, UP); ++p)
             acc[nt][2 * r + odd] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -450,16 +474,16 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NT>& s, f32x4 (&acc
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NTL; ++nt)
           acc[nt][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
               __uint_as_float(s.w[i][j]), __uint_as_float(s.act[nt][i >> 2][i & 3]), acc[nt][j], 0, 0, 0);
   } else {
     constexpr int P = act_parts(F, UP);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      u32x4 b[NT][P];
+      u32x4 b[NTL][P];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NTL; ++nt) {
         if constexpr (F == kFmtMxF32) {
           float f[8];
 #pragma unroll
@@ -470,22 +494,136 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NT>& s, f32x4 (&acc
           for (int p = 0; p < P; ++p) b[nt][p] = s.act[nt][4 * p + i];
         }
       }
-#pragma unroll
-      for (int j = 0; j < fmt_groups(F); ++j) {
-        const float sc = __uint_as_float(s.s[j] << 23);
-        u32x4 A;   // fp4 x 2^s is exact in bf16
-        A[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.w[j][i], sc, 0));
-        A[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.w[j][i], sc, 1));
-        A[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.w[j][i], sc, 2));
-        A[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.w[j][i], sc, 3));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-            acc[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(A), as_bf16x8(b[nt][p]), acc[nt][j], 0, 0, 0);
-      }
+      mma_mx<F, NT, NTL, P>(s.w, s.s, i, b, acc);
     }
   }
+}
+
+// A wave's k steps first, first + stride, ... below end.  Two steps are in
+// flight; a step's loads follow the products of the one before its
+// predecessor, so every wait is for the older of the two.  An odd count ends
+// with a step that counts as zeros, whose weights are its own last ones once
+// more.  (The barriers keep the scheduler from moving loads up, into registers
+// of their own.)
+template <int F, bool UP, int NT, int NTL>
+__device__ __forceinline__ void product_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
+                                             int stride, int end, int q, int Kd, int N, int64_t plane) {
+  Stage<F, UP, NTL> s0, s1;
+  auto load = [&](Stage<F, UP, NTL>& s, int k) {
+    load_stage<F, UP, NT, NTL>(s, L, k < end ? k : k - stride, q, Kd, N, k < end ? Kd : 0, plane);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto mma = [&](Stage<F, UP, NTL>& s) {
+    mma_stage<F, UP, NT, NTL>(s, acc);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (first >= end) return;
+  load(s0, first);
+  load(s1, first + stride);
+  mma(s0);
+#pragma unroll 1
+  for (int k = first + 2 * stride; k < end; k += 2 * stride) {
+    load(s0, k);
+    mma(s1);
+    load(s1, k + stride);
+    mma(s0);
+  }
+  mma(s1);
+}
+
+// 4-bit weights, more than 16 rows: the rows' values are the larger half of
+// what a step loads, and each lane's 16 bytes of them lie 64 bytes from its
+// neighbour's.  The block's waves, side by side on the same steps, load each
+// value once, whole lines at a time, split it into its bf16 parts, and hand it
+// on through LDS, one step ahead.
+constexpr int kActPitch = 128 * 2 + 16;   // bytes of a row in LDS: 16 rows' vectors on different banks
+template <int F, bool UP, int NT>
+constexpr int act_bytes() { return act_parts(F, UP) * 16 * NT * kActPitch; }
+
+template <int F, bool UP, int NT>
+struct WeightStage {
+  u32x4 w[fmt_groups(F)];
+  uint32_t s[fmt_groups(F)];
+};
+
+template <int F, bool UP, int NT, int NTL>
+__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
+                                            int end, int tid, int Kd, int N, int64_t plane,
+                                            const char* const (&src)[NT], char* lds) {
+  constexpr int P = act_parts(F, UP), B = fmt_f32(F) ? 4 : 2, VECS = F == kFmtMxF32 ? 2 : P;
+  const int lane = tid & (kWave - 1), m = lane & 15, q = lane >> 4, piece = tid & 15, row = tid >> 4;
+  WeightStage<F, UP, NT> s0, s1;
+  u32x4 v[NTL][VECS];   // this thread's 8 values of rows tid / 16, 16 + tid / 16
+  auto load_w = [&](WeightStage<F, UP, NT>& s, int k) {
+    load_weights<F, UP, NT>(s, L, k, q, Kd, N);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto load_act = [&](int k) {
+    const int at = fmt_step(F) * k + 8 * piece;
+#pragma unroll
+    for (int nt = 0; nt < NTL; ++nt)
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const uint64_t p = reinterpret_cast<uint64_t>(src[nt]) + (int64_t)at * B + (F == kFmtMxF32 ? (int64_t)i * 16 : i * plane);
+        v[nt][i] = ld16_global(at < Kd ? p : reinterpret_cast<uint64_t>(kZeros));
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto store_act = [&](int buf) {
+    char* base = lds + buf * act_bytes<F, UP, NT>() + row * kActPitch + piece * 16;
+#pragma unroll
+    for (int nt = 0; nt < NTL; ++nt) {
+      u32x4 part[P];
+      if constexpr (F == kFmtMxF32) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[nt][e >> 2][e & 3]);
+        split_bf16<P>(f, part);
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) part[p] = v[nt][p];
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) st16(base + (p * NT + nt) * 16 * kActPitch, part[p]);
+    }
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto mma = [&](const WeightStage<F, UP, NT>& s, int buf) {
+    const char* base = lds + buf * act_bytes<F, UP, NT>() + m * kActPitch + q * 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4 b[NTL][P];
+#pragma unroll
+      for (int nt = 0; nt < NTL; ++nt)
+#pragma unroll
+        for (int p = 0; p < P; ++p) b[nt][p] = ld16(base + (p * NT + nt) * 16 * kActPitch + i * 16);
+      mma_mx<F, NT, NTL, P>(s.w, s.s, i, b, acc);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // steps behind the end: their weights are not used, and their values not read
+  load_act(begin);
+  load_w(s0, begin);
+  load_w(s1, min(begin + 1, end - 1));
+  store_act(0);
+  int k = begin;
+#pragma unroll 1
+  for (; k + 2 < end; k += 2) {
+    load_act(k + 1);
+    mma(s0, 0);
+    load_w(s0, k + 2);
+    store_act(1);
+    load_act(k + 2);
+    mma(s1, 1);
+    load_w(s1, min(k + 3, end - 1));
+    store_act(0);
+  }
+  load_act(min(k + 1, end - 1));
+  mma(s0, 0);
+  store_act(1);
+  if (k + 1 < end) mma(s1, 1);
+  __syncthreads();   // the values are read; their LDS becomes the sums'
 }
 
 // Column of (group j, MFMA row m) inside a wave's tile of 16 * groups columns
@@ -550,8 +688,17 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int t, int c, con
   }
 }
 
+// All arguments in scalar registers at once: read where they are first used,
+// each cache line of them is a trip of its own to host memory.
+__device__ __forceinline__ void pin_args(const DecodeArgs& a) {
+  asm volatile("" ::"s"(a.T), "s"(a.H), "s"(a.E), "s"(a.K), "s"(a.I), "s"(a.Ns), "s"(a.R), "s"(a.logits), "s"(a.x),
+               "s"(a.w1), "s"(a.w3), "s"(a.w2), "s"(a.ws1), "s"(a.ws3), "s"(a.ws2), "s"(a.n_tokens), "s"(a.topk_idx),
+               "s"(a.topk_w), "s"(a.out), "s"(a.entries), "s"(a.n_entries), "s"(a.lists), "s"(a.done), "s"(a.n_done),
+               "s"(a.h), "s"(a.y));
+}
+
 // One block: one entry (up to 16 NT rows of one expert) x one tile of columns x
-// one k slice.  Its NW waves are CW column tiles next to each other x NW / CW
+// one k slice.  Its 4 waves are CW column tiles next to each other x 4 / CW
 // shares of the k steps, whose sums are added in wave order through LDS.
 //
 // HEAD: the first product's blocks route for themselves (block_route).
@@ -559,42 +706,56 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int t, int c, con
 // last: a block stores its sums coherently, waits until they are written, and
 // counts itself; whoever counts last reads them all.  Nobody waits for
 // anybody.  The first product's first block clears the counters.
-template <int F, bool UP, int NT, int NW, int CW, bool FUSED>
-__global__ __launch_bounds__(NW * kWave, NT == 1 && (!fmt_mx(F) || (UP && F == kFmtMxBf16)) ? 4 : 2) void decode_ffn_kernel(DecodeArgs a, int tiles, int slices, int slice_steps) {
+template <int F, bool UP, int NT, int CW, bool FUSED>
+__global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decode_ffn_kernel(DecodeArgs a, int slices, int slice_steps) {
   constexpr bool HEAD = UP && FUSED, TAIL = !UP && FUSED;
-  constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, KW = NW / CW, kThreads = NW * kWave;
+  constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, KW = kWaves / CW;
   constexpr int WCOLS = UP ? 8 * G : 16 * G, COLS = WCOLS * CW;   // columns of a wave, of the block
-  __shared__ __align__(16) float red[NW * kRedRows * red_stride<F>()];
+  constexpr bool SHARED = fmt_mx(F) && NT == 2;   // rows' values by way of LDS
+  constexpr int kRedFloats = kWaves * kRedRows * red_stride<F>();
+  constexpr int kActFloats = SHARED ? act_bytes<F, UP, NT>() / 2 : 0;
+  __shared__ __align__(16) float red[kRedFloats > kActFloats ? kRedFloats : kActFloats];
   __shared__ int last;
-  static_assert(sizeof(BlockRoute<NW>) <= sizeof(red) && kThreads * 16 <= sizeof(red), "other uses of the sums' LDS");
+  static_assert(sizeof(BlockRoute) <= sizeof(red) && kThreads * 16 <= sizeof(red), "other uses of the sums' LDS");
+  pin_args(a);
+  asm volatile("" ::"s"(slices), "s"(slice_steps));
   const int entry = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int m = lane & 15, q = lane >> 4;
-  const int tile = blockIdx.x % tiles, slice = blockIdx.x / tiles;
+  const int tile = blockIdx.x, slice = blockIdx.z;
   const int Kd = UP ? a.H : a.I, N = UP ? a.I : a.H;
   const int64_t RA = (int64_t)a.R + (int64_t)a.Ns * a.T;
   const int64_t plane = RA * a.I * 2;   // bytes between h's two bf16 planes
-  int group, rows, ids[NT], n_entries = 0;   // ids: this lane's rows
+  int group, rows, ids[NT];   // ids: this lane's rows
   if (UP && blockIdx.x == 0 && entry == 0)
     for (int i = tid; i < a.n_done; i += kThreads) a.done[i * kDoneStride] = 0;
   if constexpr (HEAD) {
-    BlockRoute<NW>& r = *reinterpret_cast<BlockRoute<NW>*>(red);
+    BlockRoute& r = *reinterpret_cast<BlockRoute*>(red);
     if (!block_route(a, r, entry, blockIdx.x == 0, blockIdx.x == 0 && entry == 0, 16 * NT, tid, group, rows)) return;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) ids[nt] = 16 * nt + m < rows ? r.list[16 * nt + m] : 0;
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = r.list[min(16 * nt + m, rows - 1)];
     __syncthreads();   // the list is read; its LDS becomes the sums'
   } else {
-    n_entries = *a.n_entries;
     const int2 en = a.entries[entry];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) ids[nt] = a.lists[(int64_t)entry * (16 * NT) + 16 * nt + m];
-    if (entry >= n_entries) return;
     group = en.x;
     rows = en.y;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(ids[nt]));   // asked for before rows is known
+    if (rows == 0) return;   // not in use
+    // Lanes without a row repeat the first one's.  (Read outside the choice:
+    // inside it, lane 0 would be switched off.)
+    const int id0 = __builtin_amdgcn_readfirstlane(ids[0]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = 16 * nt + m < rows ? ids[nt] : id0;
   }
+  group = __builtin_amdgcn_readfirstlane(group);
+  rows = __builtin_amdgcn_readfirstlane(rows);
   const bool shared = group >= a.E;
   const int g = shared ? group - a.E : group;
-  const int col0 = tile * COLS + wave % CW * WCOLS;   // the wave's first column
+  int col0 = tile * COLS + wave % CW * WCOLS;   // the wave's first column
+  if constexpr (SHARED) col0 = min(col0, N - 32);   // all waves work: nothing is stored for one behind the end
 
   Lane<F, UP, NT> L;
   if constexpr (fmt_mx(F)) {
@@ -608,23 +769,18 @@ __global__ __launch_bounds__(NW * kWave, NT == 1 && (!fmt_mx(F) || (UP && F == k
     L.groups = (N - col0) / 16;
   } else {
     bool second;
-    const int col = col0 + tile_col<F, UP>(0, m, second);
+    const int col = min(col0 + tile_col<F, UP>(0, m, second), N - G);
     const void* base = UP ? (second ? (shared ? a.ws3 : a.w3) : (shared ? a.ws1 : a.w1)) : (shared ? a.ws2 : a.w2);
     L.w[0] = static_cast<const char*>(base) + ((int64_t)g * Kd * N + col) * B;
-    L.col_ok = col < N;
   }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    L.act[nt] = nullptr;
-    if (16 * nt + m < rows) {
-      if constexpr (UP) {
-        const int t = shared ? ids[nt] - a.R - g * a.T : ids[nt] / a.K;
-        L.act[nt] = static_cast<const char*>(a.x) + (int64_t)t * a.H * B;
-      } else {
-        L.act[nt] = static_cast<const char*>(a.h) + (int64_t)ids[nt] * a.I * B;
-      }
+  auto row_values = [&](int id) {   // where a row's values begin
+    if constexpr (UP) {
+      const int t = shared ? id - a.R - g * a.T : id / a.K;
+      return static_cast<const char*>(a.x) + (int64_t)t * a.H * B;
+    } else {
+      return static_cast<const char*>(a.h) + (int64_t)id * a.I * B;
     }
-  }
+  };
 
   f32x4 acc[NT][G];
 #pragma unroll
@@ -634,21 +790,18 @@ __global__ __launch_bounds__(NW * kWave, NT == 1 && (!fmt_mx(F) || (UP && F == k
 
   const int steps = (Kd + fmt_step(F) - 1) / fmt_step(F);
   const int begin = slice * slice_steps, end = min(steps, begin + slice_steps);
-  Stage<F, UP, NT> s0, s1;
-  int k = begin + wave / CW;
-  if (k < end && col0 < N) {
-    load_stage<F, UP, NT>(s0, L, k, q, Kd, N, plane);
-    for (;;) {
-      const bool more1 = k + KW < end;
-      if (more1) load_stage<F, UP, NT>(s1, L, k + KW, q, Kd, N, plane);
-      mma_stage<F, UP, NT>(s0, acc);
-      if (!more1) break;
-      const bool more0 = k + 2 * KW < end;
-      if (more0) load_stage<F, UP, NT>(s0, L, k + 2 * KW, q, Kd, N, plane);
-      mma_stage<F, UP, NT>(s1, acc);
-      if (!more0) break;
-      k += 2 * KW;
-    }
+  if constexpr (SHARED) {
+    const char* src[NT];   // lane l of every wave holds ids l % 16; this thread's rows are tid / 16 and 16 more
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) src[nt] = row_values(__shfl(ids[nt], tid >> 4, kWave));
+    char* lds = reinterpret_cast<char*>(red);
+    if (rows <= 16) shared_loop<F, UP, NT, 1>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    else shared_loop<F, UP, NT, NT>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+  } else if (col0 < N) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) L.act[nt] = row_values(ids[nt]);
+    if (NT > 1 && rows <= 16) product_loop<F, UP, NT, 1>(L, acc, begin + wave / CW, KW, end, q, Kd, N, plane);
+    else product_loop<F, UP, NT, NT>(L, acc, begin + wave / CW, KW, end, q, Kd, N, plane);
   }
 
   constexpr int RS = red_stride<F>();
@@ -705,7 +858,7 @@ __global__ __launch_bounds__(NW * kWave, NT == 1 && (!fmt_mx(F) || (UP && F == k
     __syncthreads();
     if (tid == 0)
       last = __hip_atomic_fetch_add(&a.done[tile * kDoneStride], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-             n_entries * slices - 1;
+             *a.n_entries * slices - 1;
     __syncthreads();
     if (!last) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
@@ -742,29 +895,35 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int s
   if (c < a.H) store_out<BF16>(a, t, c, combine_items(a, slices, t, c, 0, 1));
 }
 
-template <int F, bool UP, int NT, int NW, int CW>
+template <int F, bool UP, int NT, int CW>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
   const int tiles = UP ? p.up_tiles : p.down_tiles, slices = UP ? 1 : p.slices;
   const int steps = UP ? (a.H + fmt_step(F) - 1) / fmt_step(F) : p.slice_steps;
-  const dim3 grid(tiles * slices, p.entries);
+  const dim3 grid(tiles, p.entries, slices);
   if (UP ? p.head : p.tail)
-    decode_ffn_kernel<F, UP, NT, NW, CW, true><<<grid, NW * kWave, 0, st>>>(a, tiles, slices, steps);
+    decode_ffn_kernel<F, UP, NT, CW, true><<<grid, kThreads, 0, st>>>(a, slices, steps);
   else
-    decode_ffn_kernel<F, UP, NT, NW, CW, false><<<grid, NW * kWave, 0, st>>>(a, tiles, slices, steps);
+    decode_ffn_kernel<F, UP, NT, CW, false><<<grid, kThreads, 0, st>>>(a, slices, steps);
   return hipGetLastError();
+}
+template <int F, bool UP, int NT>
+hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
+  if constexpr (fmt_mx(F) && NT == 2) return launch_product<F, UP, NT, 4>(a, p, st);
+  else switch (UP ? p.up_width : p.down_width) {
+    case 1: return launch_product<F, UP, NT, 1>(a, p, st);
+    case 2: return launch_product<F, UP, NT, 2>(a, p, st);
+    default: return launch_product<F, UP, NT, 4>(a, p, st);
+  }
 }
 template <int F, bool UP>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  const bool wide = (UP ? p.up_waves : p.down_waves) == 4;
-  if (p.row_tile == 16)
-    return wide ? launch_product<F, UP, 1, 4, 4>(a, p, st) : launch_product<F, UP, 1, 8, 1>(a, p, st);
-  return wide ? launch_product<F, UP, 2, 4, 4>(a, p, st) : launch_product<F, UP, 2, 8, 1>(a, p, st);
+  return p.row_tile == 16 ? launch_product<F, UP, 1>(a, p, st) : launch_product<F, UP, 2>(a, p, st);
 }
 
 template <int F>
 hipError_t launch_fmt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
   if (!p.head) {
-    decode_route_kernel<<<1, kRouteThreads, 0, st>>>(a, p.row_tile);
+    decode_route_kernel<<<1, kRouteThreads, 0, st>>>(a, p.row_tile, p.entries);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -777,13 +936,28 @@ hipError_t launch_fmt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) 
 
 }  // namespace
 
+// Column tiles a block's waves take side by side (1, 2 or 4).  Where a row of
+// the matrix is long, pieces of it that are read at the same time and are far
+// apart use few of the memory's channels, so the block reads as wide a piece as
+// leaves kFillBlocks blocks (bf16 [4096, 14336] x 2, 32 tokens: 1, 2, 4 tiles
+// 503, 476, 454 us a call; one token: 140, 127, 155).  Short rows want more
+// blocks instead ([2048, 1408] x 2, 16 tokens: 159, 166, 185 us).
+// 4-bit rows are long ones, and their waves work side by side on the same rows'
+// values where those go through LDS.
+static int tile_width(bool mx, int row_tile, int64_t row_bytes, int columns, int tile, double groups_and_slices) {
+  if (mx && row_tile == 32) return 4;
+  for (int w = mx ? 2 : row_bytes >= 2 * kLongRow ? 4 : row_bytes >= kLongRow ? 2 : 1; w > 1; w /= 2)
+    if ((columns + w * tile - 1) / (w * tile) * groups_and_slices >= kFillBlocks) return w;
+  return 1;
+}
+
 DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I, int Ns) {
   const int f = mx ? (is_bf16 ? kFmtMxBf16 : kFmtMxF32) : (is_bf16 ? kFmtBf16 : kFmtF32);
-  const int cols = 16 * fmt_groups(f), step = fmt_step(f);
+  const int tile = 16 * fmt_groups(f), step = fmt_step(f), size = is_bf16 ? 2 : 4;
   DecodePlan p;
   p.row_tile = T <= 16 ? 16 : 32;
   const int64_t R = (int64_t)T * K;
-  p.head = R <= 4 * kWave && T <= kHeadTokens;   // a pair for every thread of the smaller blocks
+  p.head = R <= kThreads && T <= kHeadTokens;   // a pair for every thread of a block
   p.tail = T <= kTailTokens;
   const int busy = (int)(R < E ? R : E);   // experts with rows, at most
   // an expert with c rows has at most 1 + (c - 1) / row_tile entries
@@ -792,21 +966,13 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
   double miss = 1.0;
   for (int t = 0; t < T; ++t) miss *= 1.0 - (double)K / E;
   const double groups = E * (1.0 - miss) + Ns;
-  // Four column tiles side by side read 0.5 to 1 KiB of a row at once, where
-  // that leaves enough blocks for the 256 CUs.
-  const int up1 = (I + cols / 2 - 1) / (cols / 2), up4 = (I + 2 * cols - 1) / (2 * cols);
-  p.up_waves = up4 * groups >= kWideBlocks ? 4 : 1;
-  p.up_tiles = p.up_waves == 4 ? up4 : up1;
-  const int down1 = (H + cols - 1) / cols, down4 = (H + 4 * cols - 1) / (4 * cols);
-  const int steps = (I + step - 1) / step;
-  p.down_waves = down4 * groups * steps >= 8 * kWideBlocks ? 4 : 1;
-  p.down_tiles = p.down_waves == 4 ? down4 : down1;
-  // k slices: enough blocks for the CUs twice over, each with a step for every wave
-  const int shares = p.down_waves == 4 ? 1 : 8;
-  int s = (int)(512.0 / (p.down_tiles * groups) + 0.999);
-  const int most = (steps + shares - 1) / shares;
-  s = s < 1 ? 1 : s > 8 ? 8 : s;
-  if (s > most) s = most;
+  p.up_width = tile_width(mx, p.row_tile, (int64_t)I * size, I, tile / 2, groups);
+  p.up_tiles = (I + p.up_width * tile / 2 - 1) / (p.up_width * tile / 2);
+  const int steps = (I + step - 1) / step, most = steps < kMaxSlices ? steps : kMaxSlices;
+  p.down_width = tile_width(mx, p.row_tile, (int64_t)H * size, H, tile, groups * (most < 2 ? most : 2));
+  p.down_tiles = (H + p.down_width * tile - 1) / (p.down_width * tile);
+  int s = (int)(kSliceBlocks / (p.down_tiles * groups) + 0.999);
+  s = s < 1 ? 1 : s > most ? most : s;
   p.slice_steps = (steps + s - 1) / s;
   p.slices = (steps + p.slice_steps - 1) / p.slice_steps;
   return p;

@@ -29,8 +29,8 @@ struct DecodePlan {
   bool tail;        // the second product's last blocks add up the output
   int row_tile;     // rows of one entry at most (16 or 32)
   int entries;      // bound on the number of entries (expert x row tile)
-  int up_waves;     // column tiles a block's waves span (1 or 4): gate/up projection
-  int down_waves;   // and down projection
+  int up_width;     // column tiles a block's waves span (1, 2 or 4): gate/up projection
+  int down_width;   // and down projection
   int up_tiles;     // blocks' column tiles of the gate/up projection
   int down_tiles;   // column tiles of the down projection
   int slices;       // k slices of the down projection
