@@ -22,7 +22,7 @@ constexpr int kWaves = 4;               // waves of a product block
 constexpr int kThreads = kWaves * kWave;
 constexpr int kRedRows = 8;             // rows whose sums go through LDS at once
 constexpr int kRouteThreads = 1024;
-constexpr int kHeadTokens = 64;         // routing inside the first product's blocks up to here
+constexpr int kHeadTokens = 16;         // top-k inside the first product's blocks up to here
 constexpr int kTailTokens = 4;          // the output's sum inside the second product up to here
 constexpr int64_t kLongRow = 4096;      // bytes
 constexpr double kFillBlocks = 220;
@@ -164,8 +164,8 @@ __device__ __forceinline__ int tokens_in_use(const DecodeArgs& a) {
 // of an entry's rows comes from a counter; no result depends on it (a row's
 // sums do not mix with its neighbours').
 //
-// One block routes all tokens and writes the list (batches beyond what each
-// product block routes for itself, see decode_plan).
+// One block routes all tokens and writes the list (more pairs than a product's
+// block lists for itself, see decode_plan).
 __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(DecodeArgs a, int row_tile, int entries) {
   __shared__ int count[kMaxExperts], first[kMaxExperts], fill[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
@@ -210,26 +210,47 @@ __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(DecodeArgs 
   }
 }
 
+// The top-k alone, a wave a token: the list is then made by each block of the
+// first product.
+__global__ __launch_bounds__(kThreads) void decode_topk_kernel(DecodeArgs a) {
+  const int lane = threadIdx.x & (kWave - 1), t = blockIdx.x * kWaves + threadIdx.x / kWave;
+  if (t >= a.T) return;
+  const int n = tokens_in_use(a);
+  if (a.E <= kWave) route_tokens<1, 1>(a.logits, t, 1, a.T, n, a.E, a.K, lane, a.topk_idx, a.topk_w);
+  else route_tokens<kMaxExperts / kWave, 1>(a.logits, t, 1, a.T, n, a.E, a.K, lane, a.topk_idx, a.topk_w);
+}
+
 // The same list, entry by entry, by every block of the first product for
-// itself (at most one pair a thread).  It costs a block the latency of one
-// load and of its picks; a launch of its own costs more, on the host too.
-// Writes what the second product and the caller need: the entry and its rows
-// by the blocks of column tile 0, the picks by the very first block.
+// itself: from the picks, or (few tokens) from the logits.  It costs a block
+// the latency of a load or two; a launch of its own costs more, on the host
+// too, and one block that does it for all takes longer (200 tokens of 4 picks:
+// 17 us).  Writes what the second product and the caller need: the entry and
+// its rows by the blocks of column tile 0, the picks by the very first block.
+constexpr int kListRounds = 8, kListPairs = kListRounds * kThreads;   // pairs a block can list
 struct BlockRoute {
-  int32_t idx[kThreads];
+  int32_t idx[kThreads];   // picks and weights made here: at most a pair a thread
   float w[kThreads];
   int32_t list[32];
   int32_t count[kMaxExperts];
-  int32_t below[kWaves];
+  int32_t below[kListRounds * kWaves];
 };
 __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, int entry, bool write_entry,
                                             bool write_picks, int row_tile, int tid, int& group, int& rows) {
   const int lane = tid & (kWave - 1), wave = tid / kWave;
-  const int E = a.E, K = a.K, n = tokens_in_use(a), pairs = n * K;
+  const int E = a.E, K = a.K;
+  int mine[kListRounds];   // the expert of pair tid + 256 i
+  if (a.picked) {
+#pragma unroll
+    for (int i = 0; i < kListRounds; ++i) {
+      const int p = tid + i * kThreads;
+      mine[i] = p < a.R ? a.topk_idx[p] : -1;
+    }
+  }
+  const int n = tokens_in_use(a), pairs = n * K;
   for (int e = tid; e < kMaxExperts; e += kThreads) r.count[e] = 0;
-  route_all(a, n, wave, kWaves, lane, r.idx, r.w);
+  if (!a.picked) route_all(a, n, wave, kWaves, lane, r.idx, r.w);
   __syncthreads();
-  if (a.T == 1) {   // each pick is an entry of its own, and so is each shared expert
+  if (a.T == 1 && !a.picked) {   // each pick is an entry of its own, and so is each shared expert
     if (write_picks) {
       if (tid < pairs) {
         a.topk_idx[tid] = r.idx[tid];
@@ -253,8 +274,16 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
     }
     return true;
   }
-  const int mine = tid < pairs ? r.idx[tid] : -1;
-  if (tid < pairs) atomicAdd(&r.count[mine], 1);
+  if (!a.picked) {
+    mine[0] = r.idx[tid];
+#pragma unroll
+    for (int i = 1; i < kListRounds; ++i) mine[i] = -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kListRounds; ++i) {
+    if (tid + i * kThreads >= pairs) mine[i] = -1;
+    if (mine[i] >= 0) atomicAdd(&r.count[mine[i]], 1);
+  }
   __syncthreads();
   // the expert that holds this entry, and which of its entries it is
   int seen = 0, e = -1, part = 0;
@@ -287,8 +316,8 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
   }
   const int per = (n + row_tile - 1) / row_tile, total = seen + a.Ns * per;
   if (write_picks) {
-    if (tid < pairs) {
-      a.topk_idx[tid] = mine;
+    if (!a.picked && tid < pairs) {
+      a.topk_idx[tid] = mine[0];
       a.topk_w[tid] = r.w[tid];
     }
     if (tid == 0) *a.n_entries = total;
@@ -299,12 +328,26 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
   }
   if (e >= 0) {   // the entry's rows: the expert's pairs in order, from part * row_tile on
     group = e;
-    const uint64_t mask = __ballot(mine == e);
-    if (lane == 0) r.below[wave] = __popcll(mask);
+    uint64_t mask[kListRounds];
+#pragma unroll
+    for (int i = 0; i < kListRounds; ++i) {
+      mask[i] = __ballot(mine[i] == e);
+      if (lane == 0) r.below[i * kWaves + wave] = __popcll(mask[i]);
+    }
     __syncthreads();
-    int rank = __popcll(mask & ((1ull << lane) - 1)) - part * row_tile;
-    for (int v = 0; v < wave; ++v) rank += r.below[v];
-    if (mine == e && rank >= 0 && rank < row_tile) r.list[rank] = tid;
+    int sum = lane < kListRounds * kWaves ? r.below[lane] : 0;   // up to and with a wave's share
+#pragma unroll
+    for (int o = 1; o < kListRounds * kWaves; o <<= 1) {
+      const int v = __shfl_up(sum, o, kWave);
+      if (lane >= o) sum += v;
+    }
+#pragma unroll
+    for (int i = 0; i < kListRounds; ++i) {
+      const int at = i * kWaves + __builtin_amdgcn_readfirstlane(wave);
+      const int base = __builtin_amdgcn_readlane(sum, at) - __popcll(mask[i]) - part * row_tile;
+      const int rank = base + __popcll(mask[i] & ((1ull << lane) - 1));
+      if (mine[i] == e && rank >= 0 && rank < row_tile) r.list[rank] = tid + i * kThreads;
+    }
   } else {
     const int s = (entry - seen) / per, t0 = (entry - seen - s * per) * row_tile;
     group = E + s;
@@ -359,7 +402,7 @@ template <int F, bool UP, int NT>
 struct Stage {
   static constexpr int kLoads = fmt_mx(F) ? fmt_groups(F) : 8;
   u32x4 w[kLoads];
-  uint32_t s[fmt_mx(F) ? fmt_groups(F) : 1];
+  uint32_t s;   // 4 bit: the scales of 4 columns next to each other (see lane_scales)
   u32x4 act[NT][act_vecs(F, UP)];
 };
 
@@ -368,14 +411,14 @@ struct Stage {
 template <int F, bool UP, int NT>
 struct Lane {
   const char* w[fmt_mx(F) && UP ? 2 : 1];   // 4 bit: in W1 and W3 (up) or in W2
-  const char* sc[fmt_mx(F) && UP ? 2 : 1];  // scales
+  const char* sc;                           // 4 bit: this lane's 4 scales in row 0
   int groups;                               // 4 bit: column groups inside the matrix (whole ones: N % 32 == 0)
   const char* act[NT];
 };
 
 // What lanes behind the matrix's end, or behind the wave's last step, take for
 // their rows' values.
-__device__ const u32x4 kZeros[8] = {};
+__device__ const u32x4 kZeros[32] = {};
 // A load of one of two places (a choice of pointers would make it a flat load,
 // which waits for everything).
 __device__ __forceinline__ u32x4 ld16_global(uint64_t address) {
@@ -397,8 +440,8 @@ __device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int
     for (int j = 0; j < fmt_groups(F); ++j) {
       const int i = UP ? j & 1 : 0, jj = min(UP ? j >> 1 : j, L.groups - 1);
       s.w[j] = ld16_stream(L.w[i] + at * kMxCodeBytes + jj * 16 * kMxCodeBytes);
-      s.s[j] = static_cast<const uint8_t*>(static_cast<const void*>(L.sc[i]))[at + jj * 16];
     }
+    s.s = *reinterpret_cast<const uint32_t*>(L.sc + at);
   } else {
     constexpr int B = fmt_f32(F) ? 4 : 2;
     const char* p = L.w[0] + (int64_t)k * N * B;
@@ -407,13 +450,23 @@ __device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int
   }
 }
 
+// 4-bit weights: where column c of h is kept in its row.  Inside 128 columns the
+// four lanes' groups of 32 take turns, 8 columns at a time, so what the lanes
+// read of a row with one load lies together (64 bytes).  Rows are padded to
+// whole 128s.
+__device__ __forceinline__ int mx_h_place(int c) {
+  return (c & ~127) | ((c >> 3) & 3) << 5 | ((c >> 5) & 3) << 3 | (c & 7);
+}
+
 template <int F, bool UP, int NT, int NTL>
 __device__ __forceinline__ void load_stage(Stage<F, UP, NTL>& s, const Lane<F, UP, NT>& L, int step, int q,
                                            int Kd, int N, int limit, int64_t plane) {
   constexpr int V = act_vecs(F, UP), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
   constexpr int PER = LEN * B / 16;   // vectors of a lane's values from one plane
+  constexpr int V8 = 8 * B / 16;      // and of 8 values
+  constexpr bool TURNS = fmt_mx(F) && !UP;   // h in the order of mx_h_place
   load_weights<F, UP, NT>(s, L, step, q, Kd, N);
-  const int at = fmt_step(F) * step + LEN * q, k = min(at, Kd - LEN);
+  const int at = fmt_step(F) * step + LEN * q, k = TURNS ? fmt_step(F) * step + 8 * q : at;
 #pragma unroll
   for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
@@ -421,23 +474,39 @@ __device__ __forceinline__ void load_stage(Stage<F, UP, NTL>& s, const Lane<F, U
       const uint64_t p = reinterpret_cast<uint64_t>(L.act[nt]) + (int64_t)k * B + v0 / PER * plane;
       const uint64_t from = at < limit ? p : reinterpret_cast<uint64_t>(kZeros);
 #pragma unroll
-      for (int v = 0; v < PER; ++v) s.act[nt][v0 + v] = ld16_global(from + v * 16);
+      for (int v = 0; v < PER; ++v)
+        s.act[nt][v0 + v] = ld16_global(from + (TURNS ? v / V8 * 32 * B + v % V8 * 16 : v * 16));
     }
+}
+
+// The scales 2^s of a lane's columns 16 j + m.  They are loaded 4 columns to a
+// lane (lane m of the 16 that share a group of 32 rows has columns 4 m .. 4 m +
+// 3; up: lanes 0..7 of W1, 8..15 of W3), one load in the place of one for each
+// column group's bytes (which cost the wide layer's first product 13 % of its
+// time), and handed to the lanes that want them.
+template <int F, bool UP>
+__device__ __forceinline__ void lane_scales(uint32_t loaded, int lane, float (&sc)[fmt_groups(F)]) {
+  const int from = 4 * ((lane & 48) + ((lane & 15) >> 2)), shift = 8 * (lane & 3);
+#pragma unroll
+  for (int j = 0; j < fmt_groups(F); ++j) {
+    const int at = UP ? 32 * (j & 1) + 16 * (j >> 1) : 16 * j;   // bytes from `from` to the source lane
+    const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute(from + at, (int)loaded);
+    sc[j] = __uint_as_float(((v >> shift) & 0xFFu) << 23);
+  }
 }
 
 // acc[nt][j] += word i of the lanes' codes (8 rows of column group j) x the
 // rows' values b of those 8; fp4 x 2^s is exact in bf16.
 template <int F, int NT, int NTL, int P>
-__device__ __forceinline__ void mma_mx(const u32x4 (&w)[fmt_groups(F)], const uint32_t (&scale)[fmt_groups(F)], int i,
+__device__ __forceinline__ void mma_mx(const u32x4 (&w)[fmt_groups(F)], const float (&sc)[fmt_groups(F)], int i,
                                        const u32x4 (&b)[NTL][P], f32x4 (&acc)[NT][fmt_groups(F)]) {
 #pragma unroll
   for (int j = 0; j < fmt_groups(F); ++j) {
-    const float sc = __uint_as_float(scale[j] << 23);
     u32x4 A;
-    A[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 0));
-    A[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 1));
-    A[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 2));
-    A[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc, 3));
+    A[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc[j], 0));
+    A[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc[j], 1));
+    A[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc[j], 2));
+    A[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][i], sc[j], 3));
 #pragma unroll
     for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
@@ -448,7 +517,7 @@ __device__ __forceinline__ void mma_mx(const u32x4 (&w)[fmt_groups(F)], const ui
 
 // acc[nt][j] += the step's weights (16 columns of group j) x rows (16 of tile nt).
 template <int F, bool UP, int NT, int NTL>
-__device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, f32x4 (&acc)[NT][fmt_groups(F)]) {
+__device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, int lane, f32x4 (&acc)[NT][fmt_groups(F)]) {
   if constexpr (F == kFmtBf16) {
     // A lane holds 8 columns of 8 rows; an operand wants 8 rows of one column:
     // halves of two rows' words are put together, one v_perm per two weights.
@@ -479,6 +548,8 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, f32x4 (&ac
               __uint_as_float(s.w[i][j]), __uint_as_float(s.act[nt][i >> 2][i & 3]), acc[nt][j], 0, 0, 0);
   } else {
     constexpr int P = act_parts(F, UP);
+    float sc[fmt_groups(F)];
+    lane_scales<F, UP>(s.s, lane, sc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 b[NTL][P];
@@ -494,7 +565,7 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, f32x4 (&ac
           for (int p = 0; p < P; ++p) b[nt][p] = s.act[nt][4 * p + i];
         }
       }
-      mma_mx<F, NT, NTL, P>(s.w, s.s, i, b, acc);
+      mma_mx<F, NT, NTL, P>(s.w, sc, i, b, acc);
     }
   }
 }
@@ -507,14 +578,15 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, f32x4 (&ac
 // of their own.)
 template <int F, bool UP, int NT, int NTL>
 __device__ __forceinline__ void product_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
-                                             int stride, int end, int q, int Kd, int N, int64_t plane) {
+                                             int stride, int end, int lane, int Kd, int N, int64_t plane) {
+  const int q = lane >> 4;
   Stage<F, UP, NTL> s0, s1;
   auto load = [&](Stage<F, UP, NTL>& s, int k) {
     load_stage<F, UP, NT, NTL>(s, L, k < end ? k : k - stride, q, Kd, N, k < end ? Kd : 0, plane);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mma = [&](Stage<F, UP, NTL>& s) {
-    mma_stage<F, UP, NT, NTL>(s, acc);
+    mma_stage<F, UP, NT, NTL>(s, lane, acc);
     __builtin_amdgcn_sched_barrier(0);
   };
   if (first >= end) return;
@@ -543,7 +615,7 @@ constexpr int act_bytes() { return act_parts(F, UP) * 16 * NT * kActPitch; }
 template <int F, bool UP, int NT>
 struct WeightStage {
   u32x4 w[fmt_groups(F)];
-  uint32_t s[fmt_groups(F)];
+  uint32_t s;
 };
 
 template <int F, bool UP, int NT, int NTL>
@@ -560,12 +632,13 @@ __device__ __forceinline__ void shared_loop(const Lane<F, UP, NT>& L, f32x4 (&ac
   };
   auto load_act = [&](int k) {
     const int at = fmt_step(F) * k + 8 * piece;
+    const int col = UP ? at : fmt_step(F) * k + 32 * (piece & 3) + 8 * (piece >> 2);   // see mx_h_place
 #pragma unroll
     for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
         const uint64_t p = reinterpret_cast<uint64_t>(src[nt]) + (int64_t)at * B + (F == kFmtMxF32 ? (int64_t)i * 16 : i * plane);
-        v[nt][i] = ld16_global(at < Kd ? p : reinterpret_cast<uint64_t>(kZeros));
+        v[nt][i] = ld16_global(col < Kd ? p : reinterpret_cast<uint64_t>(kZeros));
       }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -590,15 +663,17 @@ __device__ __forceinline__ void shared_loop(const Lane<F, UP, NT>& L, f32x4 (&ac
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mma = [&](const WeightStage<F, UP, NT>& s, int buf) {
-    const char* base = lds + buf * act_bytes<F, UP, NT>() + m * kActPitch + q * 64;
+    const char* base = lds + buf * act_bytes<F, UP, NT>() + m * kActPitch + q * (UP ? 64 : 16);
+    float sc[fmt_groups(F)];
+    lane_scales<F, UP>(s.s, lane, sc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 b[NTL][P];
 #pragma unroll
       for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
-        for (int p = 0; p < P; ++p) b[nt][p] = ld16(base + (p * NT + nt) * 16 * kActPitch + i * 16);
-      mma_mx<F, NT, NTL, P>(s.w, s.s, i, b, acc);
+        for (int p = 0; p < P; ++p) b[nt][p] = ld16(base + (p * NT + nt) * 16 * kActPitch + i * (UP ? 16 : 64));
+      mma_mx<F, NT, NTL, P>(s.w, sc, i, b, acc);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -694,14 +769,14 @@ __device__ __forceinline__ void pin_args(const DecodeArgs& a) {
   asm volatile("" ::"s"(a.T), "s"(a.H), "s"(a.E), "s"(a.K), "s"(a.I), "s"(a.Ns), "s"(a.R), "s"(a.logits), "s"(a.x),
                "s"(a.w1), "s"(a.w3), "s"(a.w2), "s"(a.ws1), "s"(a.ws3), "s"(a.ws2), "s"(a.n_tokens), "s"(a.topk_idx),
                "s"(a.topk_w), "s"(a.out), "s"(a.entries), "s"(a.n_entries), "s"(a.lists), "s"(a.done), "s"(a.n_done),
-               "s"(a.h), "s"(a.y));
+               "s"(a.h), "s"(a.y), "s"(a.picked));
 }
 
 // One block: one entry (up to 16 NT rows of one expert) x one tile of columns x
 // one k slice.  Its 4 waves are CW column tiles next to each other x 4 / CW
 // shares of the k steps, whose sums are added in wave order through LDS.
 //
-// HEAD: the first product's blocks route for themselves (block_route).
+// HEAD: the first product's blocks make the list for themselves (block_route).
 // TAIL: the second's add up the output of a column tile when they are its
 // last: a block stores its sums coherently, waits until they are written, and
 // counts itself; whoever counts last reads them all.  Nobody waits for
@@ -714,9 +789,11 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
   constexpr bool SHARED = fmt_mx(F) && NT == 2;   // rows' values by way of LDS
   constexpr int kRedFloats = kWaves * kRedRows * red_stride<F>();
   constexpr int kActFloats = SHARED ? act_bytes<F, UP, NT>() / 2 : 0;
-  __shared__ __align__(16) float red[kRedFloats > kActFloats ? kRedFloats : kActFloats];
+  constexpr int kRouteFloats = HEAD ? (sizeof(BlockRoute) + 15) / 16 * 4 : 0;
+  constexpr int kMainFloats = kRedFloats > kActFloats ? kRedFloats : kActFloats;
+  __shared__ __align__(16) float red[kMainFloats > kRouteFloats ? kMainFloats : kRouteFloats];
   __shared__ int last;
-  static_assert(sizeof(BlockRoute) <= sizeof(red) && kThreads * 16 <= sizeof(red), "other uses of the sums' LDS");
+  static_assert(kThreads * 16 <= sizeof(red), "the parts' sums of a token");
   pin_args(a);
   asm volatile("" ::"s"(slices), "s"(slice_steps));
   const int entry = blockIdx.y;
@@ -725,7 +802,8 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
   const int tile = blockIdx.x, slice = blockIdx.z;
   const int Kd = UP ? a.H : a.I, N = UP ? a.I : a.H;
   const int64_t RA = (int64_t)a.R + (int64_t)a.Ns * a.T;
-  const int64_t plane = RA * a.I * 2;   // bytes between h's two bf16 planes
+  const int64_t Ih = fmt_mx(F) ? (a.I + 127) / 128 * 128 : a.I;   // a row of h
+  const int64_t plane = RA * Ih * 2;   // bytes between h's two bf16 planes
   int group, rows, ids[NT];   // ids: this lane's rows
   if (UP && blockIdx.x == 0 && entry == 0)
     for (int i = tid; i < a.n_done; i += kThreads) a.done[i * kDoneStride] = 0;
@@ -764,7 +842,9 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
     for (int i = 0; i < (UP ? 2 : 1); ++i) {
       const void* base = UP ? (i ? (shared ? a.ws3 : a.w3) : (shared ? a.ws1 : a.w1)) : (shared ? a.ws2 : a.w2);
       L.w[i] = static_cast<const char*>(base) + (g * one + col0 + m) * kMxCodeBytes;
-      L.sc[i] = static_cast<const char*>(base) + (shared ? a.Ns : a.E) * one * kMxCodeBytes + g * one + col0 + m;
+      if (i == 0 || m >= 8)
+        L.sc = static_cast<const char*>(base) + (shared ? a.Ns : a.E) * one * kMxCodeBytes + g * one + col0 +
+               min(4 * (UP ? m & 7 : m), N - col0 - 4);
     }
     L.groups = (N - col0) / 16;
   } else {
@@ -778,7 +858,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
       const int t = shared ? id - a.R - g * a.T : id / a.K;
       return static_cast<const char*>(a.x) + (int64_t)t * a.H * B;
     } else {
-      return static_cast<const char*>(a.h) + (int64_t)id * a.I * B;
+      return static_cast<const char*>(a.h) + id * Ih * B;
     }
   };
 
@@ -800,8 +880,8 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
   } else if (col0 < N) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) L.act[nt] = row_values(ids[nt]);
-    if (NT > 1 && rows <= 16) product_loop<F, UP, NT, 1>(L, acc, begin + wave / CW, KW, end, q, Kd, N, plane);
-    else product_loop<F, UP, NT, NT>(L, acc, begin + wave / CW, KW, end, q, Kd, N, plane);
+    if (NT > 1 && rows <= 16) product_loop<F, UP, NT, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+    else product_loop<F, UP, NT, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
   }
 
   constexpr int RS = red_stride<F>();
@@ -837,13 +917,14 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
       const int64_t dst = row * N + tile * COLS + bc;
       if constexpr (UP) {
         const float hv = silu_f(s) * s3;
+        const int64_t place = row * Ih + (fmt_mx(F) ? mx_h_place(tile * COLS + bc) : tile * COLS + bc);
         if constexpr (fmt_f32(F)) {
-          static_cast<float*>(a.h)[dst] = hv;
+          static_cast<float*>(a.h)[place] = hv;
         } else {
           const uint32_t hi = f32_to_bf16(hv);
           uint16_t* hp = static_cast<uint16_t*>(a.h);
-          hp[dst] = (uint16_t)hi;
-          hp[RA * a.I + dst] = (uint16_t)f32_to_bf16(hv - bf16_to_f32(hi));
+          hp[place] = (uint16_t)hi;
+          hp[RA * Ih + place] = (uint16_t)f32_to_bf16(hv - bf16_to_f32(hi));
         }
       } else if constexpr (TAIL) {
         __hip_atomic_store(&a.y[(int64_t)slice * RA * N + dst], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -922,8 +1003,9 @@ hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t 
 
 template <int F>
 hipError_t launch_fmt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if (!p.head) {
-    decode_route_kernel<<<1, kRouteThreads, 0, st>>>(a, p.row_tile, p.entries);
+  if (!p.head || a.picked) {
+    if (p.head) decode_topk_kernel<<<(a.T + kWaves - 1) / kWaves, kThreads, 0, st>>>(a);
+    else decode_route_kernel<<<1, kRouteThreads, 0, st>>>(a, p.row_tile, p.entries);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -957,7 +1039,8 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
   DecodePlan p;
   p.row_tile = T <= 16 ? 16 : 32;
   const int64_t R = (int64_t)T * K;
-  p.head = R <= kThreads && T <= kHeadTokens;   // a pair for every thread of a block
+  p.head = R <= kListPairs;
+  p.picked = T > kHeadTokens || R > kThreads;
   p.tail = T <= kTailTokens;
   const int busy = (int)(R < E ? R : E);   // experts with rows, at most
   // an expert with c rows has at most 1 + (c - 1) / row_tile entries

@@ -25,7 +25,8 @@ constexpr int kMxCodeBytes = 16;
 // Where the down projection's partial sums are cut: S slices of `steps` k
 // steps each.
 struct DecodePlan {
-  bool head;        // the first product's blocks route for themselves
+  bool head;        // the first product's blocks list the work for themselves
+  bool picked;      // with head: the top-k has a launch of its own
   bool tail;        // the second product's last blocks add up the output
   int row_tile;     // rows of one entry at most (16 or 32)
   int entries;      // bound on the number of entries (expert x row tile)
@@ -58,8 +59,9 @@ struct DecodeArgs {
   int32_t* lists;      // [entries, row_tile] row ids
   int32_t* done;       // [n_done], kDoneStride apart: blocks of a column tile that have stored their sums
   int n_done;          // 0: the sum has a launch of its own
-  void* h;             // [RA, I]: f32, or two bf16 planes (value, then what it left)
+  void* h;             // [RA, I] (4 bit: rows of whole 128s): f32, or two bf16 planes (value, what it left)
   float* y;            // [slices, RA, H]
+  int picked;          // topk_idx and topk_w are written before the first product
 };
 hipError_t launch_decode(bool is_bf16, bool mx, const DecodeArgs& a, const DecodePlan& p, hipStream_t st);
 

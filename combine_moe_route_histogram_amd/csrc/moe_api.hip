@@ -335,7 +335,7 @@ DecodeLayout decode_layout(const moe_dims* d) {
   L.n_entries = off; off = align_up(off + 16);
   L.lists = off;     off = align_up(off + entries * a.row_tile * 4);
   L.done = off;      off = align_up(off + tiles * kDoneStride * 4);
-  L.h = off;         off = align_up(off + RA * d->I * 4);
+  L.h = off;         off = align_up(off + RA * (((size_t)d->I + 127) / 128 * 128) * 4);   // 4 bit: rows of whole 128s
   L.y = off;         off = align_up(off + slices * RA * d->H * 4);
   L.total = off;
   return L;
@@ -380,6 +380,7 @@ int decode(const moe_dims* d, bool mx, const float* logits, const void* x, const
   a.lists = ws_at<int32_t>(ws, L.lists);
   a.done = ws_at<int32_t>(ws, L.done);
   a.n_done = p.tail ? p.down_tiles : 0;
+  a.picked = p.picked;
   a.h = ws_at<char>(ws, L.h);
   a.y = ws_at<float>(ws, L.y);
   return hip_status(launch_decode(d->dtype == MOE_BF16, mx, a, p, as_stream(stream)), what);
