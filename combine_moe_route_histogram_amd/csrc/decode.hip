@@ -388,22 +388,28 @@ __device__ __forceinline__ void split_bf16(const float* f, u32x4* part) {
   }
 }
 
+// Rows of an entry at most.  4-bit weights with bf16 rows: up to 8 tokens the
+// two parts of a row are columns of one operand, and beyond that the rows go
+// through LDS; a kernel that holds the parts of 16 rows side by side would need
+// 146 registers, three waves on a SIMD in the place of four.  (The way a row is
+// summed must not depend on how many rows its expert has, so the choice is by
+// the number of tokens.)
+constexpr int row_tile_of(int f, int nt) { return f == kFmtMxBf16 && nt == 1 ? 8 : 16 * nt; }
+
 // bf16 parts of the row operand: x is bf16 already; h keeps two parts, so the
 // second product sees it to 16 bits instead of 8; float32 rows on 4-bit
 // weights keep all three.
 constexpr int act_parts(int f, bool up) { return f == kFmtMxF32 ? 3 : fmt_f32(f) ? 1 : up ? 1 : 2; }
-// 16-byte vectors of a lane's row operand per k step.
-constexpr int act_vecs(int f, bool up) {
-  return f == kFmtF32 ? 2 : f == kFmtMxF32 ? 8 : (fmt_mx(f) ? 4 : 1) * act_parts(f, up);
-}
+// 16-byte vectors of a lane's row operand per k step, with `parts` of them.
+constexpr int act_vecs(int f, int parts) { return f == kFmtF32 ? 2 : f == kFmtMxF32 ? 8 : (fmt_mx(f) ? 4 : 1) * parts; }
 
 // One k step of a wave in registers: the weights and the rows' values.
-template <int F, bool UP, int NT>
+template <int F, int P, int NT>
 struct Stage {
   static constexpr int kLoads = fmt_mx(F) ? fmt_groups(F) : 8;
   u32x4 w[kLoads];
   uint32_t s;   // 4 bit: the scales of 4 columns next to each other (see lane_scales)
-  u32x4 act[NT][act_vecs(F, UP)];
+  u32x4 act[NT][act_vecs(F, P)];
 };
 
 // A lane's place: its column(s) in row 0 of the matrix it reads, and its rows.
@@ -458,10 +464,10 @@ __device__ __forceinline__ int mx_h_place(int c) {
   return (c & ~127) | ((c >> 3) & 3) << 5 | ((c >> 5) & 3) << 3 | (c & 7);
 }
 
-template <int F, bool UP, int NT, int NTL>
-__device__ __forceinline__ void load_stage(Stage<F, UP, NTL>& s, const Lane<F, UP, NT>& L, int step, int q,
+template <int F, bool UP, int NT, int NTL, int P>
+__device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT>& L, int step, int q,
                                            int Kd, int N, int limit, int64_t plane) {
-  constexpr int V = act_vecs(F, UP), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
+  constexpr int V = act_vecs(F, P), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
   constexpr int PER = LEN * B / 16;   // vectors of a lane's values from one plane
   constexpr int V8 = 8 * B / 16;      // and of 8 values
   constexpr bool TURNS = fmt_mx(F) && !UP;   // h in the order of mx_h_place
@@ -516,8 +522,8 @@ __device__ __forceinline__ void mma_mx(const u32x4 (&w)[fmt_groups(F)], const fl
 }
 
 // acc[nt][j] += the step's weights (16 columns of group j) x rows (16 of tile nt).
-template <int F, bool UP, int NT, int NTL>
-__device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, int lane, f32x4 (&acc)[NT][fmt_groups(F)]) {
+template <int F, bool UP, int NT, int NTL, int P>
+__device__ __forceinline__ void mma_stage(const Stage<F, P, NTL>& s, int lane, f32x4 (&acc)[NT][fmt_groups(F)]) {
   if constexpr (F == kFmtBf16) {
     // A lane holds 8 columns of 8 rows; an operand wants 8 rows of one column:
     // halves of two rows' words are put together, one v_perm per two weights.
@@ -532,7 +538,7 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, int lane, 
 #pragma unroll
         for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
-          for (int p = 0; p < act_parts(F, UP); ++p)
+          for (int p = 0; p < P; ++p)
             acc[nt][2 * r + odd] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                 as_bf16x8(A), as_bf16x8(s.act[nt][p]), acc[nt][2 * r + odd], 0, 0, 0);
       }
@@ -547,7 +553,6 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, int lane, 
           acc[nt][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
               __uint_as_float(s.w[i][j]), __uint_as_float(s.act[nt][i >> 2][i & 3]), acc[nt][j], 0, 0, 0);
   } else {
-    constexpr int P = act_parts(F, UP);
     float sc[fmt_groups(F)];
     lane_scales<F, UP>(s.s, lane, sc);
 #pragma unroll
@@ -576,17 +581,17 @@ __device__ __forceinline__ void mma_stage(const Stage<F, UP, NTL>& s, int lane, 
 // with a step that counts as zeros, whose weights are its own last ones once
 // more.  (The barriers keep the scheduler from moving loads up, into registers
 // of their own.)
-template <int F, bool UP, int NT, int NTL>
+template <int F, bool UP, int NT, int NTL, int P = act_parts(F, UP)>
 __device__ __forceinline__ void product_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
                                              int stride, int end, int lane, int Kd, int N, int64_t plane) {
   const int q = lane >> 4;
-  Stage<F, UP, NTL> s0, s1;
-  auto load = [&](Stage<F, UP, NTL>& s, int k) {
-    load_stage<F, UP, NT, NTL>(s, L, k < end ? k : k - stride, q, Kd, N, k < end ? Kd : 0, plane);
+  Stage<F, P, NTL> s0, s1;
+  auto load = [&](Stage<F, P, NTL>& s, int k) {
+    load_stage<F, UP, NT, NTL, P>(s, L, k < end ? k : k - stride, q, Kd, N, k < end ? Kd : 0, plane);
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto mma = [&](Stage<F, UP, NTL>& s) {
-    mma_stage<F, UP, NT, NTL>(s, lane, acc);
+  auto mma = [&](Stage<F, P, NTL>& s) {
+    mma_stage<F, UP, NT, NTL, P>(s, lane, acc);
     __builtin_amdgcn_sched_barrier(0);
   };
   if (first >= end) return;
@@ -782,11 +787,12 @@ __device__ __forceinline__ void pin_args(const DecodeArgs& a) {
 // counts itself; whoever counts last reads them all.  Nobody waits for
 // anybody.  The first product's first block clears the counters.
 template <int F, bool UP, int NT, int CW, bool FUSED>
-__global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decode_ffn_kernel(DecodeArgs a, int slices, int slice_steps) {
+__global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void decode_ffn_kernel(DecodeArgs a, int slices, int slice_steps) {
   constexpr bool HEAD = UP && FUSED, TAIL = !UP && FUSED;
   constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, KW = kWaves / CW;
   constexpr int WCOLS = UP ? 8 * G : 16 * G, COLS = WCOLS * CW;   // columns of a wave, of the block
   constexpr bool SHARED = fmt_mx(F) && NT == 2;   // rows' values by way of LDS
+  constexpr int RT = row_tile_of(F, NT);           // rows of an entry at most
   constexpr int kRedFloats = kWaves * kRedRows * red_stride<F>();
   constexpr int kActFloats = SHARED ? act_bytes<F, UP, NT>() / 2 : 0;
   constexpr int kRouteFloats = HEAD ? (sizeof(BlockRoute) + 15) / 16 * 4 : 0;
@@ -809,14 +815,14 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
     for (int i = tid; i < a.n_done; i += kThreads) a.done[i * kDoneStride] = 0;
   if constexpr (HEAD) {
     BlockRoute& r = *reinterpret_cast<BlockRoute*>(red);
-    if (!block_route(a, r, entry, blockIdx.x == 0, blockIdx.x == 0 && entry == 0, 16 * NT, tid, group, rows)) return;
+    if (!block_route(a, r, entry, blockIdx.x == 0, blockIdx.x == 0 && entry == 0, RT, tid, group, rows)) return;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) ids[nt] = r.list[min(16 * nt + m, rows - 1)];
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = r.list[min((16 * nt + m) % RT, rows - 1)];
     __syncthreads();   // the list is read; its LDS becomes the sums'
   } else {
     const int2 en = a.entries[entry];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) ids[nt] = a.lists[(int64_t)entry * (16 * NT) + 16 * nt + m];
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = a.lists[(int64_t)entry * RT + (16 * nt + m) % RT];
     group = en.x;
     rows = en.y;
 #pragma unroll
@@ -826,7 +832,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
     // inside it, lane 0 would be switched off.)
     const int id0 = __builtin_amdgcn_readfirstlane(ids[0]);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) ids[nt] = 16 * nt + m < rows ? ids[nt] : id0;
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = (16 * nt + m) % RT < rows ? ids[nt] : id0;
   }
   group = __builtin_amdgcn_readfirstlane(group);
   rows = __builtin_amdgcn_readfirstlane(rows);
@@ -880,8 +886,22 @@ __global__ __launch_bounds__(kThreads, NT == 1 && !fmt_mx(F) ? 4 : 2) void decod
   } else if (col0 < N) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) L.act[nt] = row_values(ids[nt]);
-    if (NT > 1 && rows <= 16) product_loop<F, UP, NT, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
-    else product_loop<F, UP, NT, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+    if constexpr (RT == 8) {
+      // The second part of row n is column n + 8 of the operand, in the place
+      // of a second product.  (Lanes n and n + 8 have the same row.)
+      if (!UP && m >= 8) L.act[0] += plane;
+      product_loop<F, UP, NT, 1, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      if constexpr (!UP) {
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[0][j][i] += __shfl_xor(acc[0][j][i], 8, 16);
+      }
+    } else if (NT > 1 && rows <= 16) {
+      product_loop<F, UP, NT, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+    } else {
+      product_loop<F, UP, NT, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+    }
   }
 
   constexpr int RS = red_stride<F>();
@@ -998,7 +1018,7 @@ hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t 
 }
 template <int F, bool UP>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  return p.row_tile == 16 ? launch_product<F, UP, 1>(a, p, st) : launch_product<F, UP, 2>(a, p, st);
+  return p.row_tile < 32 ? launch_product<F, UP, 1>(a, p, st) : launch_product<F, UP, 2>(a, p, st);
 }
 
 template <int F>
@@ -1037,7 +1057,7 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
   const int f = mx ? (is_bf16 ? kFmtMxBf16 : kFmtMxF32) : (is_bf16 ? kFmtBf16 : kFmtF32);
   const int tile = 16 * fmt_groups(f), step = fmt_step(f), size = is_bf16 ? 2 : 4;
   DecodePlan p;
-  p.row_tile = T <= 16 ? 16 : 32;
+  p.row_tile = T <= row_tile_of(f, 1) ? row_tile_of(f, 1) : row_tile_of(f, 2);
   const int64_t R = (int64_t)T * K;
   p.head = R <= kListPairs;
   p.picked = T > kHeadTokens || R > kThreads;

@@ -327,13 +327,14 @@ DecodeLayout decode_layout(const moe_dims* d) {
   const DecodePlan a = decode_plan_for(d, false), b = mx_ok ? decode_plan_for(d, true) : a;
   const size_t R = (size_t)d->T * d->K, RA = R + (size_t)d->n_shared * d->T;
   const size_t entries = a.entries > b.entries ? a.entries : b.entries;
+  const size_t la = (size_t)a.entries * a.row_tile, lb = (size_t)b.entries * b.row_tile, lists = la > lb ? la : lb;
   const size_t tiles = a.down_tiles > b.down_tiles ? a.down_tiles : b.down_tiles;
   const size_t slices = a.slices > b.slices ? a.slices : b.slices;
   DecodeLayout L;
   size_t off = 0;
   L.entries = off;   off = align_up(off + entries * 8);
   L.n_entries = off; off = align_up(off + 16);
-  L.lists = off;     off = align_up(off + entries * a.row_tile * 4);
+  L.lists = off;     off = align_up(off + lists * 4);
   L.done = off;      off = align_up(off + tiles * kDoneStride * 4);
   L.h = off;         off = align_up(off + RA * (((size_t)d->I + 127) / 128 * 128) * 4);   // 4 bit: rows of whole 128s
   L.y = off;         off = align_up(off + slices * RA * d->H * 4);
