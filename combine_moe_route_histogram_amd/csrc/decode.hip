@@ -22,10 +22,10 @@ constexpr int kWaves = 4;               // waves of a product block
 constexpr int kThreads = kWaves * kWave;
 constexpr int kRedRows = 8;             // rows whose sums go through LDS at once
 constexpr int kRouteThreads = 1024;
-constexpr int kHeadTokens = 16;         // top-k inside the first product's blocks up to here
+constexpr int kHeadTokens = 4;          // top-k inside the first product's blocks up to here
 constexpr int kTailTokens = 4;          // the output's sum inside the second product up to here
 constexpr int64_t kLongRow = 4096;      // bytes
-constexpr double kFillBlocks = 220;
+constexpr double kFillBlocks = 220, kManyBlocks = 512;
 constexpr double kSliceBlocks = 400;    // the down projection is cut along k for so many blocks,
 constexpr int kMaxSlices = 8;           // into so many slices at most
 
@@ -239,6 +239,7 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
   const int lane = tid & (kWave - 1), wave = tid / kWave;
   const int E = a.E, K = a.K;
   int mine[kListRounds];   // the expert of pair tid + 256 i
+  const int rounds = a.picked ? (a.R + kThreads - 1) / kThreads : 1;
   if (a.picked) {
 #pragma unroll
     for (int i = 0; i < kListRounds; ++i) {
@@ -281,6 +282,7 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
   }
 #pragma unroll
   for (int i = 0; i < kListRounds; ++i) {
+    if (i >= rounds) break;
     if (tid + i * kThreads >= pairs) mine[i] = -1;
     if (mine[i] >= 0) atomicAdd(&r.count[mine[i]], 1);
   }
@@ -331,11 +333,12 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
     uint64_t mask[kListRounds];
 #pragma unroll
     for (int i = 0; i < kListRounds; ++i) {
+      if (i >= rounds) break;
       mask[i] = __ballot(mine[i] == e);
       if (lane == 0) r.below[i * kWaves + wave] = __popcll(mask[i]);
     }
     __syncthreads();
-    int sum = lane < kListRounds * kWaves ? r.below[lane] : 0;   // up to and with a wave's share
+    int sum = lane < rounds * kWaves ? r.below[lane] : 0;   // up to and with a wave's share
 #pragma unroll
     for (int o = 1; o < kListRounds * kWaves; o <<= 1) {
       const int v = __shfl_up(sum, o, kWave);
@@ -343,6 +346,7 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
     }
 #pragma unroll
     for (int i = 0; i < kListRounds; ++i) {
+      if (i >= rounds) break;
       const int at = i * kWaves + __builtin_amdgcn_readfirstlane(wave);
       const int base = __builtin_amdgcn_readlane(sum, at) - __popcll(mask[i]) - part * row_tile;
       const int rank = base + __popcll(mask[i] & ((1ull << lane) - 1));
@@ -365,8 +369,8 @@ __device__ __forceinline__ bool block_route(const DecodeArgs& a, BlockRoute& r, 
 // ----------------------------------------------------------------- products
 
 __device__ __forceinline__ bf16x8 as_bf16x8(const u32x4& v) { return __builtin_bit_cast(bf16x8, v); }
-__device__ __forceinline__ u32x4 ld16_stream(const void* p) {
-  return __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+__device__ __forceinline__ u32x4 ld16_stream(uint64_t address) {
+  return __builtin_nontemporal_load(reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(address));
 }
 
 // x = hi + lo (+ lo2), each part a bf16: what a rounding leaves is exact in
@@ -403,6 +407,11 @@ constexpr int act_parts(int f, bool up) { return f == kFmtMxF32 ? 3 : fmt_f32(f)
 // 16-byte vectors of a lane's row operand per k step, with `parts` of them.
 constexpr int act_vecs(int f, int parts) { return f == kFmtF32 ? 2 : f == kFmtMxF32 ? 8 : (fmt_mx(f) ? 4 : 1) * parts; }
 
+// Steps in flight a wave.  (Four, with two waves on a SIMD in the place of
+// four: 4-bit fine layer T=1 19.3 us against 17.8, wide bf16 T=32 441 against
+// 436.)
+constexpr int kStages = 2;
+
 // One k step of a wave in registers: the weights and the rows' values.
 template <int F, int P, int NT>
 struct Stage {
@@ -424,7 +433,7 @@ struct Lane {
 
 // What lanes behind the matrix's end, or behind the wave's last step, take for
 // their rows' values.
-__device__ const u32x4 kZeros[32] = {};
+__device__ const u32x4 kZeros[64] = {};
 // A load of one of two places (a choice of pointers would make it a flat load,
 // which waits for everything).
 __device__ __forceinline__ u32x4 ld16_global(uint64_t address) {
@@ -438,21 +447,28 @@ __device__ __forceinline__ u32x4 ld16_global(uint64_t address) {
 // zeros.
 constexpr int step_len(int f) { return fmt_mx(f) ? kMxGroup : 8; }   // a lane's rows in one k step
 template <int F, bool UP, int NT, class S>
-__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int step, int q, int Kd, int N) {
+__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int step, int q, int Kd, int N,
+                                             bool real = true) {
   const int k = min(fmt_step(F) * step + step_len(F) * q, Kd - step_len(F));
+  const uint64_t zeros = reinterpret_cast<uint64_t>(kZeros);
   if constexpr (fmt_mx(F)) {
     const int64_t at = (int64_t)(k / kMxGroup) * N;
+    uint64_t p[UP ? 2 : 1];
+#pragma unroll
+    for (int i = 0; i < (UP ? 2 : 1); ++i) p[i] = real ? reinterpret_cast<uint64_t>(L.w[i]) + at * kMxCodeBytes : zeros;
 #pragma unroll
     for (int j = 0; j < fmt_groups(F); ++j) {
-      const int i = UP ? j & 1 : 0, jj = min(UP ? j >> 1 : j, L.groups - 1);
-      s.w[j] = ld16_stream(L.w[i] + at * kMxCodeBytes + jj * 16 * kMxCodeBytes);
+      const int jj = min(UP ? j >> 1 : j, L.groups - 1);
+      s.w[j] = ld16_stream(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes);
     }
-    s.s = *reinterpret_cast<const uint32_t*>(L.sc + at);
+    const uint64_t sc = real ? reinterpret_cast<uint64_t>(L.sc) + at : zeros;
+    s.s = *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(sc);
   } else {
     constexpr int B = fmt_f32(F) ? 4 : 2;
-    const char* p = L.w[0] + (int64_t)k * N * B;
+    const uint64_t p = real ? reinterpret_cast<uint64_t>(L.w[0]) + (int64_t)k * N * B : zeros;
+    const int64_t row = real ? (int64_t)N * B : 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s.w[i] = ld16_stream(p + (int64_t)i * N * B);
+    for (int i = 0; i < 8; ++i) s.w[i] = ld16_stream(p + i * row);
   }
 }
 
@@ -466,19 +482,19 @@ __device__ __forceinline__ int mx_h_place(int c) {
 
 template <int F, bool UP, int NT, int NTL, int P>
 __device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT>& L, int step, int q,
-                                           int Kd, int N, int limit, int64_t plane) {
+                                           int Kd, int N, bool real, int64_t plane) {
   constexpr int V = act_vecs(F, P), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
   constexpr int PER = LEN * B / 16;   // vectors of a lane's values from one plane
   constexpr int V8 = 8 * B / 16;      // and of 8 values
   constexpr bool TURNS = fmt_mx(F) && !UP;   // h in the order of mx_h_place
-  load_weights<F, UP, NT>(s, L, step, q, Kd, N);
+  load_weights<F, UP, NT>(s, L, step, q, Kd, N, real);
   const int at = fmt_step(F) * step + LEN * q, k = TURNS ? fmt_step(F) * step + 8 * q : at;
 #pragma unroll
   for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
     for (int v0 = 0; v0 < V; v0 += PER) {
       const uint64_t p = reinterpret_cast<uint64_t>(L.act[nt]) + (int64_t)k * B + v0 / PER * plane;
-      const uint64_t from = at < limit ? p : reinterpret_cast<uint64_t>(kZeros);
+      const uint64_t from = real && at < Kd ? p : reinterpret_cast<uint64_t>(kZeros);
 #pragma unroll
       for (int v = 0; v < PER; ++v)
         s.act[nt][v0 + v] = ld16_global(from + (TURNS ? v / V8 * 32 * B + v % V8 * 16 : v * 16));
@@ -575,37 +591,39 @@ __device__ __forceinline__ void mma_stage(const Stage<F, P, NTL>& s, int lane, f
   }
 }
 
-// A wave's k steps first, first + stride, ... below end.  Two steps are in
-// flight; a step's loads follow the products of the one before its
-// predecessor, so every wait is for the older of the two.  An odd count ends
-// with a step that counts as zeros, whose weights are its own last ones once
-// more.  (The barriers keep the scheduler from moving loads up, into registers
-// of their own.)
+// A wave's k steps first, first + stride, ... below end.  kStages steps are in
+// flight; a step's loads follow the products of the one whose registers it
+// takes, so every wait is for the oldest.  The count is filled up with steps
+// that load zeros from one place.  (The barriers keep the scheduler from
+// moving loads up, into registers of their own.)
 template <int F, bool UP, int NT, int NTL, int P = act_parts(F, UP)>
 __device__ __forceinline__ void product_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
                                              int stride, int end, int lane, int Kd, int N, int64_t plane) {
+  constexpr int S = kStages;
   const int q = lane >> 4;
-  Stage<F, P, NTL> s0, s1;
-  auto load = [&](Stage<F, P, NTL>& s, int k) {
-    load_stage<F, UP, NT, NTL, P>(s, L, k < end ? k : k - stride, q, Kd, N, k < end ? Kd : 0, plane);
+  Stage<F, P, NTL> s[S];
+  auto load = [&](Stage<F, P, NTL>& st, int k) {
+    load_stage<F, UP, NT, NTL, P>(st, L, k, q, Kd, N, k < end, plane);
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto mma = [&](Stage<F, P, NTL>& s) {
-    mma_stage<F, UP, NT, NTL, P>(s, lane, acc);
+  auto mma = [&](Stage<F, P, NTL>& st) {
+    mma_stage<F, UP, NT, NTL, P>(st, lane, acc);
     __builtin_amdgcn_sched_barrier(0);
   };
   if (first >= end) return;
-  load(s0, first);
-  load(s1, first + stride);
-  mma(s0);
+#pragma unroll
+  for (int i = 0; i < S; ++i) load(s[i], first + i * stride);
+  mma(s[0]);
 #pragma unroll 1
-  for (int k = first + 2 * stride; k < end; k += 2 * stride) {
-    load(s0, k);
-    mma(s1);
-    load(s1, k + stride);
-    mma(s0);
+  for (int k = first + S * stride; k < end; k += S * stride) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      load(s[i], k + i * stride);
+      mma(s[(i + 1) % S]);
+    }
   }
-  mma(s1);
+#pragma unroll
+  for (int i = 1; i < S; ++i) mma(s[i]);
 }
 
 // 4-bit weights, more than 16 rows: the rows' values are the larger half of
@@ -1042,14 +1060,16 @@ hipError_t launch_fmt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) 
 // the matrix is long, pieces of it that are read at the same time and are far
 // apart use few of the memory's channels, so the block reads as wide a piece as
 // leaves kFillBlocks blocks (bf16 [4096, 14336] x 2, 32 tokens: 1, 2, 4 tiles
-// 503, 476, 454 us a call; one token: 140, 127, 155).  Short rows want more
-// blocks instead ([2048, 1408] x 2, 16 tokens: 159, 166, 185 us).
-// 4-bit rows are long ones, and their waves work side by side on the same rows'
-// values where those go through LDS.
+// 507, 465, 437 us a call; one token: 136, 123, 146).  Short rows want more
+// blocks ([2048, 1408] x 2, 1 and 2 tiles: 16 tokens of 4 in 32 experts 95 and
+// 102 us, of 6 in 64 experts 167 and 165, 32 tokens 203 and 194).  4-bit rows
+// are long ones, and their waves work side by side on the same rows' values
+// where those go through LDS.
 static int tile_width(bool mx, int row_tile, int64_t row_bytes, int columns, int tile, double groups_and_slices) {
   if (mx && row_tile == 32) return 4;
-  for (int w = mx ? 2 : row_bytes >= 2 * kLongRow ? 4 : row_bytes >= kLongRow ? 2 : 1; w > 1; w /= 2)
-    if ((columns + w * tile - 1) / (w * tile) * groups_and_slices >= kFillBlocks) return w;
+  const bool short_row = !mx && row_bytes < kLongRow;
+  for (int w = !mx && row_bytes >= 2 * kLongRow ? 4 : 2; w > 1; w /= 2)
+    if ((columns + w * tile - 1) / (w * tile) * groups_and_slices >= (short_row ? kManyBlocks : kFillBlocks)) return w;
   return 1;
 }
 
