@@ -444,9 +444,15 @@ def _launch(name, stream, head, tensors, tail):
     dtype, elements).  Tensors of another device than the one the work runs on are refused: a
     kernel would read memory that its device may not reach."""
     index = stream.device_index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device()
-    args = [_ptr(*t) for t in tensors]
-    for t, arg_name, _, _ in tensors:
-        if t is not None and t.get_device() != index:
+    args = []
+    for t, arg_name, dtype, numel in tensors:
+        if t is None:
+            args.append(None)
+        elif (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype
+              and t.is_contiguous() and t.numel() >= numel):
+            args.append(t.data_ptr())
+        else:   # says what is wrong
+            _ptr(t, arg_name, dtype, numel)
             raise ValueError(f"{arg_name} is on {t.device}, the call runs on cuda:{index}")
     _call(name, *head, *args, *tail, _stream(stream))
 
@@ -458,7 +464,7 @@ def _decode(name, d, dt, n, ns, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, 
             ((logits, "logits", f32, T * d.E), (x, "x", act, T * H), (w1, "w1", dt, n), (w3, "w3", dt, n),
              (w2, "w2", dt, n), (ws1, "ws1", dt, ns), (ws3, "ws3", dt, ns), (ws2, "ws2", dt, ns),
              (n_tokens, "n_tokens", i32, 1), (topk_idx, "topk_idx", i32, T * K), (topk_w, "topk_w", f32, T * K),
-             (out, "out", act, T * H), (ws, "ws", torch.uint8, None)), (0 if ws is None else ws.numel(),))
+             (out, "out", act, T * H), (ws, "ws", torch.uint8, 0)), (0 if ws is None else ws.numel(),))
 
 
 def moe_decode(d: Dims, logits, x, w1, w3, w2, ws1, ws3, ws2, n_tokens, topk_idx, topk_w, out, ws,
@@ -485,20 +491,22 @@ def moe_mx_bytes(G: int, K: int, N: int) -> int:
 
 
 def _mx_dtype(w):
-    """MOE_F32 or MOE_BF16 of a weight tensor (None: bf16, the call reports the NULL)."""
+    """MOE_F32 or MOE_BF16 of a weight tensor, and its torch type (None: bf16, the call reports the NULL)."""
     if w is None:
-        return BF16
+        return BF16, None
     for code, dt in _TORCH_DTYPE.items():
-        if w.dtype == dt:
-            return code
+        if w.dtype is dt:
+            return code, dt
     raise TypeError(f"w must be {torch.float32} or {torch.bfloat16} (got {w.dtype})")
 
 
 def moe_mx_quantize(G: int, K: int, N: int, w, mx, stream=None):
-    _launch("moe_mx_quantize", stream, (G, K, N, _mx_dtype(w)),
-            ((w, "w", None, G * K * N), (mx, "mx", torch.uint8, _mx_numel(G, K, N))), ())
+    code, dt = _mx_dtype(w)
+    _launch("moe_mx_quantize", stream, (G, K, N, code),
+            ((w, "w", dt, G * K * N), (mx, "mx", torch.uint8, _mx_numel(G, K, N))), ())
 
 
 def moe_mx_dequantize(G: int, K: int, N: int, mx, w, stream=None):
-    _launch("moe_mx_dequantize", stream, (G, K, N, _mx_dtype(w)),
-            ((mx, "mx", torch.uint8, _mx_numel(G, K, N)), (w, "w", None, G * K * N)), ())
+    code, dt = _mx_dtype(w)
+    _launch("moe_mx_dequantize", stream, (G, K, N, code),
+            ((mx, "mx", torch.uint8, _mx_numel(G, K, N)), (w, "w", dt, G * K * N)), ())

@@ -95,25 +95,44 @@ def test_mx_bytes():
 
 
 def test_a_tensor_of_another_device_is_refused(monkeypatch):
-    """One process drives one GPU: a tensor of another one is named, not launched on."""
+    """One process drives one GPU: a tensor of another one is named, not launched on.  (Tensors of
+    two devices cannot be had here: a CPU tensor that says it is on a GPU stands for each.)"""
     import torch
 
-    class Fake:
-        def __init__(self, i):
-            self.i, self.device = i, torch.device("cuda", i)
-
+    class On(torch.Tensor):
         def get_device(self):
-            return self.i
+            return self.index
+
+        @property
+        def device(self):
+            return torch.device("cuda", self.index)
+
+        @property
+        def is_cuda(self):
+            return True
+
+    def on(index):
+        t = torch.zeros(4).as_subclass(On)
+        t.index = index
+        return t
     called = []
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(M, "_ptr", lambda t, name, dtype, numel: None)
     monkeypatch.setattr(M, "_stream", lambda stream: None)
-    monkeypatch.setattr(M, "_call", lambda name, *args: called.append(name))
-    M._launch("moe_decode", None, (), ((Fake(0), "x", None, 1), (None, "ws1", None, 1)), ())
-    assert called == ["moe_decode"]
+    monkeypatch.setattr(M, "_call", lambda name, *args: called.append((name, args)))
+    f32 = torch.float32
+    M._launch("moe_decode", None, (7,), ((on(0), "x", f32, 4), (None, "ws1", f32, 4)), (9,))
+    assert len(called) == 1 and called[0][1][0] == 7 and called[0][1][2:] == (None, 9, None)
     with pytest.raises(ValueError, match="out is on cuda:1, the call runs on cuda:0"):
-        M._launch("moe_decode", None, (), ((Fake(0), "x", None, 1), (Fake(1), "out", None, 1)), ())
-    assert called == ["moe_decode"]
+        M._launch("moe_decode", None, (), ((on(0), "x", f32, 4), (on(1), "out", f32, 4)), ())
+    with pytest.raises(ValueError, match="x has 4 elements, needs 5"):
+        M._launch("moe_decode", None, (), ((on(0), "x", f32, 5),), ())
+    with pytest.raises(ValueError, match="x must be a GPU tensor"):
+        M._launch("moe_decode", None, (), ((torch.zeros(4), "x", f32, 4),), ())
+    with pytest.raises(TypeError, match="x must be"):
+        M._launch("moe_decode", None, (), ((on(0), "x", torch.int32, 4),), ())
+    with pytest.raises(TypeError, match="must be a torch.Tensor"):
+        M._launch("moe_decode", None, (), (([1.0], "x", f32, 1),), ())
+    assert len(called) == 1
 
 
 def test_mx_oracle_hand_worked():

@@ -61,6 +61,21 @@ def test_quantize_and_back_bit_exact(G, K, N, dtype):
     assert np.array_equal(host(back.float()).astype(np.float64), D.mx_values(code, s))
 
 
+def test_quantize_smallest_numbers():
+    """Groups whose largest magnitude is near or below the smallest normal float32: the scale stays
+    2^-126, and the codes follow it."""
+    w = np.zeros((1, 32, 8), np.float32)
+    for c, big in enumerate([2.0 ** -126, 1.5 * 2.0 ** -126, 2.0 ** -125, 2.0 ** -124, 5 * 2.0 ** -126, 2.0 ** -123]):
+        w[0, :, c] = big * np.linspace(-1, 1, 32)
+        w[0, 0, c] = big
+        w[0, np.abs(w[0, :, c]) < 2.0 ** -126, c] = 0.0      # normal numbers and zeros
+    code, s = D.mx_quantize(w.astype(np.float64))
+    mx = torch.empty(M.moe_mx_bytes(1, 32, 8), dtype=torch.uint8, device="cuda")
+    M.moe_mx_quantize(1, 32, 8, dev(w), mx)
+    torch.cuda.synchronize()
+    assert np.array_equal(mx.cpu().numpy(), D.mx_pack(code, s))
+
+
 def test_dequantize_takes_every_code_and_scale():
     """All 16 codes under scale bytes 1..252 (253 and 254 put the largest codes beyond float32)."""
     G, K, N = 1, 32 * 63, 8
@@ -94,6 +109,10 @@ SHAPES = [
     (256, 64, 3, 1, 96, 0),
     (256, 32, 256, 256, 32, 0),
     (255, 416, 16, 4, 736, 1),
+    (3, 64, 200, 5, 96, 1),
+    (8, 4096, 3, 1, 64, 1),
+    (9, 128, 4, 2, 4224, 0),
+    (7, 2080, 5, 2, 544, 2),
 ]
 ODD = [  # dims that are multiples of 8 only: the plain weights
     (1, 8, 1, 1, 8, 0),
@@ -185,19 +204,23 @@ def test_routing_has_the_bits_of_moe_route(T, E, K):
     assert np.array_equal(host(b.topk_w).view(np.uint32), host(ref.topk_w).view(np.uint32))
 
 
+PADDED = [((20, 96, 6, 2, 160, 1), used) for used in (0, 1, 5, 19, 20, 21, -3)]
+PADDED += [((1, 64, 8, 2, 64, 1), 0), ((1, 64, 8, 2, 64, 1), 1), ((3, 64, 8, 2, 64, 1), 2),
+           ((8, 64, 200, 5, 64, 2), 7), ((200, 64, 40, 20, 64, 1), 90), ((200, 64, 40, 20, 64, 1), 0)]
+
+
 @pytest.mark.parametrize("mx", [False, True], ids=["plain", "mx"])
-@pytest.mark.parametrize("used", [0, 1, 5, 19, 20, 21, -3])
+@pytest.mark.parametrize("shape,used", PADDED, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else str(v))
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_padded_batch(used, dtype, mx):
-    """Rows behind n_tokens are not read (they hold NaN here) and stay as they were; the rows in
+def test_padded_batch(shape, used, dtype, mx):
+    """Rows behind n_tokens have no effect (they hold NaN here) and stay as they were; the rows in
     use have the bits of the full call's."""
-    shape = (20, 96, 6, 2, 160, 1)
-    print(f"case padded used={used} {dtype} mx={mx}", flush=True)
+    print(f"case padded {shape} used={used} {dtype} mx={mx}", flush=True)
     inp = _inputs(shape, dtype)
     p = _packed_inputs(inp, dtype)[0] if mx else device_inputs(inp)
     full = _buffers(shape, dtype)
     L.decode(full, p)
-    n = min(max(used, 0), 20)
+    n = min(max(used, 0), shape[0])
     q = dict(p, n_tokens=torch.tensor([used], dtype=torch.int32, device="cuda"))
     q["x"], q["logits"] = p["x"].clone(), p["logits"].clone()
     q["x"][n:] = float("nan")
@@ -226,6 +249,40 @@ def test_all_tokens_on_the_same_experts(dtype, mx):
     torch.cuda.synchronize()
     assert (host(b.topk_idx) == [4, 11]).all()
     _check(b, D.decode(inp, 2, dtype, values), 150, dtype)
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["plain", "mx"])
+def test_offsets_beyond_32_bits(mx):
+    """Weights of more than 2^32 bytes: the last expert's result has the bits of a layer that holds
+    it alone."""
+    E, H, I = (70, 4096, 16384) if mx else (36, 4096, 16384)
+    print(f"case large E={E} H={H} I={I} mx={mx}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    if mx:
+        one = H * I // 32
+        make = lambda: torch.cat([torch.randint(0, 256, (16 * one * E,), generator=gen, device="cuda", dtype=torch.uint8),
+                                  torch.randint(116, 120, (one * E,), generator=gen, device="cuda", dtype=torch.uint8)])
+        last = lambda w: torch.cat([w[16 * one * (E - 1):16 * one * E], w[16 * one * E + one * (E - 1):]])
+    else:
+        make = lambda: torch.randn(E, H, I, generator=gen, device="cuda", dtype=torch.bfloat16) * 0.02
+        last = lambda w: w[E - 1:].contiguous()
+    p = {n: make() for n in ("w1", "w3")}
+    p["w2"] = make() if mx else make().view(E, I, H)
+    assert p["w1"].numel() * p["w1"].element_size() > 2 ** (31 if mx else 32)
+    p["x"] = torch.randn(2, H, generator=gen, device="cuda", dtype=torch.bfloat16)
+    p["logits"] = torch.zeros(2, E, device="cuda")
+    p["logits"][:, E - 1] = 1.0
+    b = L.DecodeBuffers(L.make_dims(2, H, E, 1, I, 0, "bf16"))
+    L.decode(b, p)
+    q = {n: last(p[n]) for n in ("w1", "w3", "w2")}
+    q["x"], q["logits"] = p["x"], p["logits"][:, E - 1:].contiguous()
+    c = L.DecodeBuffers(L.make_dims(2, H, 1, 1, I, 0, "bf16"))
+    L.decode(c, q)
+    torch.cuda.synchronize()
+    assert (host(b.topk_idx) == E - 1).all()
+    # the two layers may cut the down projection differently: float32 sums of I products
+    a, r = b.out.float(), c.out.float()
+    assert r.abs().max() > 0.1 and (a - r).abs().max() <= 2.0 ** -7 * r.abs().max()
 
 
 @pytest.mark.parametrize("mx", [False, True], ids=["plain", "mx"])
