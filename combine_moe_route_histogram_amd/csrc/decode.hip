@@ -227,10 +227,12 @@ __global__ __launch_bounds__(kThreads) void decode_topk_kernel(DecodeArgs a) {
 // 17 us).  Writes what the second product and the caller need: the entry and
 // its rows by the blocks of column tile 0, the picks by the very first block.
 constexpr int kListRounds = 8, kListPairs = kListRounds * kThreads;   // pairs a block can list
+constexpr int kMaxRowTile = 64;
+constexpr int kXcds = 8;   // blocks that follow each other go to the chiplets in turn
 struct BlockRoute {
   int32_t idx[kThreads];   // picks and weights made here: at most a pair a thread
   float w[kThreads];
-  int32_t list[32];
+  int32_t list[kMaxRowTile];
   int32_t count[kMaxExperts];
   int32_t below[kListRounds * kWaves];
 };
@@ -398,6 +400,18 @@ __device__ __forceinline__ void split_bf16(const float* f, u32x4* part) {
 // 146 registers, three waves on a SIMD in the place of four.  (The way a row is
 // summed must not depend on how many rows its expert has, so the choice is by
 // the number of tokens.)
+//
+// Where the experts have kManyRows rows each or more, on average, an entry of
+// the formats without scales holds 64: the weights are read half as often, and
+// through the caches, since other entries of the expert read them too.  (us a
+// call with entries of 32, read past the caches, and of 64.  bf16 [4096, 14336]
+// x 2 in 8 experts, 24, 32 and 64 rows each: 519 and 655, 773 and 677, 1256 and
+// 898; [2048, 1408] x 4 in 32, 8 and 32 rows: 104 and 129, 179 and 153.  f32
+// [4096, 14336] x 2 in 4, 24, 32, 48, 64 and 128 rows: 814 and 825, 1314 and
+// 996, 1706 and 1370, 2016 and 2064, 3854 and 3293.)  The two bf16 parts of 64
+// rows do not fit into the registers: there two blocks next to each other on
+// one chiplet take 32 of an entry's rows each.
+constexpr int kManyRows = 32;
 constexpr int row_tile_of(int f, int nt) { return f == kFmtMxBf16 && nt == 1 ? 8 : 16 * nt; }
 
 // bf16 parts of the row operand: x is bf16 already; h keeps two parts, so the
@@ -423,7 +437,7 @@ struct Stage {
 
 // A lane's place: its column(s) in row 0 of the matrix it reads, and its rows.
 // Lanes without a column or a row of their own repeat a valid one.
-template <int F, bool UP, int NT>
+template <int F, bool UP, int NT, bool MANY>
 struct Lane {
   const char* w[fmt_mx(F) && UP ? 2 : 1];   // 4 bit: in W1 and W3 (up) or in W2
   const char* sc;                           // 4 bit: this lane's 4 scales in row 0
@@ -446,8 +460,8 @@ __device__ __forceinline__ u32x4 ld16_global(uint64_t address) {
 // comes of such columns is not stored, and rows at or behind `limit` meet
 // zeros.
 constexpr int step_len(int f) { return fmt_mx(f) ? kMxGroup : 8; }   // a lane's rows in one k step
-template <int F, bool UP, int NT, class S>
-__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int step, int q, int Kd, int N,
+template <int F, bool UP, int NT, bool MANY, class S>
+__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT, MANY>& L, int step, int q, int Kd, int N,
                                              bool real = true) {
   const int k = min(fmt_step(F) * step + step_len(F) * q, Kd - step_len(F));
   const uint64_t zeros = reinterpret_cast<uint64_t>(kZeros);
@@ -468,7 +482,7 @@ __device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int
     const uint64_t p = real ? reinterpret_cast<uint64_t>(L.w[0]) + (int64_t)k * N * B : zeros;
     const int64_t row = real ? (int64_t)N * B : 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s.w[i] = ld16_stream(p + i * row);
+    for (int i = 0; i < 8; ++i) s.w[i] = MANY ? ld16_global(p + i * row) : ld16_stream(p + i * row);
   }
 }
 
@@ -480,14 +494,14 @@ __device__ __forceinline__ int mx_h_place(int c) {
   return (c & ~127) | ((c >> 3) & 3) << 5 | ((c >> 5) & 3) << 3 | (c & 7);
 }
 
-template <int F, bool UP, int NT, int NTL, int P>
-__device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT>& L, int step, int q,
+template <int F, bool UP, int NT, bool MANY, int NTL, int P>
+__device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT, MANY>& L, int step, int q,
                                            int Kd, int N, bool real, int64_t plane) {
   constexpr int V = act_vecs(F, P), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
   constexpr int PER = LEN * B / 16;   // vectors of a lane's values from one plane
   constexpr int V8 = 8 * B / 16;      // and of 8 values
   constexpr bool TURNS = fmt_mx(F) && !UP;   // h in the order of mx_h_place
-  load_weights<F, UP, NT>(s, L, step, q, Kd, N, real);
+  load_weights<F, UP, NT, MANY>(s, L, step, q, Kd, N, real);
   const int at = fmt_step(F) * step + LEN * q, k = TURNS ? fmt_step(F) * step + 8 * q : at;
 #pragma unroll
   for (int nt = 0; nt < NTL; ++nt)
@@ -596,14 +610,14 @@ __device__ __forceinline__ void mma_stage(const Stage<F, P, NTL>& s, int lane, f
 // takes, so every wait is for the oldest.  The count is filled up with steps
 // that load zeros from one place.  (The barriers keep the scheduler from
 // moving loads up, into registers of their own.)
-template <int F, bool UP, int NT, int NTL, int P = act_parts(F, UP)>
-__device__ __forceinline__ void product_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
+template <int F, bool UP, int NT, bool MANY, int NTL, int P = act_parts(F, UP)>
+__device__ __forceinline__ void product_loop(const Lane<F, UP, NT, MANY>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
                                              int stride, int end, int lane, int Kd, int N, int64_t plane) {
   constexpr int S = kStages;
   const int q = lane >> 4;
   Stage<F, P, NTL> s[S];
   auto load = [&](Stage<F, P, NTL>& st, int k) {
-    load_stage<F, UP, NT, NTL, P>(st, L, k, q, Kd, N, k < end, plane);
+    load_stage<F, UP, NT, MANY, NTL, P>(st, L, k, q, Kd, N, k < end, plane);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mma = [&](Stage<F, P, NTL>& st) {
@@ -642,7 +656,7 @@ struct WeightStage {
 };
 
 template <int F, bool UP, int NT, int NTL>
-__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
+__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, false>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
                                             int end, int tid, int Kd, int N, int64_t plane,
                                             const char* const (&src)[NT], char* lds) {
   constexpr int P = act_parts(F, UP), B = fmt_f32(F) ? 4 : 2, VECS = F == kFmtMxF32 ? 2 : P;
@@ -650,7 +664,7 @@ __device__ __forceinline__ void shared_loop(const Lane<F, UP, NT>& L, f32x4 (&ac
   WeightStage<F, UP, NT> s0, s1;
   u32x4 v[NTL][VECS];   // this thread's 8 values of rows tid / 16, 16 + tid / 16
   auto load_w = [&](WeightStage<F, UP, NT>& s, int k) {
-    load_weights<F, UP, NT>(s, L, k, q, Kd, N);
+    load_weights<F, UP, NT, false>(s, L, k, q, Kd, N);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto load_act = [&](int k) {
@@ -795,8 +809,8 @@ __device__ __forceinline__ void pin_args(const DecodeArgs& a) {
                "s"(a.h), "s"(a.y), "s"(a.picked));
 }
 
-// One block: one entry (up to 16 NT rows of one expert) x one tile of columns x
-// one k slice.  Its 4 waves are CW column tiles next to each other x 4 / CW
+// One block: one entry (up to 16 NT rows of one expert; MANY: or 16 NT of an
+// entry's 64) x one tile of columns x one k slice.  Its 4 waves are CW column tiles next to each other x 4 / CW
 // shares of the k steps, whose sums are added in wave order through LDS.
 //
 // HEAD: the first product's blocks make the list for themselves (block_route).
@@ -804,7 +818,7 @@ __device__ __forceinline__ void pin_args(const DecodeArgs& a) {
 // last: a block stores its sums coherently, waits until they are written, and
 // counts itself; whoever counts last reads them all.  Nobody waits for
 // anybody.  The first product's first block clears the counters.
-template <int F, bool UP, int NT, int CW, bool FUSED>
+template <int F, bool UP, int NT, int CW, bool FUSED, bool MANY>
 __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void decode_ffn_kernel(DecodeArgs a, int slices, int slice_steps) {
   constexpr bool HEAD = UP && FUSED, TAIL = !UP && FUSED;
   constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, KW = kWaves / CW;
@@ -820,10 +834,12 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
   static_assert(kThreads * 16 <= sizeof(red), "the parts' sums of a token");
   pin_args(a);
   asm volatile("" ::"s"(slices), "s"(slice_steps));
-  const int entry = blockIdx.y;
+  constexpr int HALVES = MANY ? kMaxRowTile / RT : 1;   // blocks that share an entry's rows
+  const int entry = blockIdx.y, half = HALVES > 1 ? blockIdx.x / kXcds % HALVES : 0;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int m = lane & 15, q = lane >> 4;
-  const int tile = blockIdx.x, slice = blockIdx.z;
+  const int tile = HALVES > 1 ? blockIdx.x / (HALVES * kXcds) * kXcds + blockIdx.x % kXcds : blockIdx.x;
+  const int slice = blockIdx.z;
   const int Kd = UP ? a.H : a.I, N = UP ? a.I : a.H;
   const int64_t RA = (int64_t)a.R + (int64_t)a.Ns * a.T;
   const int64_t Ih = fmt_mx(F) ? (a.I + 127) / 128 * 128 : a.I;   // a row of h
@@ -840,12 +856,12 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
   } else {
     const int2 en = a.entries[entry];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) ids[nt] = a.lists[(int64_t)entry * RT + (16 * nt + m) % RT];
+    for (int nt = 0; nt < NT; ++nt) ids[nt] = a.lists[(int64_t)(entry * HALVES + half) * RT + (16 * nt + m) % RT];
     group = en.x;
-    rows = en.y;
+    rows = HALVES > 1 ? min(en.y - half * RT, RT) : en.y;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(ids[nt]));   // asked for before rows is known
-    if (rows == 0) return;   // not in use
+    if (rows <= 0 || (HALVES > 1 && tile * COLS >= N)) return;   // not in use
     // Lanes without a row repeat the first one's.  (Read outside the choice:
     // inside it, lane 0 would be switched off.)
     const int id0 = __builtin_amdgcn_readfirstlane(ids[0]);
@@ -859,7 +875,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
   int col0 = tile * COLS + wave % CW * WCOLS;   // the wave's first column
   if constexpr (SHARED) col0 = min(col0, N - 32);   // all waves work: nothing is stored for one behind the end
 
-  Lane<F, UP, NT> L;
+  Lane<F, UP, NT, MANY> L;
   if constexpr (fmt_mx(F)) {
     const int64_t one = (int64_t)(Kd / kMxGroup) * N;   // groups of 32 of one matrix
 #pragma unroll
@@ -908,7 +924,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
       // The second part of row n is column n + 8 of the operand, in the place
       // of a second product.  (Lanes n and n + 8 have the same row.)
       if (!UP && m >= 8) L.act[0] += plane;
-      product_loop<F, UP, NT, 1, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, MANY, 1, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
       if constexpr (!UP) {
 #pragma unroll
         for (int j = 0; j < G; ++j)
@@ -916,9 +932,13 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
           for (int i = 0; i < 4; ++i) acc[0][j][i] += __shfl_xor(acc[0][j][i], 8, 16);
       }
     } else if (NT > 1 && rows <= 16) {
-      product_loop<F, UP, NT, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, MANY, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+    } else if (NT > 2 && rows <= 32) {
+      product_loop<F, UP, NT, MANY, 2>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+    } else if (NT > 3 && rows <= 48) {
+      product_loop<F, UP, NT, MANY, 3>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
     } else {
-      product_loop<F, UP, NT, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, MANY, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
     }
   }
 
@@ -1014,29 +1034,34 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int s
   if (c < a.H) store_out<BF16>(a, t, c, combine_items(a, slices, t, c, 0, 1));
 }
 
-template <int F, bool UP, int NT, int CW>
+template <int F, bool UP, int NT, int CW, bool MANY>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
   const int tiles = UP ? p.up_tiles : p.down_tiles, slices = UP ? 1 : p.slices;
   const int steps = UP ? (a.H + fmt_step(F) - 1) / fmt_step(F) : p.slice_steps;
-  const dim3 grid(tiles, p.entries, slices);
-  if (UP ? p.head : p.tail)
-    decode_ffn_kernel<F, UP, NT, CW, true><<<grid, kThreads, 0, st>>>(a, slices, steps);
-  else
-    decode_ffn_kernel<F, UP, NT, CW, false><<<grid, kThreads, 0, st>>>(a, slices, steps);
+  constexpr int halves = MANY ? kMaxRowTile / (16 * NT) : 1;
+  const dim3 grid(halves > 1 ? (tiles + kXcds - 1) / kXcds * kXcds * halves : tiles, p.entries, slices);
+  if (UP ? p.head : p.tail) {
+    if constexpr (UP || !MANY) decode_ffn_kernel<F, UP, NT, CW, true, MANY><<<grid, kThreads, 0, st>>>(a, slices, steps);
+  } else {
+    decode_ffn_kernel<F, UP, NT, CW, false, MANY><<<grid, kThreads, 0, st>>>(a, slices, steps);
+  }
   return hipGetLastError();
 }
-template <int F, bool UP, int NT>
+template <int F, bool UP, int NT, bool MANY = false>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if constexpr (fmt_mx(F) && NT == 2) return launch_product<F, UP, NT, 4>(a, p, st);
+  if constexpr (fmt_mx(F) && NT == 2) return launch_product<F, UP, NT, 4, MANY>(a, p, st);
   else switch (UP ? p.up_width : p.down_width) {
-    case 1: return launch_product<F, UP, NT, 1>(a, p, st);
-    case 2: return launch_product<F, UP, NT, 2>(a, p, st);
-    default: return launch_product<F, UP, NT, 4>(a, p, st);
+    case 1: return launch_product<F, UP, NT, 1, MANY>(a, p, st);
+    case 2: return launch_product<F, UP, NT, 2, MANY>(a, p, st);
+    default: return launch_product<F, UP, NT, 4, MANY>(a, p, st);
   }
 }
 template <int F, bool UP>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  return p.row_tile < 32 ? launch_product<F, UP, 1>(a, p, st) : launch_product<F, UP, 2>(a, p, st);
+  if (p.row_tile < 32) return launch_product<F, UP, 1>(a, p, st);
+  if constexpr (!fmt_mx(F))
+    if (p.row_tile == kMaxRowTile) return launch_product<F, UP, F == kFmtBf16 && !UP ? 2 : 4, true>(a, p, st);
+  return launch_product<F, UP, 2>(a, p, st);
 }
 
 template <int F>
@@ -1079,6 +1104,7 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
   DecodePlan p;
   p.row_tile = T <= row_tile_of(f, 1) ? row_tile_of(f, 1) : row_tile_of(f, 2);
   const int64_t R = (int64_t)T * K;
+  if (!mx && T > p.row_tile && R >= (int64_t)kManyRows * E) p.row_tile = kMaxRowTile;
   p.head = R <= kListPairs;
   p.picked = T > kHeadTokens || R > kThreads;
   p.tail = T <= kTailTokens;

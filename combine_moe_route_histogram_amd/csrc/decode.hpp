@@ -28,7 +28,7 @@ struct DecodePlan {
   bool head;        // the first product's blocks list the work for themselves
   bool picked;      // with head: the top-k has a launch of its own
   bool tail;        // the second product's last blocks add up the output
-  int row_tile;     // rows of one entry at most (8, 16 or 32)
+  int row_tile;     // rows of one entry at most (8, 16, 32 or 64)
   int entries;      // bound on the number of entries (expert x row tile)
   int up_width;     // column tiles a block's waves span (1, 2 or 4): gate/up projection
   int down_width;   // and down projection

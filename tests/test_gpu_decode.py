@@ -120,6 +120,15 @@ ODD = [  # dims that are multiples of 8 only: the plain weights
     (19, 200, 7, 3, 1000, 0),
     (40, 1000, 9, 2, 136, 2),
 ]
+MANY = [  # 32 rows an expert and more: entries of 64 rows, full, in part and more than one
+    (33, 72, 1, 1, 40, 0),
+    (48, 1544, 1, 1, 200, 1),
+    (64, 96, 2, 2, 2064, 0),
+    (65, 200, 1, 1, 136, 1),
+    (150, 2312, 2, 2, 736, 1),
+    (256, 264, 5, 3, 520, 2),
+    (256, 64, 40, 12, 72, 0),
+]
 
 
 def _inputs(shape, dtype, seed=900):
@@ -161,7 +170,7 @@ def _check(b, ref, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("shape", SHAPES + ODD, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shape", SHAPES + ODD + MANY, ids=lambda s: "x".join(map(str, s)))
 def test_decode_against_float64(shape, dtype):
     print(f"case decode {shape} {dtype}", flush=True)
     inp = _inputs(shape, dtype)
@@ -206,7 +215,8 @@ def test_routing_has_the_bits_of_moe_route(T, E, K):
 
 PADDED = [((20, 96, 6, 2, 160, 1), used) for used in (0, 1, 5, 19, 20, 21, -3)]
 PADDED += [((1, 64, 8, 2, 64, 1), 0), ((1, 64, 8, 2, 64, 1), 1), ((3, 64, 8, 2, 64, 1), 2),
-           ((8, 64, 200, 5, 64, 2), 7), ((200, 64, 40, 20, 64, 1), 90), ((200, 64, 40, 20, 64, 1), 0)]
+           ((8, 64, 200, 5, 64, 2), 7), ((200, 64, 40, 20, 64, 1), 90), ((200, 64, 40, 20, 64, 1), 0),
+           ((150, 96, 2, 2, 160, 1), 149), ((150, 96, 2, 2, 160, 1), 33), ((150, 96, 2, 2, 160, 1), 3)]
 
 
 @pytest.mark.parametrize("mx", [False, True], ids=["plain", "mx"])
