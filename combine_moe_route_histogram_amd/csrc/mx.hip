@@ -10,7 +10,9 @@
 //
 // Bound: bytes.  A thread owns 4 columns of one group: it reads 32 rows of 8
 // or 16 bytes (a wave reads 512 or 1024 contiguous bytes of each row) and
-// writes 4 x 16 bytes of codes, contiguous with its neighbours'.
+// writes 4 x 16 bytes of codes, contiguous with its neighbours'.  Measured:
+// bf16 [64, 2048, 1408] (467 MB in all) 87 us either way, 5.4 TB/s; bf16
+// [8, 4096, 14336] back 230 us, 5.2 TB/s (a large copy: 4.9).
 #include "common.hpp"
 #include "decode.hpp"
 

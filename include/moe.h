@@ -378,8 +378,10 @@ int moe_route_bwd(const moe_dims* d, const float* dtopk_w, const float* topk_w,
  *  ws: device workspace of at least moe_decode_workspace_bytes(d) bytes, 256-
  *           byte aligned, in any state; it may be shared by calls that are
  *           ordered on one stream, by none that overlap.
- * No output depends on the other rows of the batch or on T, but by the k
- * slices of the down projection, which the library chooses from the dims. */
+ * A row's bits depend on its own logits and x, the weights and the dims (T
+ * among them: the order of the sums is chosen by it), never on the other rows
+ * of the batch.  An infinity or NaN in x or in a weight that a row meets makes
+ * that row infinite or NaN (NaN, too, where exact arithmetic has an infinity). */
 size_t moe_decode_workspace_bytes(const moe_dims* d);
 int moe_decode(const moe_dims* d, const float* logits, const void* x, const void* w1, const void* w3,
                const void* w2, const void* ws1, const void* ws3, const void* ws2,

@@ -296,15 +296,16 @@ def test_offsets_beyond_32_bits(mx):
 
 
 @pytest.mark.parametrize("mx", [False, True], ids=["plain", "mx"])
-def test_rows_do_not_mix(mx):
+@pytest.mark.parametrize("shape", [(48, 128, 8, 3, 96, 1), (150, 128, 2, 2, 96, 1)], ids=lambda s: "x".join(map(str, s)))
+def test_rows_do_not_mix(shape, mx):
     """A row's result does not depend on the other rows: permuted tokens give permuted bits, and a
     row of NaN or infinity stays alone."""
-    shape = (48, 128, 8, 3, 96, 1)
+    T = shape[0]
     inp = _inputs(shape, "bf16")
     p = _packed_inputs(inp, "bf16")[0] if mx else device_inputs(inp)
     a = _buffers(shape, "bf16")
     L.decode(a, p)
-    order = torch.from_numpy(np.random.default_rng(3).permutation(48)).cuda()
+    order = torch.from_numpy(np.random.default_rng(3).permutation(T)).cuda()
     q = dict(p, x=p["x"][order].contiguous(), logits=p["logits"][order].contiguous())
     b = _buffers(shape, "bf16")
     L.decode(b, q)
@@ -315,7 +316,7 @@ def test_rows_do_not_mix(mx):
     L.decode(c, q)
     torch.cuda.synchronize()
     assert torch.equal(b.out, a.out[order]) and torch.equal(b.topk_idx, a.topk_idx[order])
-    rest = [t for t in range(48) if t not in (5, 30)]
+    rest = [t for t in range(T) if t not in (5, 30)]
     assert torch.equal(c.out[rest], a.out[rest]) and c.out[5].isnan().all()
 
 
