@@ -412,16 +412,20 @@ __device__ __forceinline__ void split_bf16(const float* f, u32x4* part) {
 // summed must not depend on how many rows its expert has, so the choice is by
 // the number of tokens.)
 //
-// Where the experts have kManyRows rows each or more, on average, an entry of
-// the formats without scales holds 64: the weights are read half as often, and
-// through the caches, since other entries of the expert read them too.  (us a
-// call with entries of 32, read past the caches, and of 64.  bf16 [4096, 14336]
-// x 2 in 8 experts, 24, 32 and 64 rows each: 519 and 655, 773 and 677, 1256 and
-// 898; [2048, 1408] x 4 in 32, 8 and 32 rows: 104 and 129, 179 and 153.  f32
-// [4096, 14336] x 2 in 4, 24, 32, 48, 64 and 128 rows: 814 and 825, 1314 and
-// 996, 1706 and 1370, 2016 and 2064, 3854 and 3293.)  The two bf16 parts of 64
-// rows do not fit into the registers: there two blocks next to each other on
-// one chiplet take 32 of an entry's rows each.
+// Where the experts have kManyRows rows each or more, on average, an entry
+// holds 64: the weights are read half as often, and through the caches, since
+// other entries of the expert read them too.  (us a call with entries of 32,
+// read past the caches, and of 64.  bf16 [4096, 14336] x 2 in 8 experts, 24, 32
+// and 64 rows each: 519 and 655, 773 and 677, 1256 and 898; [2048, 1408] x 4 in
+// 32, 8 and 32 rows: 104 and 129, 179 and 153.  f32 [4096, 14336] x 2 in 4, 24,
+// 32, 48, 64 and 128 rows: 814 and 825, 1314 and 996, 1706 and 1370, 2016 and
+// 2064, 3854 and 3293.  4 bit bf16 [4096, 14336] x 2 in 8, 24, 32 and 64 rows:
+// 181 and 178, 225 and 201, 358 and 313; [2048, 1408] x 4 in 32, 8 and 32 rows:
+// 44.0 and 46.7, 72.7 and 67.1; but with one expert of 64 rows, which leaves 112
+// blocks, 58 and 76: there the 32.)  Two bf16 parts of 64 rows do not fit into
+// the registers of the plain products: there two blocks next to each other on
+// one chiplet take 32 of an entry's rows each.  Three parts of them (f32 on 4
+// bit) would take two thirds of a CU's LDS.
 constexpr int kManyRows = 32;
 constexpr int row_tile_of(int f, int nt) { return f == kFmtMxBf16 && nt == 1 ? 8 : 16 * nt; }
 
@@ -484,7 +488,7 @@ __device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT, MANY>& 
 #pragma unroll
     for (int j = 0; j < fmt_groups(F); ++j) {
       const int jj = min(UP ? j >> 1 : j, L.groups - 1);
-      s.w[j] = ld16_stream(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes);
+      s.w[j] = MANY ? ld16_global(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes) : ld16_stream(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes);
     }
     const uint64_t sc = real ? reinterpret_cast<uint64_t>(L.sc) + at : zeros;
     s.s = *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(sc);
@@ -666,8 +670,8 @@ struct WeightStage {
   uint32_t s;
 };
 
-template <int F, bool UP, int NT, int NTL>
-__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, false>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
+template <int F, bool UP, int NT, bool MANY, int NTL>
+__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, MANY>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
                                             int end, int tid, int Kd, int N, int64_t plane,
                                             const char* const (&src)[NT], char* lds) {
   constexpr int P = act_parts(F, UP), B = fmt_f32(F) ? 4 : 2, VECS = F == kFmtMxF32 ? 2 : P;
@@ -675,7 +679,7 @@ __device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, false>& L, f32
   WeightStage<F, UP, NT> s0, s1;
   u32x4 v[NTL][VECS];   // this thread's 8 values of rows tid / 16, 16 + tid / 16
   auto load_w = [&](WeightStage<F, UP, NT>& s, int k) {
-    load_weights<F, UP, NT, false>(s, L, k, q, Kd, N);
+    load_weights<F, UP, NT, MANY>(s, L, k, q, Kd, N);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto load_act = [&](int k) {
@@ -834,7 +838,12 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
   constexpr bool HEAD = UP && FUSED, TAIL = !UP && FUSED;
   constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, KW = kWaves / CW;
   constexpr int WCOLS = UP ? 8 * G : 16 * G, COLS = WCOLS * CW;   // columns of a wave, of the block
-  constexpr bool SHARED = fmt_mx(F) && NT == 2;   // rows' values by way of LDS
+  constexpr bool SHARED = fmt_mx(F) && NT >= 2;   // rows' values by way of LDS
+  // No sums to join, W1's and W3's in one lane: the sums are stored from the
+  // registers (through LDS, 8 rows at a time: 4 bit, 200 tokens of 4 in 32
+  // experts 64.4 us in the place of 59.2).  A plain kernel of 16 rows would
+  // need a register too many.
+  constexpr bool DIRECT = KW == 1 && !TAIL && (fmt_mx(F) || (!UP && NT > 1));
   constexpr int RT = row_tile_of(F, NT);           // rows of an entry at most
   constexpr int kRedFloats = kWaves * kRedRows * red_stride<F>();
   constexpr int kActFloats = SHARED ? act_bytes<F, UP, NT>() / 2 : 0;
@@ -926,8 +935,10 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) src[nt] = row_values(__shfl(ids[nt], tid >> 4, kWave));
     char* lds = reinterpret_cast<char*>(red);
-    if (rows <= 16) shared_loop<F, UP, NT, 1>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
-    else shared_loop<F, UP, NT, NT>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    if (rows <= 16) shared_loop<F, UP, NT, MANY, 1>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    else if (NT > 2 && rows <= 32) shared_loop<F, UP, NT, MANY, 2>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    else if (NT > 3 && rows <= 48) shared_loop<F, UP, NT, MANY, 3>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    else shared_loop<F, UP, NT, MANY, NT>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
   } else if (col0 < N) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) L.act[nt] = row_values(ids[nt]);
@@ -951,6 +962,51 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
     } else {
       product_loop<F, UP, NT, MANY, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
     }
+  }
+
+  if constexpr (DIRECT) {   // a wave's sums are whole: from its registers to memory, 4 columns a lane
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (16 * nt + m >= rows) continue;
+      const int64_t row = ids[nt];
+      const int c0 = tile * COLS + wave % CW * WCOLS;
+#pragma unroll
+      for (int j = 0; j < (UP ? G / 2 : G); ++j) {
+        if constexpr (UP) {
+          const int c = c0 + 16 * j + 4 * q;
+          if (c >= N) continue;
+          float hv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) hv[i] = silu_f(acc[nt][2 * j][i]) * acc[nt][2 * j + 1][i];
+          const int64_t place = row * Ih + mx_h_place(c);
+          if constexpr (fmt_f32(F)) {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.h) + place) = f32x4{hv[0], hv[1], hv[2], hv[3]};
+          } else {
+            u32x2 hi, lo;
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              hi[d] = pack_bf16x2(hv[2 * d], hv[2 * d + 1]);
+              lo[d] = pack_bf16x2(hv[2 * d] - __uint_as_float(hi[d] << 16), hv[2 * d + 1] - __uint_as_float(hi[d] & 0xFFFF0000u));
+            }
+            uint16_t* hp = static_cast<uint16_t*>(a.h) + place;
+            *reinterpret_cast<u32x2*>(hp) = hi;
+            *reinterpret_cast<u32x2*>(hp + RA * Ih) = lo;
+          }
+        } else if constexpr (fmt_mx(F)) {
+          const int c = c0 + 16 * j + 4 * q;
+          if (c < N) *reinterpret_cast<f32x4*>(a.y + ((int64_t)slice * RA + row) * N + c) = acc[nt][j];
+        } else if (j % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + G * (4 * q + i) + j;
+            if (c < N)
+              *reinterpret_cast<f32x4*>(a.y + ((int64_t)slice * RA + row) * N + c) =
+                  f32x4{acc[nt][j][i], acc[nt][j + 1][i], acc[nt][j + 2][i], acc[nt][j + 3][i]};
+          }
+        }
+      }
+    }
+    return;
   }
 
   constexpr int RS = red_stride<F>();
@@ -1060,7 +1116,7 @@ hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t 
 }
 template <int F, bool UP, int NT, bool MANY = false>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if constexpr (fmt_mx(F) && NT == 2) return launch_product<F, UP, NT, 4, MANY>(a, p, st);
+  if constexpr (fmt_mx(F) && NT >= 2) return launch_product<F, UP, NT, 4, MANY>(a, p, st);
   else switch (UP ? p.up_width : p.down_width) {
     case 1: return launch_product<F, UP, NT, 1, MANY>(a, p, st);
     case 2: return launch_product<F, UP, NT, 2, MANY>(a, p, st);
@@ -1070,7 +1126,7 @@ hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t 
 template <int F, bool UP>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
   if (p.row_tile < 32) return launch_product<F, UP, 1>(a, p, st);
-  if constexpr (!fmt_mx(F))
+  if constexpr (F != kFmtMxF32)
     if (p.row_tile == kMaxRowTile) return launch_product<F, UP, F == kFmtBf16 && !UP ? 2 : 4, true>(a, p, st);
   return launch_product<F, UP, 2>(a, p, st);
 }
@@ -1102,7 +1158,7 @@ hipError_t launch_fmt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) 
 // are long ones, and their waves work side by side on the same rows' values
 // where those go through LDS.
 static int tile_width(bool mx, int row_tile, int64_t row_bytes, int columns, int tile, double groups_and_slices) {
-  if (mx && row_tile == 32) return 4;
+  if (mx && row_tile >= 32) return 4;
   const bool short_row = !mx && row_bytes < kLongRow;
   for (int w = !mx && row_bytes >= 2 * kLongRow ? 4 : 2; w > 1; w /= 2)
     if ((columns + w * tile - 1) / (w * tile) * groups_and_slices >= (short_row ? kManyBlocks : kFillBlocks)) return w;
@@ -1115,17 +1171,20 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
   DecodePlan p;
   p.row_tile = T <= row_tile_of(f, 1) ? row_tile_of(f, 1) : row_tile_of(f, 2);
   const int64_t R = (int64_t)T * K;
-  if (!mx && T > p.row_tile && R >= (int64_t)kManyRows * E) p.row_tile = kMaxRowTile;
   p.head = R <= kListPairs;
   p.picked = T > kHeadTokens || R > kThreads;
   p.tail = T <= kTailTokens;
-  const int busy = (int)(R < E ? R : E);   // experts with rows, at most
-  // an expert with c rows has at most 1 + (c - 1) / row_tile entries
-  p.entries = busy + (int)((R - busy) / p.row_tile) + Ns * ((T + p.row_tile - 1) / p.row_tile);
   // experts with rows as expected of even routing, and the shared ones
   double miss = 1.0;
   for (int t = 0; t < T; ++t) miss *= 1.0 - (double)K / E;
   const double groups = E * (1.0 - miss) + Ns;
+  if (f != kFmtMxF32 && T > p.row_tile && R >= (int64_t)kManyRows * E) {
+    const double entries = R / (double)kMaxRowTile > groups ? R / (double)kMaxRowTile : groups;
+    if (!mx || I / (kWaves * tile / 2) * entries >= kFillBlocks) p.row_tile = kMaxRowTile;
+  }
+  const int busy = (int)(R < E ? R : E);   // experts with rows, at most
+  // an expert with c rows has at most 1 + (c - 1) / row_tile entries
+  p.entries = busy + (int)((R - busy) / p.row_tile) + Ns * ((T + p.row_tile - 1) / p.row_tile);
   p.up_width = tile_width(mx, p.row_tile, (int64_t)I * size, I, tile / 2, groups);
   p.up_tiles = (I + p.up_width * tile / 2 - 1) / (p.up_width * tile / 2);
   const int steps = (I + step - 1) / step, most = steps < kMaxSlices ? steps : kMaxSlices;

@@ -126,13 +126,14 @@ def decode(b: DecodeBuffers, p: dict, stream=None):
          p.get("n_tokens"), b.topk_idx, b.topk_w, b.out, b.ws, stream)
 
 
-def quantize_weights(p: dict, stream=None) -> dict:
-    """A copy of p with its weight matrices packed to 4 bits (moe_mx_quantize)."""
+def quantize_weights(p: dict) -> dict:
+    """A copy of p with its weight matrices packed to 4 bits (moe_mx_quantize), on the current
+    stream: the packed tensors are allocated here, so memory and work must be of one stream."""
     q = dict(p)
     for name in ("w1", "w3", "w2", "ws1", "ws3", "ws2"):
         w = p.get(name)
         if w is not None:
             G, K, N = w.shape
             q[name] = torch.empty(moe_mx_bytes(G, K, N), dtype=torch.uint8, device=w.device)
-            moe_mx_quantize(G, K, N, w, q[name], stream)
+            moe_mx_quantize(G, K, N, w, q[name])
     return q

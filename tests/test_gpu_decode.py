@@ -68,7 +68,6 @@ def test_quantize_smallest_numbers():
     for c, big in enumerate([2.0 ** -126, 1.5 * 2.0 ** -126, 2.0 ** -125, 2.0 ** -124, 5 * 2.0 ** -126, 2.0 ** -123]):
         w[0, :, c] = big * np.linspace(-1, 1, 32)
         w[0, 0, c] = big
-        w[0, np.abs(w[0, :, c]) < 2.0 ** -126, c] = 0.0      # normal numbers and zeros
     code, s = D.mx_quantize(w.astype(np.float64))
     mx = torch.empty(M.moe_mx_bytes(1, 32, 8), dtype=torch.uint8, device="cuda")
     M.moe_mx_quantize(1, 32, 8, dev(w), mx)
@@ -113,6 +112,9 @@ SHAPES = [
     (8, 4096, 3, 1, 64, 1),
     (9, 128, 4, 2, 4224, 0),
     (7, 2080, 5, 2, 544, 2),
+    (1, 64, 256, 256, 32, 0),      # more picks than a wave has lanes, in the block, and in a launch
+    (3, 64, 200, 100, 64, 1),
+    (4, 64, 64, 64, 32, 0),
 ]
 ODD = [  # dims that are multiples of 8 only: the plain weights
     (1, 8, 1, 1, 8, 0),
@@ -128,6 +130,11 @@ MANY = [  # 32 rows an expert and more: entries of 64 rows, full, in part and mo
     (150, 2312, 2, 2, 736, 1),
     (256, 264, 5, 3, 520, 2),
     (256, 64, 40, 12, 72, 0),
+]
+MANY_MX = [   # the same, with as many column tiles as entries of 64 rows want
+    (64, 64, 2, 2, 14080, 0),
+    (151, 96, 2, 1, 14336, 1),
+    (256, 160, 6, 6, 5152, 2),
 ]
 
 
@@ -181,7 +188,7 @@ def test_decode_against_float64(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shape", SHAPES + MANY_MX, ids=lambda s: "x".join(map(str, s)))
 def test_decode_mx_against_float64(shape, dtype):
     print(f"case decode_mx {shape} {dtype}", flush=True)
     inp = _inputs(shape, dtype)

@@ -23,7 +23,9 @@ def test_down_projection_publishes_its_sums(tmp_path):
 def test_products_load_by_counted_waits(tmp_path):
     """The products keep two steps of loads in flight: no load of theirs may be a flat one, and no
     register may live in scratch memory (both wait for everything that is outstanding)."""
-    bodies = _functions(_asm("decode.hip", tmp_path), r"decode_ffn_kernelILi")
+    asm = _asm("decode.hip", tmp_path)
+    # up to the end of the function: a kernel may have more than one s_endpgm
+    bodies = re.findall(r"^_Z\S*decode_ffn_kernelILi\S*:(.*?)^\.Lfunc_end", asm, flags=re.M | re.S)
     assert bodies
     for body in bodies:
         assert not re.search(r"^\s*(flat|scratch)_", body, flags=re.M)
