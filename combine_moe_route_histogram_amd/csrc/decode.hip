@@ -15,7 +15,7 @@
 // 6.9 TB/s on this card): bf16 [4096, 14336] x 2 in 8 experts, 32 tokens 439 us,
 // 6.4 TB/s; [2048, 1408] x 6 in 64 experts and 2 shared ones, one token 30.9 us,
 // 4.5 TB/s, of which the routing, the two launches and the sum are about 7;
-// 4-bit weights, the same 17.1 and, 200 tokens of 4 in 32 experts, 61.6 us.
+// 4-bit weights, the same 17.1 and, 200 tokens of 4 in 32 experts, 59 us.
 #include "common.hpp"
 #include "decode.hpp"
 #include "kernels.hpp"
@@ -36,6 +36,7 @@ constexpr int kRouteThreads = 1024;
 constexpr int kHeadTokens = 4;
 constexpr int kTailTokens = 4;
 constexpr int64_t kLongRow = 4096;      // bytes
+constexpr int kLineBytes = 128;         // what the memory moves at once
 constexpr double kFillBlocks = 220, kManyBlocks = 512;
 constexpr double kSliceBlocks = 400;    // the down projection is cut along k for so many blocks,
 constexpr int kMaxSlices = 8;           // into so many slices at most
@@ -452,7 +453,7 @@ struct Stage {
 
 // A lane's place: its column(s) in row 0 of the matrix it reads, and its rows.
 // Lanes without a column or a row of their own repeat a valid one.
-template <int F, bool UP, int NT, bool MANY>
+template <int F, bool UP, int NT, bool CACHED>
 struct Lane {
   const char* w[fmt_mx(F) && UP ? 2 : 1];   // 4 bit: in W1 and W3 (up) or in W2
   const char* sc;                           // 4 bit: this lane's 4 scales in row 0
@@ -475,8 +476,8 @@ __device__ __forceinline__ u32x4 ld16_global(uint64_t address) {
 // comes of such columns is not stored, and rows at or behind `limit` meet
 // zeros.
 constexpr int step_len(int f) { return fmt_mx(f) ? kMxGroup : 8; }   // a lane's rows in one k step
-template <int F, bool UP, int NT, bool MANY, class S>
-__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT, MANY>& L, int step, int q, int Kd, int N,
+template <int F, bool UP, int NT, bool CACHED, class S>
+__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT, CACHED>& L, int step, int q, int Kd, int N,
                                              bool real = true) {
   const int k = min(fmt_step(F) * step + step_len(F) * q, Kd - step_len(F));
   const uint64_t zeros = reinterpret_cast<uint64_t>(kZeros);
@@ -488,7 +489,7 @@ __device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT, MANY>& 
 #pragma unroll
     for (int j = 0; j < fmt_groups(F); ++j) {
       const int jj = min(UP ? j >> 1 : j, L.groups - 1);
-      s.w[j] = MANY ? ld16_global(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes) : ld16_stream(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes);
+      s.w[j] = CACHED ? ld16_global(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes) : ld16_stream(p[UP ? j & 1 : 0] + jj * 16 * kMxCodeBytes);
     }
     const uint64_t sc = real ? reinterpret_cast<uint64_t>(L.sc) + at : zeros;
     s.s = *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(sc);
@@ -497,7 +498,7 @@ __device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT, MANY>& 
     const uint64_t p = real ? reinterpret_cast<uint64_t>(L.w[0]) + (int64_t)k * N * B : zeros;
     const int64_t row = real ? (int64_t)N * B : 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s.w[i] = MANY ? ld16_global(p + i * row) : ld16_stream(p + i * row);
+    for (int i = 0; i < 8; ++i) s.w[i] = CACHED ? ld16_global(p + i * row) : ld16_stream(p + i * row);
   }
 }
 
@@ -509,14 +510,14 @@ __device__ __forceinline__ int mx_h_place(int c) {
   return (c & ~127) | ((c >> 3) & 3) << 5 | ((c >> 5) & 3) << 3 | (c & 7);
 }
 
-template <int F, bool UP, int NT, bool MANY, int NTL, int P>
-__device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT, MANY>& L, int step, int q,
+template <int F, bool UP, int NT, bool CACHED, int NTL, int P>
+__device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT, CACHED>& L, int step, int q,
                                            int Kd, int N, bool real, int64_t plane) {
   constexpr int V = act_vecs(F, P), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
   constexpr int PER = LEN * B / 16;   // vectors of a lane's values from one plane
   constexpr int V8 = 8 * B / 16;      // and of 8 values
   constexpr bool TURNS = fmt_mx(F) && !UP;   // h in the order of mx_h_place
-  load_weights<F, UP, NT, MANY>(s, L, step, q, Kd, N, real);
+  load_weights<F, UP, NT, CACHED>(s, L, step, q, Kd, N, real);
   const int at = fmt_step(F) * step + LEN * q, k = TURNS ? fmt_step(F) * step + 8 * q : at;
 #pragma unroll
   for (int nt = 0; nt < NTL; ++nt)
@@ -625,14 +626,14 @@ __device__ __forceinline__ void mma_stage(const Stage<F, P, NTL>& s, int lane, f
 // takes, so every wait is for the oldest.  The count is filled up with steps
 // that load zeros from one place.  (The barriers keep the scheduler from
 // moving loads up, into registers of their own.)
-template <int F, bool UP, int NT, bool MANY, int NTL, int P = act_parts(F, UP)>
-__device__ __forceinline__ void product_loop(const Lane<F, UP, NT, MANY>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
+template <int F, bool UP, int NT, bool CACHED, int NTL, int P = act_parts(F, UP)>
+__device__ __forceinline__ void product_loop(const Lane<F, UP, NT, CACHED>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
                                              int stride, int end, int lane, int Kd, int N, int64_t plane) {
   constexpr int S = kStages;
   const int q = lane >> 4;
   Stage<F, P, NTL> s[S];
   auto load = [&](Stage<F, P, NTL>& st, int k) {
-    load_stage<F, UP, NT, MANY, NTL, P>(st, L, k, q, Kd, N, k < end, plane);
+    load_stage<F, UP, NT, CACHED, NTL, P>(st, L, k, q, Kd, N, k < end, plane);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mma = [&](Stage<F, P, NTL>& st) {
@@ -670,8 +671,8 @@ struct WeightStage {
   uint32_t s;
 };
 
-template <int F, bool UP, int NT, bool MANY, int NTL>
-__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, MANY>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
+template <int F, bool UP, int NT, bool CACHED, int NTL>
+__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, CACHED>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
                                             int end, int tid, int Kd, int N, int64_t plane,
                                             const char* const (&src)[NT], char* lds) {
   constexpr int P = act_parts(F, UP), B = fmt_f32(F) ? 4 : 2, VECS = F == kFmtMxF32 ? 2 : P;
@@ -679,7 +680,7 @@ __device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, MANY>& L, f32x
   WeightStage<F, UP, NT> s0, s1;
   u32x4 v[NTL][VECS];   // this thread's 8 values of rows tid / 16, 16 + tid / 16
   auto load_w = [&](WeightStage<F, UP, NT>& s, int k) {
-    load_weights<F, UP, NT, MANY>(s, L, k, q, Kd, N);
+    load_weights<F, UP, NT, CACHED>(s, L, k, q, Kd, N);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto load_act = [&](int k) {
@@ -833,7 +834,7 @@ __device__ __forceinline__ void pin_args(const DecodeArgs& a) {
 // last: a block stores its sums coherently, waits until they are written, and
 // counts itself; whoever counts last reads them all.  Nobody waits for
 // anybody.  The first product's first block clears the counters.
-template <int F, bool UP, int NT, int CW, bool FUSED, bool MANY>
+template <int F, bool UP, int NT, int CW, bool FUSED, bool MANY, bool CACHED>
 __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void decode_ffn_kernel(DecodeArgs a, int slices, int slice_steps) {
   constexpr bool HEAD = UP && FUSED, TAIL = !UP && FUSED;
   constexpr int G = fmt_groups(F), B = fmt_f32(F) ? 4 : 2, KW = kWaves / CW;
@@ -895,7 +896,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
   int col0 = tile * COLS + wave % CW * WCOLS;   // the wave's first column
   if constexpr (SHARED) col0 = min(col0, N - 32);   // all waves work: nothing is stored for one behind the end
 
-  Lane<F, UP, NT, MANY> L;
+  Lane<F, UP, NT, CACHED> L;
   if constexpr (fmt_mx(F)) {
     const int64_t one = (int64_t)(Kd / kMxGroup) * N;   // groups of 32 of one matrix
 #pragma unroll
@@ -935,10 +936,10 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) src[nt] = row_values(__shfl(ids[nt], tid >> 4, kWave));
     char* lds = reinterpret_cast<char*>(red);
-    if (rows <= 16) shared_loop<F, UP, NT, MANY, 1>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
-    else if (NT > 2 && rows <= 32) shared_loop<F, UP, NT, MANY, 2>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
-    else if (NT > 3 && rows <= 48) shared_loop<F, UP, NT, MANY, 3>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
-    else shared_loop<F, UP, NT, MANY, NT>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    if (rows <= 16) shared_loop<F, UP, NT, CACHED, 1>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    else if (NT > 2 && rows <= 32) shared_loop<F, UP, NT, CACHED, 2>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    else if (NT > 3 && rows <= 48) shared_loop<F, UP, NT, CACHED, 3>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
+    else shared_loop<F, UP, NT, CACHED, NT>(L, acc, begin, end, tid, Kd, N, plane, src, lds);
   } else if (col0 < N) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) L.act[nt] = row_values(ids[nt]);
@@ -946,7 +947,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
       // The second part of row n is column n + 8 of the operand, in the place
       // of a second product.  (Lanes n and n + 8 have the same row.)
       if (!UP && m >= 8) L.act[0] += plane;
-      product_loop<F, UP, NT, MANY, 1, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, CACHED, 1, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
       if constexpr (!UP) {
 #pragma unroll
         for (int j = 0; j < G; ++j)
@@ -954,13 +955,13 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
           for (int i = 0; i < 4; ++i) acc[0][j][i] += __shfl_xor(acc[0][j][i], 8, 16);
       }
     } else if (NT > 1 && rows <= 16) {
-      product_loop<F, UP, NT, MANY, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, CACHED, 1>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
     } else if (NT > 2 && rows <= 32) {
-      product_loop<F, UP, NT, MANY, 2>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, CACHED, 2>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
     } else if (NT > 3 && rows <= 48) {
-      product_loop<F, UP, NT, MANY, 3>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, CACHED, 3>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
     } else {
-      product_loop<F, UP, NT, MANY, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
+      product_loop<F, UP, NT, CACHED, NT>(L, acc, begin + wave / CW, KW, end, lane, Kd, N, plane);
     }
   }
 
@@ -1101,34 +1102,44 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int s
   if (c < a.H) store_out<BF16>(a, t, c, combine_items(a, slices, t, c, 0, 1));
 }
 
-template <int F, bool UP, int NT, int CW, bool MANY>
+template <int F, bool UP, int NT, int CW, bool MANY, bool CACHED>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
   const int tiles = UP ? p.up_tiles : p.down_tiles, slices = UP ? 1 : p.slices;
   const int steps = UP ? (a.H + fmt_step(F) - 1) / fmt_step(F) : p.slice_steps;
   constexpr int halves = MANY ? kMaxRowTile / (16 * NT) : 1;
   const dim3 grid(halves > 1 ? (tiles + kXcds - 1) / kXcds * kXcds * halves : tiles, p.entries, slices);
   if (UP ? p.head : p.tail) {
-    if constexpr (UP || !MANY) decode_ffn_kernel<F, UP, NT, CW, true, MANY><<<grid, kThreads, 0, st>>>(a, slices, steps);
+    static_assert(kTailTokens <= 8, "the tail's entries have 16 rows at most");
+    if constexpr (UP || NT == 1)
+      decode_ffn_kernel<F, UP, NT, CW, true, MANY, CACHED><<<grid, kThreads, 0, st>>>(a, slices, steps);
   } else {
-    decode_ffn_kernel<F, UP, NT, CW, false, MANY><<<grid, kThreads, 0, st>>>(a, slices, steps);
+    decode_ffn_kernel<F, UP, NT, CW, false, MANY, CACHED><<<grid, kThreads, 0, st>>>(a, slices, steps);
   }
   return hipGetLastError();
 }
-template <int F, bool UP, int NT, bool MANY = false>
+template <int F, bool UP, int NT, bool MANY, bool CACHED>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if constexpr (fmt_mx(F) && NT >= 2) return launch_product<F, UP, NT, 4, MANY>(a, p, st);
+  if constexpr (fmt_mx(F) && NT >= 2) return launch_product<F, UP, NT, 4, MANY, CACHED>(a, p, st);
   else switch (UP ? p.up_width : p.down_width) {
-    case 1: return launch_product<F, UP, NT, 1, MANY>(a, p, st);
-    case 2: return launch_product<F, UP, NT, 2, MANY>(a, p, st);
-    default: return launch_product<F, UP, NT, 4, MANY>(a, p, st);
+    case 1: return launch_product<F, UP, NT, 1, MANY, CACHED>(a, p, st);
+    case 2: return launch_product<F, UP, NT, 2, MANY, CACHED>(a, p, st);
+    default: return launch_product<F, UP, NT, 4, MANY, CACHED>(a, p, st);
   }
 }
+// Weights are read past the caches (through them the calls take 5 to 12 % longer)
+// unless others read the same lines: other entries of the expert (kManyRows), or
+// the tiles to the left and right where rows do not begin on a line ([2816,
+// 2840] x 8 in 26 experts, one token 110.6 us past, 105.8 through the caches;
+// [584, 2632] x 8 in 100, 14 tokens 172 and 154; [2048, 1400] x 4 in 32, 2
+// tokens 44.6 and 39.2).
 template <int F, bool UP>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if (p.row_tile < 32) return launch_product<F, UP, 1>(a, p, st);
   if constexpr (F != kFmtMxF32)
-    if (p.row_tile == kMaxRowTile) return launch_product<F, UP, F == kFmtBf16 && !UP ? 2 : 4, true>(a, p, st);
-  return launch_product<F, UP, 2>(a, p, st);
+    if (p.row_tile == kMaxRowTile) return launch_product<F, UP, F == kFmtBf16 && !UP ? 2 : 4, true, true>(a, p, st);
+  if constexpr (!fmt_mx(F))
+    if ((int64_t)(UP ? a.I : a.H) * (fmt_f32(F) ? 4 : 2) % kLineBytes)
+      return p.row_tile < 32 ? launch_product<F, UP, 1, false, true>(a, p, st) : launch_product<F, UP, 2, false, true>(a, p, st);
+  return p.row_tile < 32 ? launch_product<F, UP, 1, false, false>(a, p, st) : launch_product<F, UP, 2, false, false>(a, p, st);
 }
 
 template <int F>
