@@ -38,8 +38,13 @@ constexpr int kTailTokens = 4;
 constexpr int64_t kLongRow = 4096;      // bytes
 constexpr int kLineBytes = 128;         // what the memory moves at once
 constexpr double kFillBlocks = 220, kManyBlocks = 512;
-constexpr double kSliceBlocks = 400;    // the down projection is cut along k for so many blocks,
-constexpr int kMaxSlices = 8;           // into so many slices at most
+// The down projection is cut along k for so many blocks, into so many slices at
+// most.  (150, 220 and 280 blocks, over 132 calls of five layers, all formats,
+// 1 to 128 tokens: 0.6, 1.1 and 1.2 % longer in the mean; bf16 [4096, 14336] x 2
+// in 8 experts, 32 tokens 455 -> 510, 520, 465 us, f32 [2048, 1408] x 4 in 32, 8
+// tokens 149 -> 129, 140, 140.)
+constexpr double kSliceBlocks = 400;
+constexpr int kMaxSlices = 8;
 
 enum Fmt : int { kFmtBf16 = 0, kFmtF32 = 1, kFmtMxBf16 = 2, kFmtMxF32 = 3 };
 constexpr bool fmt_mx(int f) { return f >= kFmtMxBf16; }
@@ -656,7 +661,7 @@ __device__ __forceinline__ void product_loop(const Lane<F, UP, NT, CACHED>& L, f
   for (int i = 1; i < S; ++i) mma(s[i]);
 }
 
-// 4-bit weights, more than 16 rows: the rows' values are the larger half of
+// 4-bit weights, more than 8 tokens (f32: 16): the rows' values are the larger half of
 // what a step loads, and each lane's 16 bytes of them lie 64 bytes from its
 // neighbour's.  The block's waves, side by side on the same steps, load each
 // value once, whole lines at a time, split it into its bf16 parts, and hand it
