@@ -393,7 +393,12 @@ __device__ __forceinline__ u32x4 ld16_stream(uint64_t address) {
 }
 
 // x = hi + lo (+ lo2), each part a bf16: what a rounding leaves is exact in
-// float32, so two parts keep 16 bits of it and three all 24.
+// float32, so two parts keep 16 bits of it and three all 24.  The first part of
+// a number that would round to infinity is the largest bf16, and the rest, less
+// than 2^120 there, is the other parts' (an infinite first part would leave
+// -inf, and the row NaN).
+constexpr float kMaxBf16 = 0x1.FEp127f;
+__device__ __forceinline__ float first_part(float v) { return __builtin_amdgcn_fmed3f(v, -kMaxBf16, kMaxBf16); }
 template <int P>
 __device__ __forceinline__ void split_bf16(const float* f, u32x4* part) {
   float r[8];
@@ -403,7 +408,8 @@ __device__ __forceinline__ void split_bf16(const float* f, u32x4* part) {
   for (int p = 0; p < P; ++p) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const uint32_t v = pack_bf16x2(r[2 * d], r[2 * d + 1]);
+      const uint32_t v = p == 0 ? pack_bf16x2(first_part(r[2 * d]), first_part(r[2 * d + 1]))
+                                : pack_bf16x2(r[2 * d], r[2 * d + 1]);
       part[p][d] = v;
       r[2 * d] -= __uint_as_float(v << 16);
       r[2 * d + 1] -= __uint_as_float(v & 0xFFFF0000u);
@@ -991,7 +997,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
             u32x2 hi, lo;
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-              hi[d] = pack_bf16x2(hv[2 * d], hv[2 * d + 1]);
+              hi[d] = pack_bf16x2(first_part(hv[2 * d]), first_part(hv[2 * d + 1]));
               lo[d] = pack_bf16x2(hv[2 * d] - __uint_as_float(hi[d] << 16), hv[2 * d + 1] - __uint_as_float(hi[d] & 0xFFFF0000u));
             }
             uint16_t* hp = static_cast<uint16_t*>(a.h) + place;
@@ -1052,7 +1058,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
         if constexpr (fmt_f32(F)) {
           static_cast<float*>(a.h)[place] = hv;
         } else {
-          const uint32_t hi = f32_to_bf16(hv);
+          const uint32_t hi = f32_to_bf16(first_part(hv));
           uint16_t* hp = static_cast<uint16_t*>(a.h);
           hp[place] = (uint16_t)hi;
           hp[RA * Ih + place] = (uint16_t)f32_to_bf16(hv - bf16_to_f32(hi));
