@@ -6,7 +6,9 @@
 // the nearest grid value of w / 2^s, ties to the even code, magnitudes above 6
 // to 6 (OCP Microscaling, MXFP4).  Division by 2^s is exact, so the only
 // rounding is the code's own; gfx950 has it as one instruction per two
-// weights, in both directions.
+// weights, in both directions.  The instruction takes the exponent field of
+// its scale operand, so byte << 23 is every scale byte of the format: field 0
+// is 2^-127 and not the float 0, field 255 makes NaN.
 //
 // Bound: bytes.  A thread owns 4 columns of one group: it reads 32 rows of 8
 // or 16 bytes (a wave reads 512 or 1024 contiguous bytes of each row) and

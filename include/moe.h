@@ -403,14 +403,18 @@ int moe_decode_mx(const moe_dims* d, const float* logits, const void* x, const v
  * G matrices [K, N] take moe_mx_bytes(G, K, N) = G*K*N*17/32 bytes: first the
  * codes [G, K/32, N, 16] (byte j holds weight 2j of the 32 in its low half and
  * weight 2j+1 in its high half), then the scales [G, K/32, N]; scale byte b
- * stands for 2^(b-127), 1 <= b <= 254.  K must be a multiple of 32, N of 8.
- * Codes quantised elsewhere can be laid out like this and used as well.
+ * stands for 2^(b-127) from 0 to 254, and 255 for NaN (E8M0).  K must be a
+ * multiple of 32, N of 8.  Codes quantised elsewhere can be laid out like this
+ * and used as well: quantize writes bytes 1 to 252, the others are read too.  A
+ * weight beyond float32's range (bytes 253 and 254, codes from 4 and from 2 on)
+ * counts as infinity, and a group under byte 255 as NaN, zeros included.
  *  quantize:   w [G, K, N] of `dtype` in (finite), mx out.  The scale is
  *              2^(floor(log2 max|w|) - 2), at least 2^-126; a code is the
  *              nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 times it (ties to the even
  *              code, magnitudes above 6 to 6).
- *  dequantize: mx in, w [G, K, N] of `dtype` out: code * scale, exact (for the
- *              calls that take plain matrices, such as a long prompt's).
+ *  dequantize: mx in, w [G, K, N] of `dtype` out: code * scale, exact, but
+ *              infinity and NaN as above (for the calls that take plain
+ *              matrices, such as a long prompt's).
  * moe_mx_bytes returns 0 for sizes outside the rules above. */
 size_t moe_mx_bytes(int G, int K, int N);
 int moe_mx_quantize(int G, int K, int N, int dtype, const void* w, void* mx, void* stream);

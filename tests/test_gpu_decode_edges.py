@@ -71,3 +71,84 @@ def test_x_up_to_the_largest_float_on_packed_weights(T):
     want = v[:, None] * 2.0 ** -100 / (1 + np.exp(-1.0))
     # exp and the division 2^-20 of it, a few additions
     assert (np.abs(b.out.double().cpu().numpy() - want) <= (2.0 ** -20 + 8 * 2.0 ** -23) * np.abs(want)).all()
+
+
+# ---------------------------------------------------------------- scale bytes
+
+def _every_scale(N=8):
+    """All 16 codes (shifted by the column) under every scale byte: packed, and float64 values."""
+    code = np.resize(np.arange(16, dtype=np.uint8), 32)[None, None, :, None] + np.arange(N, dtype=np.uint8)
+    code = np.broadcast_to(code & 15, (1, 256, 32, N)).copy()
+    s = np.broadcast_to((np.arange(256) - 127).reshape(1, 256, 1), (1, 256, N)).astype(np.int64)
+    return D.mx_pack(code, s), D.mx_values(code, s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dequantize_every_scale_byte(dtype):
+    """Byte b is 2^(b-127) from 0 to 254; a value beyond the type's range is infinity, 255 is NaN."""
+    packed, want = _every_scale()
+    back = torch.empty(1, 256 * 32, 8, dtype=DTYPE[dtype], device="cuda")
+    M.moe_mx_dequantize(1, 256 * 32, 8, torch.from_numpy(packed).cuda(), back)
+    got = back.double().cpu().numpy()
+    assert np.isnan(got[0, 255 * 32:]).all()
+    want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)[0, :255 * 32]
+    assert np.array_equal(got[0, :255 * 32], want)
+
+
+def _packed_layer(rng, E, H, I, top, scale):
+    """Packed weights with codes up to magnitude `top` in the matrices that `scale` gives a byte:
+    (device tensors, float64 values)."""
+    p, values = {}, {}
+    for name, K, N in (("w1", H, I), ("w3", H, I), ("w2", I, H)):
+        code = (rng.integers(0, top + 1, (E, K // 32, 32, N)) + 8 * rng.integers(0, 2, (E, K // 32, 32, N))).astype(np.uint8)
+        s = np.full((E, K // 32, N), scale[name] - 127, np.int64)
+        p[name], values[name] = torch.from_numpy(D.mx_pack(code, s)).cuda(), D.mx_values(code, s)
+    return p, values
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 7, 9, 17, 40])
+@pytest.mark.parametrize("byte,top", [(0, 7), (1, 7), (253, 5), (254, 3)])
+def test_decode_mx_smallest_and_largest_scales(T, byte, top, dtype):
+    """Weights under the scale bytes at both ends, as far as float32 holds their values (byte 253:
+    codes up to 3, 254: up to 1.5), in the first product and in the second."""
+    H, I = 96, 160
+    print(f"case scale byte {byte} T={T} {dtype}", flush=True)
+    rng = np.random.default_rng(17)
+    far = 100 if byte < 127 else -100      # brings the products back into the middle of the range
+    for scale, x_exp in ((dict(w1=124, w3=127 + far, w2=byte), 0), (dict(w1=124 - far, w3=byte, w2=127), far)):
+        p, values = _packed_layer(rng, 1, H, I, top, scale)
+        inp = {"logits": np.zeros((T, 1), np.float32)}
+        x = torch.from_numpy(rng.standard_normal((T, H)) * 2.0 ** x_exp).to(DTYPE[dtype])
+        inp["x"] = x.view(torch.int16).numpy().view(np.uint16) if dtype == "bf16" else x.numpy()
+        b = _decode(L.make_dims(T, H, 1, 1, I, 0, dtype), dict(p, x=x.cuda(), logits=torch.zeros(T, 1, device="cuda")))
+        ref = D.decode(inp, 1, dtype, values)
+        assert (np.abs(b.out.double().cpu().numpy() - ref["out"]) <= ref["bound"]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 7, 9, 17, 40])
+@pytest.mark.parametrize("byte,code", [(253, 7), (254, 12), (255, 0), (255, 3)])
+def test_decode_mx_values_beyond_the_range_stay_in_their_column(T, byte, code, dtype):
+    """An infinite or NaN weight of the second product makes its column of the rows that meet it
+    infinite or NaN, and changes nothing else."""
+    H, I, E = 96, 160, 2
+    print(f"case byte {byte} code {code} T={T} {dtype}", flush=True)
+    rng = np.random.default_rng(18)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(DTYPE[dtype]).cuda()
+    logits = torch.zeros(T, E, device="cuda")
+    logits[::2, 1] = 1.0                    # the even rows pick expert 1
+    p, _ = _packed_layer(rng, E, H, I, 7, dict(w1=124, w3=124, w2=124))
+    p.update(x=x, logits=logits)
+    clean = _decode(L.make_dims(T, H, E, 1, I, 0, dtype), p).out
+    w2 = p["w2"].clone()
+    groups, col = I // 32 * H, 33           # group 2 of expert 1's column 33
+    at = groups + 2 * H + col
+    w2[16 * at:16 * at + 16] = code * 17
+    w2[16 * E * groups + at] = byte
+    out = _decode(L.make_dims(T, H, E, 1, I, 0, dtype), dict(p, w2=w2)).out
+    hit = torch.zeros(T, H, dtype=torch.bool, device="cuda")
+    hit[::2, col] = True
+    assert torch.equal(out[~hit], clean[~hit]) and not out[hit].isfinite().any()
+    if byte == 255:
+        assert out[hit].isnan().all()
