@@ -381,7 +381,12 @@ int moe_route_bwd(const moe_dims* d, const float* dtopk_w, const float* topk_w,
  * A row's bits depend on its own logits and x, the weights and the dims (T
  * among them: the order of the sums is chosen by it), never on the other rows
  * of the batch.  An infinity or NaN in x or in a weight that a row meets makes
- * that row infinite or NaN (NaN, too, where exact arithmetic has an infinity). */
+ * that row infinite or NaN (NaN, too, where exact arithmetic has an infinity).
+ * A logit of -inf masks its expert: the row picks it, with weight 0, only if
+ * fewer than K others are left.  A row of logits that are all -inf picks experts
+ * 0 to K-1, and like a row with a logit of +inf it has NaN weights and hence a
+ * NaN out row (moe_route gives the same picks and weights).  NaN logits have no
+ * order: such a row picks K distinct experts, which ones is left open. */
 size_t moe_decode_workspace_bytes(const moe_dims* d);
 int moe_decode(const moe_dims* d, const float* logits, const void* x, const void* w1, const void* w3,
                const void* w2, const void* ws1, const void* ws3, const void* ws2,

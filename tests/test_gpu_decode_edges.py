@@ -152,3 +152,43 @@ def test_decode_mx_values_beyond_the_range_stay_in_their_column(T, byte, code, d
     assert torch.equal(out[~hit], clean[~hit]) and not out[hit].isfinite().any()
     if byte == 255:
         assert out[hit].isnan().all()
+
+
+# ---------------------------------------------------------------- logits without a finite one
+
+ROUTES = [  # T, E, K, Ns: picks in the product's blocks, in a launch of their own, in one block
+    (4, 8, 2, 0), (4, 100, 60, 1), (7, 8, 2, 1), (40, 64, 6, 0), (20, 100, 70, 0), (64, 64, 33, 1), (16, 256, 130, 0)]
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["plain", "mx"])
+@pytest.mark.parametrize("T,E,K,Ns", ROUTES)
+def test_rows_whose_mask_leaves_nothing(T, E, K, Ns, mx):
+    """All -inf: experts 0..K-1 and NaN weights, as with moe_route; +inf: NaN weights; the type's
+    lowest value in every place: equal weights.  The other rows keep their bits."""
+    print(f"case masked rows T={T} E={E} K={K} Ns={Ns} mx={mx}", flush=True)
+    H = I = 32
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    p = dict(logits=draw(T, E), x=draw(T, H), w1=draw(E, H, I), w3=draw(E, H, I), w2=draw(E, I, H))
+    if Ns:
+        p.update(ws1=draw(Ns, H, I), ws3=draw(Ns, H, I), ws2=draw(Ns, I, H))
+    q = L.quantize_weights(p) if mx else p
+    d = L.make_dims(T, H, E, K, I, Ns, "f32")
+    clean = _decode(d, q)
+    logits = p["logits"].clone()
+    logits[0] = float("-inf")
+    logits[1, E - 1] = float("inf")
+    logits[2] = torch.finfo(torch.float32).min
+    b = _decode(d, dict(q, logits=logits))
+    route = L.Buffers(d, backward=False)
+    L.route(route, dict(p, logits=logits))
+    torch.cuda.synchronize()
+    assert torch.equal(b.topk_idx, route.topk_idx)
+    assert torch.equal(b.topk_w.nan_to_num(2.0), route.topk_w.nan_to_num(2.0))
+    first = torch.arange(K, dtype=torch.int32, device="cuda")
+    assert torch.equal(b.topk_idx[0], first) and torch.equal(b.topk_idx[2], first) and b.topk_idx[1, 0] == E - 1
+    assert b.topk_w[:2].isnan().all() and b.out[:2].isnan().all()
+    # K equal exponentials: their sum is exact, so only the division rounds
+    assert (b.topk_w[2].double() * K - 1).abs().max() <= 2.0 ** -23 and b.out[2].isfinite().all()
+    for name in ("out", "topk_idx", "topk_w"):
+        assert torch.equal(getattr(b, name)[3:], getattr(clean, name)[3:]), name
