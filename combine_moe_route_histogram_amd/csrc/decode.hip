@@ -1113,57 +1113,65 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int s
   if (c < a.H) store_out<BF16>(a, t, c, combine_items(a, slices, t, c, 0, 1));
 }
 
-template <int F, bool UP, int NT, int CW, bool MANY, bool CACHED>
-hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  const int tiles = UP ? p.up_tiles : p.down_tiles, slices = UP ? 1 : p.slices;
-  const int steps = UP ? (a.H + fmt_step(F) - 1) / fmt_step(F) : p.slice_steps;
-  constexpr int halves = MANY ? kMaxRowTile / (16 * NT) : 1;
-  const dim3 grid(halves > 1 ? (tiles + kXcds - 1) / kXcds * kXcds * halves : tiles, p.entries, slices);
-  if (UP ? p.head : p.tail) {
-    static_assert(kTailTokens <= 8, "the tail's entries have 16 rows at most");
-    if constexpr (UP || NT == 1)
-      decode_ffn_kernel<F, UP, NT, CW, true, MANY, CACHED><<<grid, kThreads, 0, st>>>(a, slices, steps);
+// The kernels that are built: what decode_plan can ask for.
+constexpr bool kernel_built(int f, bool up, int nt, int cw, bool fused, bool many, bool cached) {
+  if (many ? f == kFmtMxF32 || nt != (f == kFmtBf16 && !up ? 2 : 4) || !cached : nt > 2 || (cached && fmt_mx(f))) return false;
+  if (fmt_mx(f) && (nt == 1) == (cw == 4)) return false;   // 1 and 2 column tiles; with rows by way of LDS, 4
+  static_assert(8 * kMaxExperts <= kListPairs && kTailTokens <= 8);
+  if (up) return fused || row_tile_of(f, nt) != 8;         // up to 8 tokens every block makes the list
+  return !fused || (nt == 1 && !many);                     // the output's sum inside: up to kTailTokens
+}
+
+template <int F, bool UP, int NT, int CW, bool FUSED, bool MANY, bool CACHED>
+hipError_t launch_kernel(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
+  if constexpr (!kernel_built(F, UP, NT, CW, FUSED, MANY, CACHED)) {
+    return hipErrorInvalidValue;
   } else {
-    decode_ffn_kernel<F, UP, NT, CW, false, MANY, CACHED><<<grid, kThreads, 0, st>>>(a, slices, steps);
-  }
-  return hipGetLastError();
-}
-template <int F, bool UP, int NT, bool MANY, bool CACHED>
-hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if constexpr (fmt_mx(F) && NT >= 2) return launch_product<F, UP, NT, 4, MANY, CACHED>(a, p, st);
-  else switch (UP ? p.up_width : p.down_width) {
-    case 1: return launch_product<F, UP, NT, 1, MANY, CACHED>(a, p, st);
-    case 2: return launch_product<F, UP, NT, 2, MANY, CACHED>(a, p, st);
-    default: return launch_product<F, UP, NT, 4, MANY, CACHED>(a, p, st);
+    const int tiles = UP ? p.up_tiles : p.down_tiles, slices = UP ? 1 : p.slices;
+    const int steps = UP ? (a.H + fmt_step(F) - 1) / fmt_step(F) : p.slice_steps;
+    constexpr int halves = MANY ? kMaxRowTile / (16 * NT) : 1;
+    const dim3 grid(halves > 1 ? (tiles + kXcds - 1) / kXcds * kXcds * halves : tiles, p.entries, slices);
+    decode_ffn_kernel<F, UP, NT, CW, FUSED, MANY, CACHED><<<grid, kThreads, 0, st>>>(a, slices, steps);
+    return hipGetLastError();
   }
 }
-// Weights are read past the caches (through them the calls take 5 to 12 % longer)
-// unless others read the same lines: other entries of the expert (kManyRows), or
-// the tiles to the left and right where rows do not begin on a line ([2816,
-// 2840] x 8 in 26 experts, one token 110.6 us past, 105.8 through the caches;
-// [584, 2632] x 8 in 100, 14 tokens 172 and 154; [2048, 1400] x 4 in 32, 2
-// tokens 44.6 and 39.2).
+template <int F, bool UP, int NT, int CW, bool FUSED>
+hipError_t launch_kernel(const DecodeArgs& a, const DecodePlan& p, const DecodeKernel& k, hipStream_t st) {
+  if (k.many) return launch_kernel<F, UP, NT, CW, FUSED, true, true>(a, p, st);
+  return k.cached ? launch_kernel<F, UP, NT, CW, FUSED, false, true>(a, p, st)
+                  : launch_kernel<F, UP, NT, CW, FUSED, false, false>(a, p, st);
+}
+template <int F, bool UP, int NT>
+hipError_t launch_kernel(const DecodeArgs& a, const DecodePlan& p, const DecodeKernel& k, hipStream_t st) {
+  switch (k.width) {
+    case 1: return k.fused ? launch_kernel<F, UP, NT, 1, true>(a, p, k, st) : launch_kernel<F, UP, NT, 1, false>(a, p, k, st);
+    case 2: return k.fused ? launch_kernel<F, UP, NT, 2, true>(a, p, k, st) : launch_kernel<F, UP, NT, 2, false>(a, p, k, st);
+    case 4: return k.fused ? launch_kernel<F, UP, NT, 4, true>(a, p, k, st) : launch_kernel<F, UP, NT, 4, false>(a, p, k, st);
+    default: return hipErrorInvalidValue;
+  }
+}
 template <int F, bool UP>
 hipError_t launch_product(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if constexpr (F != kFmtMxF32)
-    if (p.row_tile == kMaxRowTile) return launch_product<F, UP, F == kFmtBf16 && !UP ? 2 : 4, true, true>(a, p, st);
-  if constexpr (!fmt_mx(F))
-    if ((int64_t)(UP ? a.I : a.H) * (fmt_f32(F) ? 4 : 2) % kLineBytes)
-      return p.row_tile < 32 ? launch_product<F, UP, 1, false, true>(a, p, st) : launch_product<F, UP, 2, false, true>(a, p, st);
-  return p.row_tile < 32 ? launch_product<F, UP, 1, false, false>(a, p, st) : launch_product<F, UP, 2, false, false>(a, p, st);
+  const DecodeKernel& k = UP ? p.up : p.down;
+  switch (k.row_tiles) {
+    case 1: return launch_kernel<F, UP, 1>(a, p, k, st);
+    case 2: return launch_kernel<F, UP, 2>(a, p, k, st);
+    case 4: return launch_kernel<F, UP, 4>(a, p, k, st);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 template <int F>
 hipError_t launch_fmt(const DecodeArgs& a, const DecodePlan& p, hipStream_t st) {
-  if (!p.head || a.picked) {
-    if (p.head) decode_topk_kernel<<<(a.T + kWaves - 1) / kWaves, kThreads, 0, st>>>(a);
+  if (!p.up.fused || a.picked) {
+    if (p.up.fused) decode_topk_kernel<<<(a.T + kWaves - 1) / kWaves, kThreads, 0, st>>>(a);
     else decode_route_kernel<<<1, kRouteThreads, 0, st>>>(a, p.row_tile, p.entries);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   hipError_t e = launch_product<F, true>(a, p, st);
   if (e == hipSuccess) e = launch_product<F, false>(a, p, st);
-  if (p.tail || e != hipSuccess) return e;
+  if (p.down.fused || e != hipSuccess) return e;
   decode_combine_kernel<!fmt_f32(F)><<<dim3((a.H / 4 + 255) / 256, a.T), 256, 0, st>>>(a, p.slices);
   return hipGetLastError();
 }
@@ -1187,15 +1195,30 @@ static int tile_width(bool mx, int row_tile, int64_t row_bytes, int columns, int
   return 1;
 }
 
+// Weights are read past the caches (through them the calls take 5 to 12 % longer)
+// unless others read the same lines: other entries of the expert (kManyRows), or
+// the tiles to the left and right where rows do not begin on a line ([2816,
+// 2840] x 8 in 26 experts, one token 110.6 us past, 105.8 through the caches;
+// [584, 2632] x 8 in 100, 14 tokens 172 and 154; [2048, 1400] x 4 in 32, 2
+// tokens 44.6 and 39.2).
+static DecodeKernel decode_kernel(int f, bool up, int row_tile, int64_t row_bytes, int width, bool fused) {
+  DecodeKernel k;
+  k.many = row_tile == kMaxRowTile;
+  k.row_tiles = k.many ? (f == kFmtBf16 && !up ? 2 : 4) : row_tile < 32 ? 1 : 2;
+  k.width = width;
+  k.fused = fused;
+  k.cached = k.many || (!fmt_mx(f) && row_bytes % kLineBytes);
+  return k;
+}
+
 DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I, int Ns) {
   const int f = mx ? (is_bf16 ? kFmtMxBf16 : kFmtMxF32) : (is_bf16 ? kFmtBf16 : kFmtF32);
   const int tile = 16 * fmt_groups(f), step = fmt_step(f), size = is_bf16 ? 2 : 4;
   DecodePlan p;
   p.row_tile = T <= row_tile_of(f, 1) ? row_tile_of(f, 1) : row_tile_of(f, 2);
   const int64_t R = (int64_t)T * K;
-  p.head = R <= kListPairs;
+  const bool head = R <= kListPairs, tail = T <= kTailTokens;
   p.picked = T > kHeadTokens || R > kThreads;
-  p.tail = T <= kTailTokens;
   // experts with rows as expected of even routing, and the shared ones
   double miss = 1.0;
   for (int t = 0; t < T; ++t) miss *= 1.0 - (double)K / E;
@@ -1207,11 +1230,14 @@ DecodePlan decode_plan(bool is_bf16, bool mx, int T, int H, int E, int K, int I,
   const int busy = (int)(R < E ? R : E);   // experts with rows, at most
   // an expert with c rows has at most 1 + (c - 1) / row_tile entries
   p.entries = busy + (int)((R - busy) / p.row_tile) + Ns * ((T + p.row_tile - 1) / p.row_tile);
-  p.up_width = tile_width(mx, p.row_tile, (int64_t)I * size, I, tile / 2, groups);
-  p.up_tiles = (I + p.up_width * tile / 2 - 1) / (p.up_width * tile / 2);
+  const int64_t up_bytes = (int64_t)I * size, down_bytes = (int64_t)H * size;
+  const int up_width = tile_width(mx, p.row_tile, up_bytes, I, tile / 2, groups);
+  p.up_tiles = (I + up_width * tile / 2 - 1) / (up_width * tile / 2);
+  p.up = decode_kernel(f, true, p.row_tile, up_bytes, up_width, head);
   const int steps = (I + step - 1) / step, most = steps < kMaxSlices ? steps : kMaxSlices;
-  p.down_width = tile_width(mx, p.row_tile, (int64_t)H * size, H, tile, groups * (most < 2 ? most : 2));
-  p.down_tiles = (H + p.down_width * tile - 1) / (p.down_width * tile);
+  const int down_width = tile_width(mx, p.row_tile, down_bytes, H, tile, groups * (most < 2 ? most : 2));
+  p.down_tiles = (H + down_width * tile - 1) / (down_width * tile);
+  p.down = decode_kernel(f, false, p.row_tile, down_bytes, down_width, tail);
   int s = (int)(kSliceBlocks / (p.down_tiles * groups) + 0.999);
   s = s < 1 ? 1 : s > most ? most : s;
   p.slice_steps = (steps + s - 1) / s;

@@ -22,16 +22,21 @@ constexpr int kDecodeMaxDim = 1 << 20;
 constexpr int kMxGroup = 32;
 constexpr int kMxCodeBytes = 16;
 
-// Where the down projection's partial sums are cut: S slices of `steps` k
-// steps each.
+// Which of the built kernels one of the two products runs.
+struct DecodeKernel {
+  int row_tiles;  // 16-row operands of a block (1, 2 or 4)
+  int width;      // column tiles its waves span (1, 2 or 4)
+  bool fused;     // gate/up: its blocks list the work for themselves; down: its last ones add up the output
+  bool many;      // entries of 64 rows
+  bool cached;    // weights through the caches
+};
+
+// How a call is cut.
 struct DecodePlan {
-  bool head;        // the first product's blocks list the work for themselves
-  bool picked;      // with head: the top-k has a launch of its own
-  bool tail;        // the second product's last blocks add up the output
+  DecodeKernel up, down;   // gate/up and down projection
+  bool picked;      // with up.fused: the top-k has a launch of its own
   int row_tile;     // rows of one entry at most (8, 16, 32 or 64)
   int entries;      // bound on the number of entries (expert x row tile)
-  int up_width;     // column tiles a block's waves span (1, 2 or 4): gate/up projection
-  int down_width;   // and down projection
   int up_tiles;     // blocks' column tiles of the gate/up projection
   int down_tiles;   // column tiles of the down projection
   int slices;       // k slices of the down projection

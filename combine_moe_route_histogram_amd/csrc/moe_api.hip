@@ -380,7 +380,7 @@ int decode(const moe_dims* d, bool mx, const float* logits, const void* x, const
   a.n_entries = ws_at<int32_t>(ws, L.n_entries);
   a.lists = ws_at<int32_t>(ws, L.lists);
   a.done = ws_at<int32_t>(ws, L.done);
-  a.n_done = p.tail ? p.down_tiles : 0;
+  a.n_done = p.down.fused ? p.down_tiles : 0;
   a.picked = p.picked;
   a.h = ws_at<char>(ws, L.h);
   a.y = ws_at<float>(ws, L.y);
