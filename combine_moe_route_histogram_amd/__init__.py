@@ -494,6 +494,8 @@ def _mx_dtype(w):
     """MOE_F32 or MOE_BF16 of a weight tensor, and its torch type (None: bf16, the call reports the NULL)."""
     if w is None:
         return BF16, None
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor or None")
     for code, dt in _TORCH_DTYPE.items():
         if w.dtype is dt:
             return code, dt
