@@ -486,8 +486,20 @@ def _mx_numel(G, K, N):
     return G * K * N // 32 * 17
 
 
+def _fits_int32(v) -> bool:
+    return -2 ** 31 <= v < 2 ** 31
+
+
 def moe_mx_bytes(G: int, K: int, N: int) -> int:
-    return int(load().moe_mx_bytes(G, K, N))
+    # ctypes would drop the bits above 32
+    return int(load().moe_mx_bytes(G, K, N)) if _fits_int32(G) and _fits_int32(K) and _fits_int32(N) else 0
+
+
+def _check_mx_sizes(G, K, N):
+    """The C call must see the sizes that the tensors are held against: ctypes drops bits above 32."""
+    for name, v in (("G", G), ("K", K), ("N", N)):
+        if not _fits_int32(v):
+            raise ValueError(f"{name} must fit into 32 bits (got {v})")
 
 
 def _mx_dtype(w):
@@ -503,12 +515,14 @@ def _mx_dtype(w):
 
 
 def moe_mx_quantize(G: int, K: int, N: int, w, mx, stream=None):
+    _check_mx_sizes(G, K, N)
     code, dt = _mx_dtype(w)
     _launch("moe_mx_quantize", stream, (G, K, N, code),
             ((w, "w", dt, G * K * N), (mx, "mx", torch.uint8, _mx_numel(G, K, N))), ())
 
 
 def moe_mx_dequantize(G: int, K: int, N: int, mx, w, stream=None):
+    _check_mx_sizes(G, K, N)
     code, dt = _mx_dtype(w)
     _launch("moe_mx_dequantize", stream, (G, K, N, code),
             ((mx, "mx", torch.uint8, _mx_numel(G, K, N)), (w, "w", dt, G * K * N)), ())

@@ -13,3 +13,17 @@ def test_mx_weights_that_are_no_tensor(w):
         M.moe_mx_quantize(1, 32, 8, w, mx)
     with pytest.raises(TypeError, match="w must be a torch.Tensor"):
         M.moe_mx_dequantize(1, 32, 8, mx, w)
+
+
+@pytest.mark.parametrize("sizes", [(1 + 2 ** 32, 32, 8), (1 - 2 ** 32, 32, 8), (1, 32 + 2 ** 32, 8), (1, 32, 8 - 2 ** 32),
+                                   (2 ** 31, 32, 8)])
+def test_mx_sizes_beyond_32_bits(sizes, monkeypatch):
+    """A size whose low 32 bits are a good one: the call must not go out with those (the tensors
+    were held against the whole size: a negative one asks for no element)."""
+    monkeypatch.setattr(M, "_launch", lambda *a: pytest.fail("launched"))
+    w, mx = torch.zeros(256), torch.zeros(136, dtype=torch.uint8)
+    assert M.moe_mx_bytes(*sizes) == 0
+    with pytest.raises(ValueError, match="must fit into 32 bits"):
+        M.moe_mx_quantize(*sizes, w, mx)
+    with pytest.raises(ValueError, match="must fit into 32 bits"):
+        M.moe_mx_dequantize(*sizes, mx, w)
