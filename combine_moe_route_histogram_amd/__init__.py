@@ -199,9 +199,16 @@ def _ptr(t, name, dtype=None, numel=None):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (3 us a call), in the versions of
+# torch that have it: it is not part of torch's public interface.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:   # the current stream's handle without a Stream object around it (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -27,3 +27,14 @@ def test_mx_sizes_beyond_32_bits(sizes, monkeypatch):
         M.moe_mx_quantize(*sizes, w, mx)
     with pytest.raises(ValueError, match="must fit into 32 bits"):
         M.moe_mx_dequantize(*sizes, mx, w)
+
+
+def test_current_stream_without_the_private_call(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(M, "_raw_stream", None)
+    assert M._stream(None) == 77
+    monkeypatch.setattr(M, "_raw_stream", lambda device: 78 + device)
+    assert M._stream(None) == 78 and M._stream(5) == 5
