@@ -464,7 +464,7 @@ struct Stage {
 
 // A lane's place: its column(s) in row 0 of the matrix it reads, and its rows.
 // Lanes without a column or a row of their own repeat a valid one.
-template <int F, bool UP, int NT, bool CACHED>
+template <int F, bool UP, int NT>
 struct Lane {
   const char* w[fmt_mx(F) && UP ? 2 : 1];   // 4 bit: in W1 and W3 (up) or in W2
   const char* sc;                           // 4 bit: this lane's 4 scales in row 0
@@ -484,11 +484,12 @@ __device__ __forceinline__ u32x4 ld16_global(uint64_t address) {
 // Nothing here is conditional: behind a branch the compiler no longer knows
 // how many loads are in flight and waits for all of them before the next step
 // is computed.  Weights outside the matrix repeat the last ones inside: what
-// comes of such columns is not stored, and rows at or behind `limit` meet
-// zeros.
+// comes of such columns is not stored, and of the rows' values, places at or
+// behind Kd are zeros, so weights repeated along k add nothing.  A step behind
+// the wave's last one (real = false) loads zeros for both.
 constexpr int step_len(int f) { return fmt_mx(f) ? kMxGroup : 8; }   // a lane's rows in one k step
 template <int F, bool UP, int NT, bool CACHED, class S>
-__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT, CACHED>& L, int step, int q, int Kd, int N,
+__device__ __forceinline__ void load_weights(S& s, const Lane<F, UP, NT>& L, int step, int q, int Kd, int N,
                                              bool real = true) {
   const int k = min(fmt_step(F) * step + step_len(F) * q, Kd - step_len(F));
   const uint64_t zeros = reinterpret_cast<uint64_t>(kZeros);
@@ -522,7 +523,7 @@ __device__ __forceinline__ int mx_h_place(int c) {
 }
 
 template <int F, bool UP, int NT, bool CACHED, int NTL, int P>
-__device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT, CACHED>& L, int step, int q,
+__device__ __forceinline__ void load_stage(Stage<F, P, NTL>& s, const Lane<F, UP, NT>& L, int step, int q,
                                            int Kd, int N, bool real, int64_t plane) {
   constexpr int V = act_vecs(F, P), B = fmt_f32(F) ? 4 : 2, LEN = step_len(F);
   constexpr int PER = LEN * B / 16;   // vectors of a lane's values from one plane
@@ -638,7 +639,7 @@ __device__ __forceinline__ void mma_stage(const Stage<F, P, NTL>& s, int lane, f
 // that load zeros from one place.  (The barriers keep the scheduler from
 // moving loads up, into registers of their own.)
 template <int F, bool UP, int NT, bool CACHED, int NTL, int P = act_parts(F, UP)>
-__device__ __forceinline__ void product_loop(const Lane<F, UP, NT, CACHED>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
+__device__ __forceinline__ void product_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int first,
                                              int stride, int end, int lane, int Kd, int N, int64_t plane) {
   constexpr int S = kStages;
   const int q = lane >> 4;
@@ -676,21 +677,21 @@ constexpr int kActPitch = 128 * 2 + 16;   // bytes of a row in LDS: 16 rows' vec
 template <int F, bool UP, int NT>
 constexpr int act_bytes() { return act_parts(F, UP) * 16 * NT * kActPitch; }
 
-template <int F, bool UP, int NT>
+template <int F>
 struct WeightStage {
   u32x4 w[fmt_groups(F)];
   uint32_t s;
 };
 
 template <int F, bool UP, int NT, bool CACHED, int NTL>
-__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, CACHED>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
+__device__ __forceinline__ void shared_loop(const Lane<F, UP, NT>& L, f32x4 (&acc)[NT][fmt_groups(F)], int begin,
                                             int end, int tid, int Kd, int N, int64_t plane,
                                             const char* const (&src)[NT], char* lds) {
   constexpr int P = act_parts(F, UP), B = fmt_f32(F) ? 4 : 2, VECS = F == kFmtMxF32 ? 2 : P;
   const int lane = tid & (kWave - 1), m = lane & 15, q = lane >> 4, piece = tid & 15, row = tid >> 4;
-  WeightStage<F, UP, NT> s0, s1;
+  WeightStage<F> s0, s1;
   u32x4 v[NTL][VECS];   // this thread's 8 values of rows tid / 16, 16 + tid / 16
-  auto load_w = [&](WeightStage<F, UP, NT>& s, int k) {
+  auto load_w = [&](WeightStage<F>& s, int k) {
     load_weights<F, UP, NT, CACHED>(s, L, k, q, Kd, N);
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -726,7 +727,7 @@ __device__ __forceinline__ void shared_loop(const Lane<F, UP, NT, CACHED>& L, f3
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto mma = [&](const WeightStage<F, UP, NT>& s, int buf) {
+  auto mma = [&](const WeightStage<F>& s, int buf) {
     const char* base = lds + buf * act_bytes<F, UP, NT>() + m * kActPitch + q * (UP ? 64 : 16);
     float sc[fmt_groups(F)];
     lane_scales<F, UP>(s.s, lane, sc);
@@ -907,7 +908,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 && F != kFmtMxF32 ? 4 : 2) void d
   int col0 = tile * COLS + wave % CW * WCOLS;   // the wave's first column
   if constexpr (SHARED) col0 = min(col0, N - 32);   // all waves work: nothing is stored for one behind the end
 
-  Lane<F, UP, NT, CACHED> L;
+  Lane<F, UP, NT> L;
   if constexpr (fmt_mx(F)) {
     const int64_t one = (int64_t)(Kd / kMxGroup) * N;   // groups of 32 of one matrix
 #pragma unroll
