@@ -4,18 +4,19 @@
 //   a = x_t W1_e, b = x_t W3_e, h = silu(a) b, y = h W2_e      for e in idx[t] and the shared experts
 //   out[t] = sum_k g[t,k] y_k + sum_s y_s
 //
-// Bound: the bytes of the picked experts' weights, each read once.  An expert
-// has a handful of rows, so the products are matrix times a few vectors; they
+// Bound: the bytes of the picked experts' weights, read once for every entry of
+// 8 to 64 rows that an expert has (see row_tile_of), so once where its rows fit
+// into one.  An expert has a handful of rows, so the products are matrix times a few vectors; they
 // run on MFMA all the same, with the weights as the 16-row operand and the
 // (zero-padded) rows as the 16-column one: the matrix cores are idle
 // otherwise, and one instruction takes the place of 16 x rows
 // multiply-adds.  The weights go from memory to registers without LDS.
 //
 // Measured (times of a call, launches and gaps included; streaming reads reach
-// 6.9 TB/s on this card): bf16 [4096, 14336] x 2 in 8 experts, 32 tokens 439 us,
-// 6.4 TB/s; [2048, 1408] x 6 in 64 experts and 2 shared ones, one token 30.9 us,
+// 6.9 TB/s on this card): bf16 [4096, 14336] x 2 in 8 experts, 32 tokens 440 us,
+// 6.4 TB/s; [2048, 1408] x 6 in 64 experts and 2 shared ones, one token 30.5 us,
 // 4.5 TB/s, of which the routing, the two launches and the sum are about 7;
-// 4-bit weights, the same 17.1 and, 200 tokens of 4 in 32 experts, 59 us.
+// 4-bit weights, the same 17.0 and, 200 tokens of 4 in 32 experts, 58 us.
 #include "common.hpp"
 #include "decode.hpp"
 #include "kernels.hpp"
@@ -28,21 +29,35 @@ constexpr int kWaves = 4;               // waves of a product block
 constexpr int kThreads = kWaves * kWave;
 constexpr int kRedRows = 8;             // rows whose sums go through LDS at once
 constexpr int kRouteThreads = 1024;
-// Up to kHeadTokens the first product's blocks pick the experts for themselves
-// (a launch of its own for it, with [2048, 1408] x 6 in 64 experts: one token
-// 30.8 -> 33.6 us, 4 tokens 76.6 -> 78.4, 8 tokens 119.7 both), up to kTailTokens
-// the second product's last blocks add up the output (own launch: 31.0 -> 35.5 us,
-// 76.6 both; 4 bit, 4 tokens 30.3 -> 32.2; 8 tokens inside 123.2, own launch 119.7).
+
+// The thresholds below, against other values: time of a call relative to the
+// value that stands, mean (least to most) over the calls that it changes, of ten
+// layers ([128, 256] x 2 in 8 experts; [224, 960] x 6 in 42 and 2 shared; [512,
+// 2048] x 2 in 16 and 1; [1024, 4096] x 4 in 16; [2048, 1408] x 4 in 32; x 6 in
+// 64 and 2; [2880, 2880] x 4 in 32; [3712, 928] x 3 in 8 and 1; [4096, 2048] x 8
+// in 64 and 1; [4096, 14336] x 2 in 8), all four formats, 1 to 256 tokens.
+//
+// Up to kHeadTokens the first product's blocks pick the experts for themselves,
+// up to kTailTokens the second product's last blocks add up the output; beyond,
+// each has a launch.  1 in the place of 4 tokens: picks 1.07 (0.97 to 1.24), sum
+// 1.09 (0.97 to 1.59).  8: picks 0.98 (0.85 to 1.07: small layers gain, [224, 960]
+// f32 loses), sum 0.97 (0.85 to 1.06).
 constexpr int kHeadTokens = 4;
 constexpr int kTailTokens = 4;
+// A block's width (see tile_width).  Rows of kLongRow bytes or more are long:
+// 2048 1.07 (0.94 to 1.43), 8192 0.97 (0.82 to 1.11; f32 0.96, bf16 0.98).  Blocks
+// that a width has to leave, long rows: 110 1.00 (0.75 to 1.30), 440 0.98 (0.82 to
+// 1.12; the largest layer up to 1.12).  Short rows: 256 1.04 (0.95 to 1.09), 1024
+// 0.98 (0.87 to 1.02; 12 calls).
 constexpr int64_t kLongRow = 4096;      // bytes
 constexpr int kLineBytes = 128;         // what the memory moves at once
 constexpr double kFillBlocks = 220, kManyBlocks = 512;
 // The down projection is cut along k for so many blocks, into so many slices at
-// most.  (150, 220 and 280 blocks, over 132 calls of five layers, all formats,
-// 1 to 128 tokens: 0.6, 1.1 and 1.2 % longer in the mean; bf16 [4096, 14336] x 2
-// in 8 experts, 32 tokens 455 -> 510, 520, 465 us, f32 [2048, 1408] x 4 in 32, 8
-// tokens 149 -> 129, 140, 140.)
+// most.  150 blocks 0.98 (0.74 to 1.28): calls whose blocks are many already gain
+// ([2048, 1408] x 4 in 32, f32, 8 tokens 146 -> 124 us), those of few, large
+// experts lose (bf16 [4096, 14336] x 2 in 8, 32 and 64 tokens 437 -> 496, 464 ->
+// 536; f32 [1024, 4096] x 4 in 16, 128 tokens 346 -> 445); no format gains or
+// loses as a whole (0.98 to 0.99 each).
 constexpr double kSliceBlocks = 400;
 constexpr int kMaxSlices = 8;
 
@@ -434,7 +449,12 @@ __device__ __forceinline__ void split_bf16(const float* f, u32x4* part) {
 // 2064, 3854 and 3293.  4 bit bf16 [4096, 14336] x 2 in 8, 24, 32 and 64 rows:
 // 181 and 178, 225 and 201, 358 and 313; [2048, 1408] x 4 in 32, 8 and 32 rows:
 // 44.0 and 46.7, 72.7 and 67.1; but with one expert of 64 rows, which leaves 112
-// blocks, 58 and 76: there the 32.)  Two bf16 parts of 64 rows do not fit into
+// blocks, 58 and 76: there the 32.)  Shared experts do not count: they have all T
+// rows and so several entries of 32 beyond 32 tokens, but entries of 64 for their
+// sake take 1.19 times as long in the mean (0.92 to 1.83, 43 calls of the five
+// layers above that have some), and weights through the caches 0.99 (plain
+// formats; [2048, 1408] x 6 in 64 and 2, bf16, 64 tokens 212 -> 226 us, 256 tokens
+// 278 -> 260).  Two bf16 parts of 64 rows do not fit into
 // the registers of the plain products: there two blocks next to each other on
 // one chiplet take 32 of an entry's rows each.  Three parts of them (f32 on 4
 // bit) would take two thirds of a CU's LDS.

@@ -361,10 +361,13 @@ int moe_route_bwd(const moe_dims* d, const float* dtopk_w, const float* topk_w,
 
 /* The whole layer for a few tokens (generation), logits to out, in one call:
  * moe_route's top-k and weights, the experts' SwiGLU FFN for the rows each
- * token picked, the shared experts, and moe_combine's sum.  It reads the
- * weights of the experts that have a token, once each, and nothing of the
- * others.  T <= 256, H and I <= 2^20 (else MOE_EUNSUPPORTED); larger batches
- * go through the calls above.
+ * token picked, the shared experts, and moe_combine's sum.  Of the experts'
+ * weights it reads those with a token, once for every 8, 16, 32 or 64 rows that
+ * an expert has (8 or 16 where T is no more, 64 where T*K >= 32 E, but 32 for
+ * float32 rows on 4-bit weights and where blocks would be few), so once where its
+ * rows fit.  T <= 256, H and I <= 2^20 (else MOE_EUNSUPPORTED); larger batches go
+ * through the calls above, which overtake this one earlier where the experts are
+ * few and large (bf16 [4096, 14336], 2 in 8: at 128 tokens).
  *  logits [T, E] f32, x [T, H], weights as for moe_expert_ffn (ws1, ws3, ws2
  *           NULL if n_shared = 0) in
  *  n_tokens device int32[1] in, or NULL: the number of rows in use, for batches
