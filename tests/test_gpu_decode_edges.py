@@ -192,3 +192,53 @@ def test_rows_whose_mask_leaves_nothing(T, E, K, Ns, mx):
     assert (b.topk_w[2].double() * K - 1).abs().max() <= 2.0 ** -23 and b.out[2].isfinite().all()
     for name in ("out", "topk_idx", "topk_w"):
         assert torch.equal(getattr(b, name)[3:], getattr(clean, name)[3:]), name
+
+
+# ---------------------------------------------------------------- streams and graphs
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_packing_replays_eager_bits(dtype):
+    """Packing and unpacking captured into one graph: replays see new weights, with eager work and
+    synchronizations between them."""
+    G, K, N = 3, 96, 1000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w = torch.randn(G, K, N, generator=g, device="cuda").to(DTYPE[dtype])
+    make = lambda: (torch.empty(M.moe_mx_bytes(G, K, N), dtype=torch.uint8, device="cuda"), torch.empty_like(w))
+
+    def both(mx, back):
+        M.moe_mx_quantize(G, K, N, w, mx)
+        M.moe_mx_dequantize(G, K, N, mx, back)
+    mx, back = make()
+    both(mx, back)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(mx, back)
+    for rep in range(4):
+        w.copy_(torch.randn(G, K, N, generator=g, device="cuda") * 10.0 ** (rep - 2))
+        eager = make()
+        both(*eager)
+        mx.zero_()
+        back.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(mx, eager[0]) and torch.equal(back, eager[1]), rep
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_streams_by_handle_and_current(T):
+    """A stream given as torch's object, as its raw handle, and as the current one."""
+    H, I, E = 64, 96, 4
+    g = torch.Generator(device="cuda").manual_seed(5)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    p = dict(logits=draw(T, E), x=draw(T, H), w1=draw(E, H, I), w3=draw(E, H, I), w2=draw(E, I, H))
+    d = L.make_dims(T, H, E, 2, I, 0, "f32")
+    want = _decode(d, p).out
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, None):
+        b = L.DecodeBuffers(d)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side if stream is None else torch.cuda.current_stream()):
+            L.decode(b, p, stream=stream)
+        side.synchronize()
+        assert torch.equal(b.out, want)
