@@ -6,10 +6,10 @@
 //
 // Bound: the bytes of the picked experts' weights, read once for every entry of
 // 8 to 64 rows that an expert has (see row_tile_of), so once where its rows fit
-// into one.  An expert has a handful of rows, so the products are matrix times a few vectors; they
-// run on MFMA all the same, with the weights as the 16-row operand and the
-// (zero-padded) rows as the 16-column one: the matrix cores are idle
-// otherwise, and one instruction takes the place of 16 x rows
+// into one.  An expert has a handful of rows, so the products are matrix times a
+// few vectors; they run on MFMA all the same, with the weights as the 16-row
+// operand and the (zero-padded) rows as the 16-column one: the matrix cores are
+// idle otherwise, and one instruction takes the place of 16 x rows
 // multiply-adds.  The weights go from memory to registers without LDS.
 //
 // Measured (times of a call, launches and gaps included; streaming reads reach
@@ -44,6 +44,7 @@ constexpr int kRouteThreads = 1024;
 // f32 loses), sum 0.97 (0.85 to 1.06).
 constexpr int kHeadTokens = 4;
 constexpr int kTailTokens = 4;
+//
 // A block's width (see tile_width).  Rows of kLongRow bytes or more are long:
 // 2048 1.07 (0.94 to 1.43), 8192 0.97 (0.82 to 1.11; f32 0.96, bf16 0.98).  Blocks
 // that a width has to leave, long rows: 110 1.00 (0.75 to 1.30), 440 0.98 (0.82 to
@@ -52,6 +53,7 @@ constexpr int kTailTokens = 4;
 constexpr int64_t kLongRow = 4096;      // bytes
 constexpr int kLineBytes = 128;         // what the memory moves at once
 constexpr double kFillBlocks = 220, kManyBlocks = 512;
+//
 // The down projection is cut along k for so many blocks, into so many slices at
 // most.  150 blocks 0.98 (0.74 to 1.28): calls whose blocks are many already gain
 // ([2048, 1408] x 4 in 32, f32, 8 tokens 146 -> 124 us), those of few, large
