@@ -23,7 +23,8 @@ __all__ = [
     "moe_expert_ffn_bwd_input", "moe_expert_ffn_bwd_weight_gate_up", "moe_expert_ffn_bwd_weight_down",
     "moe_expert_ffn_bwd", "moe_sync_status", "moe_route_noalloc", "Tuning", "moe_get_tuning",
     "moe_tuning_predict", "moe_decode_workspace_bytes", "moe_decode", "moe_decode_mx", "moe_mx_bytes",
-    "moe_mx_quantize", "moe_mx_dequantize",
+    "moe_mx_quantize", "moe_mx_dequantize", "moe_balance_workspace_bytes", "moe_balance", "moe_balance_bwd",
+    "Newton", "MuonParams", "NEWTON_COEF", "moe_muon_workspace_bytes", "moe_orthogonalize", "moe_muon",
 ]
 
 F32, BF16 = 0, 1
@@ -533,3 +534,135 @@ def moe_mx_dequantize(G: int, K: int, N: int, mx, w, stream=None):
     code, dt = _mx_dtype(w)
     _launch("moe_mx_dequantize", stream, (G, K, N, code),
             ((mx, "mx", torch.uint8, _mx_numel(G, K, N)), (w, "w", dt, G * K * N)), ())
+
+
+# ---------------------------------------------------------------- router losses
+
+def moe_balance_workspace_bytes(d: Dims, seq_len: int) -> int:
+    return int(load().moe_balance_workspace_bytes(ctypes.byref(d), seq_len)) if _fits_int32(seq_len) else 0
+
+
+def _sequences(d, seq_len):
+    """Number of sequences; seq_len as the C call must see it (ctypes drops bits above 32)."""
+    if not _fits_int32(seq_len):
+        raise ValueError(f"seq_len must fit into 32 bits (got {seq_len})")
+    return -(-d.T // seq_len) if seq_len > 0 else 0      # the call refuses seq_len < 1
+
+
+def _numel(ws):
+    return ws.numel() if isinstance(ws, torch.Tensor) else 0
+
+
+def _mask(mask):
+    """A bool mask's bytes are 0 and 1."""
+    return mask.view(torch.uint8) if isinstance(mask, torch.Tensor) and mask.dtype is torch.bool else mask
+
+
+def moe_balance(d: Dims, seq_len: int, logits, topk_idx, mask, counts, tokens, probs, loss, ws, stream=None):
+    """mask: uint8 or bool [T], or None."""
+    S, f32, i32 = _sequences(d, seq_len), torch.float32, torch.int32
+    _launch("moe_balance", stream, (ctypes.byref(d), seq_len),
+            ((logits, "logits", f32, d.T * d.E), (topk_idx, "topk_idx", i32, d.T * d.K),
+             (_mask(mask), "mask", torch.uint8, d.T), (counts, "counts", i32, S * d.E), (tokens, "tokens", i32, S + 2),
+             (probs, "probs", f32, S * d.E), (loss, "loss", f32, 2), (ws, "ws", torch.uint8, 0)),
+            (_numel(ws),))
+
+
+def moe_balance_bwd(d: Dims, seq_len: int, logits, mask, counts, tokens, dloss, dtopk_w, topk_w, topk_idx, dlogits,
+                    stream=None):
+    S, f32, i32 = _sequences(d, seq_len), torch.float32, torch.int32
+    _launch("moe_balance_bwd", stream, (ctypes.byref(d), seq_len),
+            ((logits, "logits", f32, d.T * d.E), (_mask(mask), "mask", torch.uint8, d.T),
+             (counts, "counts", i32, S * d.E), (tokens, "tokens", i32, S + 2), (dloss, "dloss", f32, 2),
+             (dtopk_w, "dtopk_w", f32, d.T * d.K), (topk_w, "topk_w", f32, d.T * d.K),
+             (topk_idx, "topk_idx", i32, d.T * d.K), (dlogits, "dlogits", f32, d.T * d.E)), ())
+
+
+# ---------------------------------------------------------------- update by Newton-Schulz products
+
+NEWTON_COEF = ((3.4445, -4.7750, 2.0315),) * 5
+_NEWTON_MAX_STEPS = 16
+
+
+class Newton(ctypes.Structure):
+    """moe_newton: a, b, c of each step."""
+    _fields_ = [("steps", ctypes.c_int32), ("coef", (ctypes.c_float * 3) * _NEWTON_MAX_STEPS)]
+
+    def __init__(self, coef=NEWTON_COEF):
+        super().__init__()
+        if not 1 <= len(coef) <= _NEWTON_MAX_STEPS:
+            raise ValueError(f"1 to {_NEWTON_MAX_STEPS} steps (got {len(coef)})")
+        self.steps = len(coef)
+        for k, abc in enumerate(coef):
+            a, b, c = abc
+            self.coef[k][0], self.coef[k][1], self.coef[k][2] = a, b, c
+
+
+class MuonParams(ctypes.Structure):
+    """moe_muon_params."""
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32)]
+
+
+_SIGS.update({
+    "moe_balance_workspace_bytes": (ctypes.c_size_t, [_D, ctypes.c_int]),
+    "moe_balance": (ctypes.c_int, [_D, ctypes.c_int] + [_P] * 8 + [ctypes.c_size_t, _P]),
+    "moe_balance_bwd": (ctypes.c_int, [_D, ctypes.c_int] + [_P] * 10),
+    "moe_muon_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "moe_orthogonalize": (ctypes.c_int, [ctypes.c_int] * 4 + [ctypes.POINTER(Newton)] + [_P] * 3 + [ctypes.c_size_t, _P]),
+    "moe_muon": (ctypes.c_int, [ctypes.c_int] * 4 + [ctypes.POINTER(Newton), ctypes.POINTER(MuonParams)] + [_P] * 6 +
+                 [ctypes.c_size_t, _P]),
+})
+
+
+def moe_muon_workspace_bytes(G: int, R: int, C: int, dtype: int) -> int:
+    return int(load().moe_muon_workspace_bytes(G, R, C, dtype)) if all(map(_fits_int32, (G, R, C))) else 0
+
+
+def _check_stack(G, R, C):
+    for name, v in (("G", G), ("R", R), ("C", C)):
+        if not _fits_int32(v):
+            raise ValueError(f"{name} must fit into 32 bits (got {v})")
+
+
+def _newton(coef):
+    return None if coef is None else ctypes.byref(Newton(coef))
+
+
+def moe_orthogonalize(G: int, R: int, C: int, g, out, ws, coef=None, stream=None):
+    """g [G, R, C] float32 -> out [G, R, C], float32 or bf16 (which sets the precision of the products).
+    coef: (a, b, c) of each step, or None: NEWTON_COEF."""
+    _check_stack(G, R, C)
+    code, dt = _stack_dtype(out, "out")
+    n = G * R * C
+    _launch("moe_orthogonalize", stream, (G, R, C, code, _newton(coef)),
+            ((g, "g", torch.float32, n), (out, "out", dt, n), (ws, "ws", torch.uint8, 0)),
+            (_numel(ws),))
+
+
+def _stack_dtype(t, name):
+    if t is None:
+        return F32, None                     # the call reports the NULL
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor or None")
+    for code, dt in _TORCH_DTYPE.items():
+        if t.dtype is dt:
+            return code, dt
+    raise TypeError(f"{name} must be {torch.float32} or {torch.bfloat16} (got {t.dtype})")
+
+
+def moe_muon(G: int, R: int, C: int, grad, mom, master, w, ws, *, lr, momentum=0.95, weight_decay=0.0, scale=1.0,
+             nesterov=True, coef=None, stream=None):
+    """One step on a stack of weights, in place: mom and master [G, R, C] float32, w their bf16 copy or
+    None (float32 weights: the products are as exact as float32's).  lr: a number, or a float32
+    tensor of one element on the GPU."""
+    _check_stack(G, R, C)
+    if w is not None and not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor or None")
+    n, f32 = G * R * C, torch.float32
+    on_device = isinstance(lr, torch.Tensor)
+    p = MuonParams(0.0 if on_device else lr, momentum, weight_decay, scale, int(bool(nesterov)))
+    _launch("moe_muon", stream, (G, R, C, F32 if w is None else BF16, _newton(coef), ctypes.byref(p)),
+            ((lr if on_device else None, "lr", f32, 1), (grad, "grad", f32, n), (mom, "mom", f32, n),
+             (master, "master", f32, n), (w, "w", torch.bfloat16, n), (ws, "ws", torch.uint8, 0)),
+            (_numel(ws),))

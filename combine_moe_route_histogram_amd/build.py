@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 ARCH = "gfx950"
 
 SOURCES = ["route.hip", "rows.hip", "gemm.hip", "fused.hip", "bwd.hip", "tuning.hip", "decode.hip",
-           "mx.hip", "moe_api.hip"]
+           "mx.hip", "balance.hip", "muon.hip", "train_api.hip", "moe_api.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/moe.h"
+#include "api.hpp"
 #include "decode.hpp"
 #include "kernels.hpp"
 #include "tuning.hpp"
@@ -17,8 +18,11 @@
 using namespace moe;
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+// Declared in api.hpp: the argument checks and error records that all entry points share.
+namespace moe {
 
 int fail(int status, const char* fmt, ...) {
   char buf[512];
@@ -35,8 +39,38 @@ int hip_status(hipError_t e, const char* what) {
   return fail(MOE_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+int check_dims(const moe_dims* d) {
+  if (!d) return fail(MOE_EINVAL, "dims is NULL");
+  if (d->T < 1) return fail(MOE_EINVAL, "T must be >= 1 (got %d)", d->T);
+  if (d->E < 1 || d->E > kMaxExperts)
+    return fail(MOE_EUNSUPPORTED, "E must be in [1, %d] (got %d)", kMaxExperts, d->E);
+  if (d->K < 1 || d->K > d->E)
+    return fail(MOE_EUNSUPPORTED, "K must be in [1, E] (got K=%d, E=%d)", d->K, d->E);
+  if (d->H <= 0 || d->H % 8)
+    return fail(MOE_EUNSUPPORTED, "H must be a positive multiple of 8 (got %d)", d->H);
+  if (d->I <= 0 || d->I % 8)
+    return fail(MOE_EUNSUPPORTED, "I must be a positive multiple of 8 (got %d)", d->I);
+  if (d->n_shared < 0 || d->n_shared > kMaxShared)
+    return fail(MOE_EUNSUPPORTED, "n_shared must be in [0, %d] (got %d)", kMaxShared, d->n_shared);
+  if (d->n_shared > 0 && d->I_shared != d->I)
+    return fail(MOE_EUNSUPPORTED,
+                "shared experts must have the routed experts' intermediate dim (I_shared=%d, I=%d)",
+                d->I_shared, d->I);
+  if (d->dtype != MOE_F32 && d->dtype != MOE_BF16)
+    return fail(MOE_EUNSUPPORTED, "dtype must be MOE_F32 or MOE_BF16 (got %d)", d->dtype);
+  const int64_t ra = (int64_t)d->T * d->K + (int64_t)d->n_shared * d->T;
+  if (ra >= (int64_t)1 << 31) return fail(MOE_EUNSUPPORTED, "R + n_shared*T must be < 2^31");
+  return MOE_OK;
+}
+
+int check_ptr(const void* p, const char* name) {
+  if (!p) return fail(MOE_EINVAL, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) % 16) return fail(MOE_EINVAL, "%s is not 16-byte aligned", name);
+  return MOE_OK;
+}
+}  // namespace moe
+
+namespace {
 
 // Workspace sections (byte offsets).
 struct Layout {
@@ -71,36 +105,6 @@ T* ws_at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-int check_dims(const moe_dims* d) {
-  if (!d) return fail(MOE_EINVAL, "dims is NULL");
-  if (d->T < 1) return fail(MOE_EINVAL, "T must be >= 1 (got %d)", d->T);
-  if (d->E < 1 || d->E > kMaxExperts)
-    return fail(MOE_EUNSUPPORTED, "E must be in [1, %d] (got %d)", kMaxExperts, d->E);
-  if (d->K < 1 || d->K > d->E)
-    return fail(MOE_EUNSUPPORTED, "K must be in [1, E] (got K=%d, E=%d)", d->K, d->E);
-  if (d->H <= 0 || d->H % 8)
-    return fail(MOE_EUNSUPPORTED, "H must be a positive multiple of 8 (got %d)", d->H);
-  if (d->I <= 0 || d->I % 8)
-    return fail(MOE_EUNSUPPORTED, "I must be a positive multiple of 8 (got %d)", d->I);
-  if (d->n_shared < 0 || d->n_shared > kMaxShared)
-    return fail(MOE_EUNSUPPORTED, "n_shared must be in [0, %d] (got %d)", kMaxShared, d->n_shared);
-  if (d->n_shared > 0 && d->I_shared != d->I)
-    return fail(MOE_EUNSUPPORTED,
-                "shared experts must have the routed experts' intermediate dim (I_shared=%d, I=%d)",
-                d->I_shared, d->I);
-  if (d->dtype != MOE_F32 && d->dtype != MOE_BF16)
-    return fail(MOE_EUNSUPPORTED, "dtype must be MOE_F32 or MOE_BF16 (got %d)", d->dtype);
-  const int64_t ra = (int64_t)d->T * d->K + (int64_t)d->n_shared * d->T;
-  if (ra >= (int64_t)1 << 31) return fail(MOE_EUNSUPPORTED, "R + n_shared*T must be < 2^31");
-  return MOE_OK;
-}
-
-int check_ptr(const void* p, const char* name) {
-  if (!p) return fail(MOE_EINVAL, "%s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) % 16) return fail(MOE_EINVAL, "%s is not 16-byte aligned", name);
-  return MOE_OK;
-}
-
 int check_ws(const moe_dims* d, const void* ws, size_t ws_bytes) {
   const size_t need = layout(d).total;
   if (!ws) return fail(MOE_EWORKSPACE, "workspace is NULL (need %zu bytes)", need);
@@ -109,14 +113,6 @@ int check_ws(const moe_dims* d, const void* ws, size_t ws_bytes) {
   if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace has %zu bytes, need %zu", ws_bytes, need);
   return MOE_OK;
 }
-
-#define MOE_TRY(expr)            \
-  do {                           \
-    const int _s = (expr);       \
-    if (_s != MOE_OK) return _s; \
-  } while (0)
-
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 // Debug settings, read from the environment by moe_init only (never at a
 // launch): the bound of the in-kernel waits in ticks of the 100 MHz clock

@@ -1,0 +1,582 @@
+// Newton-Schulz products of stacked matrices, and the update of weights built on them.
+//
+// Per step, for X [s, l] with s <= l (the transpose of a tall matrix, taken while it is read):
+//   A = X X^T           symmetric: tiles on and above the diagonal, mirrored
+//   B = b A + c A A     symmetric, too
+//   X <- a X + B X      the last one writes the result (transposed back) or updates the weights
+// so 3 s^2 l + s^3 multiply-adds a step of 4 s^2 l + 2 s^3: bound by the matrix cores where the
+// matrices are large, by the chain of launches where they are small.
+//
+// Numbers.  X is kept as two fp16 parts (22 bits), scaled by 2^10: |x| <= 64 fits, and an
+// element of 1e-5 still has all its bits.  The products take the upper parts (11 bits) with f32
+// sums; a X is formed in f32 from both parts.  The roundings of a product then act on X from the
+// left only, inside its row space, and are not amplified by the steps: 1e-3 to 2e-3 of the
+// result's norm for any rank.  (X in one fp16 part: 2e-2 for rank 64 of 352, as null directions'
+// roundings grow 3.4-fold a step; everything in bf16: 1e-2 for a full rank and 0.2 for that one.)
+// The exact form takes three products, lo hi + hi lo + hi hi, of X, A and B in two parts each.
+#include "muon.hpp"
+
+#include "gemm_tile.hpp"
+
+namespace moe {
+
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kXScale = 1024.f;   // of stored X
+constexpr float kAScale = 256.f;    // of stored A and B
+
+enum NewtonKind { kGram, kPoly, kStep, kOut, kUpdate };
+
+// One product of a batch of matrices.  Operands and results are [batch][rows][ld] fp16 planes.
+struct Product {
+  const uint16_t *ah, *al, *bh, *bl;
+  int64_t a_mat, b_mat;     // elements of a matrix
+  int lda, ldb, k_len;
+  int m_len, n_len;         // padded sizes of the result
+  int mt, nt, per, tiles;   // tile grid, tiles of a matrix and of all
+  const uint16_t *ch, *cl;  // what the epilogue adds: A (kPoly) or X (kStep, kOut, kUpdate)
+  uint16_t *oh, *ol;        // kGram, kPoly, kStep
+  int64_t o_mat;
+  int ldo;                  // of ch, cl, oh, ol
+  float a, b, c;
+  // kOut, kUpdate
+  bool tall, bf16;
+  int R, C, g0;
+  void* out;
+  float* master;
+  uint16_t* w;
+  const float* lr_dev;
+  float lr, weight_decay, scale;
+};
+
+template <int BM_, int BN_, int WGM_, int WGN_, bool B_MN_>
+struct NsCfg {
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, STAGES = 2, BK = 64;
+  static constexpr bool B_MN = B_MN_;
+  static constexpr int NW = WGM * WGN, NT = NW * kWave;
+  static constexpr int WM = BM / WGM, WN = BN / WGN, MI = WM / 32, NJ = WN / 32;
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+  static_assert(NJ % 2 == 0, "the epilogue takes two 32-column blocks at a time");
+};
+
+// v as two fp16 parts
+__device__ __forceinline__ void split16(const float* v, u32x2& hi, u32x2& lo) {
+  f16x4 h, l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = (_Float16)v[e];
+    l[e] = (_Float16)(v[e] - (float)h[e]);
+  }
+  hi = __builtin_bit_cast(u32x2, h);
+  lo = __builtin_bit_cast(u32x2, l);
+}
+__device__ __forceinline__ void join16(const uint16_t* hp, const uint16_t* lp, float* v) {
+  const f16x4 h = __builtin_bit_cast(f16x4, *reinterpret_cast<const u32x2*>(hp));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
+  if (lp) {
+    const f16x4 l = __builtin_bit_cast(f16x4, *reinterpret_cast<const u32x2*>(lp));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += (float)l[e];
+  }
+}
+
+// Four results of row `row` from column `col` on, of matrix g of the user's tensors.
+template <int KIND>
+__device__ __forceinline__ void emit4(const Product& p, int64_t g, int row, int col, const float* v, float lr) {
+  if (row >= p.R || col >= p.C) return;
+  const int64_t at = (g * p.R + row) * p.C + col;
+  const float keep = 1.f - lr * p.weight_decay, gain = lr * p.scale;
+  if (p.C % 4 == 0) {   // aligned: 16-byte f32, 8-byte bf16
+    if constexpr (KIND == kOut) {
+      if (p.bf16) st_bf16x4(static_cast<uint16_t*>(p.out) + at, v);
+      else *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+      f32x4 m = *reinterpret_cast<const f32x4*>(p.master + at);
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = keep * m[e] - gain * v[e];
+      *reinterpret_cast<f32x4*>(p.master + at) = f32x4{x[0], x[1], x[2], x[3]};
+      if (p.w) st_bf16x4(p.w + at, x);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (col + e >= p.C) break;
+    if constexpr (KIND == kOut) {
+      if (p.bf16) static_cast<uint16_t*>(p.out)[at + e] = (uint16_t)f32_to_bf16(v[e]);
+      else static_cast<float*>(p.out)[at + e] = v[e];
+    } else {
+      const float x = keep * p.master[at + e] - gain * v[e];
+      p.master[at + e] = x;
+      if (p.w) p.w[at + e] = (uint16_t)f32_to_bf16(x);
+    }
+  }
+}
+
+// Accumulators to results: 32 x 64 blocks through the wave's LDS region, as in the layer's tiles.
+template <int KIND, bool EXACT, class C>
+__device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int m0, int n0, bool mirror,
+                                                const f32x16 (&acc)[C::MI][C::NJ],
+                                                uint8_t* const (&stages)[4], int wave, int lane) {
+  constexpr int kRps = C::STAGE_BYTES / kEpiRegionBytes;
+  static_assert(kRps >= 1 && (C::NW + kRps - 1) / kRps <= C::STAGES, "epilogue regions fit in the slices");
+  const int wm = wave / C::WGN, wn = wave % C::WGN;
+  uint8_t* const rbase = wave / kRps == 0 ? stages[0] : stages[1];
+  float* reg = reinterpret_cast<float*>(rbase + (wave % kRps) * kEpiRegionBytes);
+  float lr = 0.f;
+  if constexpr (KIND == kUpdate) lr = p.lr_dev ? *p.lr_dev : p.lr;
+  const int64_t obase = g * p.o_mat;
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i) {
+#pragma unroll
+    for (int hc = 0; hc < C::NJ / 2; ++hc) {
+      const int mb = m0 + wm * C::WM + 32 * i, nb = n0 + wn * C::WN + 64 * hc;
+      if (mb >= p.m_len || nb >= p.n_len) continue;   // the sizes are whole blocks
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        reg[row * kEpiPitch + (lane & 31)] = acc[i][2 * hc][r];
+        reg[row * kEpiPitch + 32 + (lane & 31)] = acc[i][2 * hc + 1][r];
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the wave's own region is written
+      const bool turn = KIND == kGram || KIND == kPoly ? mirror : KIND != kStep && p.tall;
+#pragma unroll
+      for (int pass = 0; pass < 8; ++pass) {
+        const int q = pass * 4 + (lane >> 4), c4 = 4 * (lane & 15);
+        const f32x4 s = *reinterpret_cast<const f32x4*>(reg + q * kEpiPitch + c4);
+        const int64_t at = obase + (int64_t)(mb + q) * p.ldo + nb + c4;
+        float v[4], x[4];
+        if constexpr (KIND == kGram) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = s[e] * (kAScale / (kXScale * kXScale));
+        } else if constexpr (KIND == kPoly) {
+          join16(p.ch + at, EXACT ? p.cl + at : nullptr, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = p.b * x[e] + p.c * (s[e] * (1.f / kAScale));
+        } else {
+          join16(p.ch + at, p.cl + at, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = p.a * x[e] + s[e] * (1.f / kAScale);
+          if constexpr (KIND != kStep) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= 1.f / kXScale;
+          }
+        }
+        if constexpr (KIND == kGram || KIND == kPoly || KIND == kStep) {
+          u32x2 hi, lo;
+          split16(v, hi, lo);
+          *reinterpret_cast<u32x2*>(p.oh + at) = hi;
+          if (EXACT || KIND == kStep) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
+        } else if (!turn) {
+          emit4<KIND>(p, p.g0 + g, mb + q, nb + c4, v, lr);
+        }
+        if (KIND != kStep && turn)
+          *reinterpret_cast<f32x4*>(reg + q * kEpiPitch + c4) = f32x4{v[0], v[1], v[2], v[3]};
+      }
+      if (KIND != kStep && turn) {   // the block's transpose: 64 rows of 32
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+#pragma unroll
+        for (int pass = 0; pass < 8; ++pass) {
+          const int n = pass * 8 + (lane >> 3), m4 = 4 * (lane & 7);
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = reg[(m4 + e) * kEpiPitch + n];
+          if constexpr (KIND == kGram || KIND == kPoly) {
+            const int64_t at = obase + (int64_t)(nb + n) * p.ldo + mb + m4;
+            u32x2 hi, lo;
+            split16(v, hi, lo);
+            *reinterpret_cast<u32x2*>(p.oh + at) = hi;
+            if (EXACT) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
+          } else if constexpr (KIND != kStep) {
+            emit4<KIND>(p, p.g0 + g, nb + n, mb + m4, v, lr);
+          }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // region reads done before it is rewritten
+    }
+  }
+}
+
+// One tile of a product; same ring of LDS slices and order of instructions as the layer's tiles
+// (run_tile_bf16), on fp16.
+template <int KIND, bool EXACT, class C>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void newton_kernel(Product p) {
+  MOE_LDS_RING(C, ring);
+  constexpr bool kSym = KIND == kGram || KIND == kPoly;
+  constexpr int MI = C::MI, NJ = C::NJ, BK = C::BK, S = C::STAGES, KS = BK / 16;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  // consecutive blocks go to different XCDs; each XCD takes a run of tiles, which share operands in its L2
+  const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
+  const int first = (int)((int64_t)p.tiles * xcd / kXcds);
+  const int L = first + idx;
+  if (L >= (int)((int64_t)p.tiles * (xcd + 1) / kXcds)) return;
+  const int64_t g = L / p.per;
+  const int r = L - (int)g * p.per;
+  int tm, tn;
+  if constexpr (kSym) {   // columns of the upper triangle: tm <= tn
+    tn = (int)((sqrtf(8.f * (float)r + 1.f) - 1.f) * 0.5f);
+    while (tn * (tn + 1) / 2 > r) --tn;
+    while ((tn + 1) * (tn + 2) / 2 <= r) ++tn;
+    tm = r - tn * (tn + 1) / 2;
+  } else {
+    band_order(r, p.mt, p.nt, 8, tm, tn);
+  }
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int m_valid = min(C::BM, p.m_len - m0), n_valid = min(C::BN, p.n_len - n0);
+  const int64_t a0 = g * p.a_mat + (int64_t)m0 * p.lda;
+  const int64_t b0 = g * p.b_mat + (C::B_MN ? (int64_t)n0 : (int64_t)n0 * p.ldb);
+  const int wm = wave / C::WGN, wn = wave % C::WGN;
+
+  DmaOperand<C::BM, C::NW, false, 1, false, BK> da;
+  DmaOperand<C::BN, C::NW, C::B_MN, 1, false, BK> db;
+  da.init(p.lda, m_valid, wave, lane);
+  db.init(p.ldb, n_valid, wave, lane);
+  const int nk1 = p.k_len / BK, nk = EXACT ? 3 * nk1 : nk1;
+  auto issue = [&](uint8_t* st, int kt) {
+    int seg = 2, k = kt;      // exact: lo hi, hi lo, then hi hi (the small products first)
+    if constexpr (EXACT) {
+      seg = (kt >= nk1) + (kt >= 2 * nk1);
+      k = kt - seg * nk1;
+    }
+    const uint16_t* a = (EXACT && seg == 0 ? p.al : p.ah) + a0 + k * BK;
+    const uint16_t* b = (EXACT && seg == 1 ? p.bl : p.bh) + b0 + (C::B_MN ? (int64_t)k * BK * p.ldb : (int64_t)k * BK);
+    da.issue(st, a, nullptr, 0, kt < nk, wave);
+    db.issue(st + C::A_BYTES, b, nullptr, 0, kt < nk, wave);
+  };
+
+  f32x16 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+  constexpr int kLoads = decltype(da)::kPerWave + decltype(db)::kPerWave;
+  const int nk_pad = (nk + S - 1) / S * S;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(ring[i], i);
+
+  auto loop = [&](auto na_c) {
+    constexpr int NA = decltype(na_c)::value;
+    constexpr int kReads = NA == 0 ? 0 : NA + NJ * (C::B_MN ? 2 : 1);
+    auto frags = [&](const uint8_t* st, int ks, bf16x8 (&av)[MI], bf16x8 (&bv)[NJ]) {
+      if constexpr (NA > 0) {
+        auto fa = [&](int i) {
+          av[i] = kc_frag<BK>(st, wm * C::WM + 32 * i + (lane & 31), 2 * ks + (lane >> 5));
+        };
+        auto fb = [&](int j) {
+          if constexpr (C::B_MN)
+            bv[j] = mn_frag(st + C::A_BYTES, C::BN, wn * C::WN + 32 * j, ks, lane);
+          else
+            bv[j] = kc_frag<BK>(st + C::A_BYTES, wn * C::WN + 32 * j + (lane & 31), 2 * ks + (lane >> 5));
+        };
+        fb(0);
+        fa(0);
+#pragma unroll
+        for (int j = 1; j < NJ; ++j) fb(j);
+#pragma unroll
+        for (int i = 1; i < NA; ++i) fa(i);
+      }
+    };
+    auto mfma_step = [&](const bf16x8 (&av)[MI], const bf16x8 (&bv)[NJ]) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, av[i]),
+                                                            __builtin_bit_cast(f16x8, bv[j]), acc[i][j], 0, 0, 0);
+    };
+    bf16x8 av[2][MI], bv[2][NJ];
+    const bf16x8 zero = {};
+#pragma unroll
+    for (int i = 0; i < MI; ++i) av[1][i] = zero;   // "previous step" of slice 0: adds zeros
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bv[1][j] = zero;
+    wait_vmcnt<0>();
+    lds_barrier();
+    for (int kt0 = 0; kt0 < nk_pad; kt0 += S) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          frags(ring[i], ks, av[ks & 1], bv[ks & 1]);
+          if (ks == 0) issue(ring[(i + S - 1) % S], kt0 + i + S - 1);
+          mfma_step(av[(ks + 1) & 1], bv[(ks + 1) & 1]);
+          if (ks == 0)
+            interleave_step<0, NA * NJ, kReads, kLoads>();
+          else
+            interleave_step<0, NA * NJ, kReads, 0>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        wait_vmcnt<0>();
+        lds_barrier();
+      }
+    }
+    mfma_step(av[1], bv[1]);   // last step of the last slice
+  };
+  const int na = wn * C::WN >= n_valid ? 0 : max(0, min(MI, (m_valid - wm * C::WM + 31) / 32));
+  with_count<MI>(__builtin_amdgcn_readfirstlane(na), loop);
+  __syncthreads();
+  newton_epilogue<KIND, EXACT, C>(p, g, m0, n0, kSym && tm != tn, acc, ring, wave, lane);
+}
+
+// --------------------------------------------------------- before the products
+
+struct Source {
+  const float* g;
+  float* mom;         // NULL: the matrices themselves
+  float momentum;
+  bool nesterov;
+  int R, C, g0;
+  int parts;
+  double* sums;       // [batch][kNormParts]
+};
+
+__device__ __forceinline__ float direction(const Source& s, float grad, float mom) {
+  return s.nesterov ? fmaf(s.momentum, mom, grad) : mom;
+}
+
+// Sums of squares of part `blockIdx.x` of matrix blockIdx.y, in 64 bits (no scale of the entries
+// overflows or vanishes); with momentum, its update on the way.
+template <int V>
+__global__ __launch_bounds__(256) void newton_squares_kernel(Source s) {
+  __shared__ double red[4];
+  const int tid = threadIdx.x;
+  const int64_t n = (int64_t)s.R * s.C / V, base = (int64_t)(s.g0 + blockIdx.y) * s.R * s.C;
+  double sum = 0.0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < n; i += (int64_t)s.parts * 256) {
+    float v[V];
+    const float* gp = s.g + base + i * V;
+    if constexpr (V == 4) Elem<float>::unpack(ld16(gp), v);
+    else v[0] = *gp;
+    if (s.mom) {
+      float m[V];
+      float* mp = s.mom + base + i * V;
+      if constexpr (V == 4) Elem<float>::unpack(ld16(mp), m);
+      else m[0] = *mp;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        m[e] = fmaf(s.momentum, m[e], v[e]);
+        v[e] = direction(s, v[e], m[e]);
+      }
+      if constexpr (V == 4) st16(mp, Elem<float>::pack(m));
+      else *mp = m[0];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum = fma((double)v[e], (double)v[e], sum);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if ((tid & 63) == 0) red[tid >> 6] = sum;
+  __syncthreads();
+  if (tid == 0) s.sums[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// X = U / |U| as two fp16 parts, zeros in the padding: one 64 x 64 tile of X for each block.  Tall
+// matrices are turned on the way, through LDS.
+template <int V>
+__global__ __launch_bounds__(256) void newton_start_kernel(Source s, bool tall, int sp, int lp, uint16_t* xh,
+                                                           uint16_t* xl) {
+  __shared__ float tile[64][65];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int ct = lp / 64, per = ct * (sp / 64);
+  const int64_t b = blockIdx.x / per;
+  const int rem = (int)(blockIdx.x - b * per);
+  const int x0 = rem / ct * 64, y0 = rem % ct * 64;    // of X: row, column
+  const int r0 = tall ? y0 : x0, c0 = tall ? x0 : y0;  // of the matrix
+  const int64_t base = (s.g0 + b) * s.R * s.C;
+  float u[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = r0 + (tid >> 4) + 16 * j, c = c0 + 4 * (tid & 15);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[j][e] = 0.f;
+    if (r < s.R && c < s.C) {
+      const int64_t at = base + (int64_t)r * s.C + c;
+      float m[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (V == 4) {
+        Elem<float>::unpack(ld16(s.g + at), u[j]);
+        if (s.mom) Elem<float>::unpack(ld16(s.mom + at), m);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < s.C) {
+            u[j][e] = s.g[at + e];
+            if (s.mom) m[e] = s.mom[at + e];
+          }
+      }
+      if (s.mom) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[j][e] = direction(s, u[j][e], m[e]);
+      }
+    }
+  }
+  double sum = 0.0;
+  for (int i = lane; i < s.parts; i += kWave) sum += s.sums[b * kNormParts + i];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  // zeros stay zeros; an infinity or NaN anywhere makes the whole matrix NaN
+  const double inv = sum == 0.0 ? 0.0 : sum < (double)INFINITY ? (double)kXScale / sqrt(sum) : (double)NAN;
+  if (tall) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[(tid >> 4) + 16 * j][4 * (tid & 15) + e] = u[j][e];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[j][e] = tile[4 * (tid & 15) + e][(tid >> 4) + 16 * j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int x = x0 + (tid >> 4) + 16 * j, y = y0 + 4 * (tid & 15);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)((double)u[j][e] * inv);
+    u32x2 hi, lo;
+    split16(v, hi, lo);
+    const int64_t at = (b * sp + x) * lp + y;
+    *reinterpret_cast<u32x2*>(xh + at) = hi;
+    *reinterpret_cast<u32x2*>(xl + at) = lo;
+  }
+}
+
+// ---------------------------------------------------------------------- host
+
+inline int up(int v, int to) { return (v + to - 1) / to * to; }
+
+template <int KIND, bool EXACT, class C>
+hipError_t product_with(Product p, int batch, hipStream_t st) {
+  p.mt = (p.m_len + C::BM - 1) / C::BM;
+  p.nt = (p.n_len + C::BN - 1) / C::BN;
+  p.per = KIND == kGram || KIND == kPoly ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
+  p.tiles = p.per * batch;
+  const unsigned grid = (unsigned)kXcds * ((p.tiles + kXcds - 1) / kXcds);
+  newton_kernel<KIND, EXACT, C><<<grid, C::NT, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t product(const Product& p, bool exact, int batch, hipStream_t st) {
+  constexpr bool kMn = KIND == kStep || KIND == kOut || KIND == kUpdate;
+  using Big = NsCfg<256, 256, 2, 4, kMn>;
+  using Small = NsCfg<128, 128, 2, 2, kMn>;
+  const int64_t mt = (p.m_len + 255) / 256, nt = (p.n_len + 255) / 256;
+  const int64_t tiles = batch * (kMn ? mt * nt : mt * (mt + 1) / 2);
+  if (tiles >= 256)
+    return exact ? product_with<KIND, true, Big>(p, batch, st) : product_with<KIND, false, Big>(p, batch, st);
+  return exact ? product_with<KIND, true, Small>(p, batch, st) : product_with<KIND, false, Small>(p, batch, st);
+}
+
+}  // namespace
+
+NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
+  NewtonPlan p{};
+  p.G = G; p.R = R; p.C = C;
+  p.tall = R > C;
+  p.s = p.tall ? C : R;
+  p.l = p.tall ? R : C;
+  p.sp = up(p.s, kNewtonPad);
+  p.lp = up(p.l, kNewtonPad);
+  p.exact = !bf16;
+  // About 2048 tiles of 256 x 256 to a launch: 8 rounds over the 256 CUs, of which the last one
+  // is partly empty; more would only take memory (at most 2^30 elements of X, or one matrix).
+  const int64_t t = (p.sp + 255) / 256, tiles = t * (t + 1) / 2;
+  const int64_t fit = ((int64_t)1 << 30) / ((int64_t)p.sp * p.lp);
+  int64_t most = (2048 + tiles - 1) / tiles;
+  if (most > fit) most = fit > 1 ? fit : 1;
+  const int64_t batches = (G + most - 1) / most;
+  p.batch = (int)((G + batches - 1) / batches);
+  const size_t x = (size_t)p.batch * p.sp * p.lp * 2, a = (size_t)p.batch * p.sp * p.sp * 2;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  p.parts = take((size_t)p.batch * kNormParts * sizeof(double));
+  for (int i = 0; i < 2; ++i) {
+    p.xh[i] = take(x);
+    p.xl[i] = take(x);
+  }
+  p.ah = take(a);
+  p.bh = take(a);
+  p.al = take(p.exact ? a : 0);
+  p.bl = take(p.exact ? a : 0);
+  p.total = off;
+  return p;
+}
+
+hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
+  const NewtonPlan& p = c.p;
+  auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(static_cast<char*>(c.ws) + off); };
+  uint16_t *const ah = at(p.ah), *const al = at(p.al), *const bh = at(p.bh), *const bl = at(p.bl);
+  const int64_t n = (int64_t)p.R * p.C;
+  for (int g0 = 0; g0 < p.G; g0 += p.batch) {
+    const int batch = p.G - g0 < p.batch ? p.G - g0 : p.batch;
+    Source s{};
+    s.g = c.g;
+    s.mom = c.mom;
+    s.momentum = c.momentum;
+    s.nesterov = c.nesterov;
+    s.R = p.R; s.C = p.C; s.g0 = g0;
+    s.sums = reinterpret_cast<double*>(at(p.parts));
+    const int64_t want = (n + 4095) / 4096;   // 16 elements or more to a thread
+    s.parts = (int)(want < kNormParts ? want : kNormParts);
+    const unsigned tiles = (unsigned)((int64_t)batch * (p.sp / 64) * (p.lp / 64));
+    const dim3 sq(s.parts, batch);
+    if (n % 4 == 0) newton_squares_kernel<4><<<sq, 256, 0, st>>>(s);
+    else newton_squares_kernel<1><<<sq, 256, 0, st>>>(s);
+    if (p.C % 4 == 0) newton_start_kernel<4><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), at(p.xl[0]));
+    else newton_start_kernel<1><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), at(p.xl[0]));
+    for (int k = 0; k < c.steps; ++k) {
+      const uint16_t *xh = at(p.xh[k & 1]), *xl = at(p.xl[k & 1]);
+      const int64_t x_mat = (int64_t)p.sp * p.lp, a_mat = (int64_t)p.sp * p.sp;
+      Product q{};
+      q.a = c.coef[k][0]; q.b = c.coef[k][1]; q.c = c.coef[k][2];
+      q.ah = xh; q.al = xl; q.bh = xh; q.bl = xl;
+      q.a_mat = q.b_mat = x_mat;
+      q.lda = q.ldb = q.k_len = p.lp;
+      q.m_len = q.n_len = p.sp;
+      q.oh = ah; q.ol = al; q.o_mat = a_mat; q.ldo = p.sp;
+      hipError_t e = product<kGram>(q, p.exact, batch, st);
+      if (e != hipSuccess) return e;
+      q.ah = ah; q.al = al; q.bh = ah; q.bl = al;
+      q.a_mat = q.b_mat = a_mat;
+      q.lda = q.ldb = q.k_len = p.sp;
+      q.ch = ah; q.cl = al;
+      q.oh = bh; q.ol = bl;
+      e = product<kPoly>(q, p.exact, batch, st);
+      if (e != hipSuccess) return e;
+      q.ah = bh; q.al = bl; q.bh = xh; q.bl = xl;
+      q.a_mat = a_mat; q.b_mat = x_mat;
+      q.lda = q.k_len = p.sp; q.ldb = p.lp;
+      q.n_len = p.lp;
+      q.ch = xh; q.cl = xl;
+      q.o_mat = x_mat; q.ldo = p.lp;
+      if (k + 1 < c.steps) {
+        q.oh = at(p.xh[(k + 1) & 1]);
+        q.ol = at(p.xl[(k + 1) & 1]);
+        e = product<kStep>(q, p.exact, batch, st);
+      } else {
+        q.tall = p.tall; q.bf16 = c.bf16;
+        q.R = p.R; q.C = p.C; q.g0 = g0;
+        q.out = c.out; q.master = c.master; q.w = c.w;
+        q.lr_dev = c.lr_dev; q.lr = c.lr; q.weight_decay = c.weight_decay; q.scale = c.scale;
+        e = c.out ? product<kOut>(q, p.exact, batch, st) : product<kUpdate>(q, p.exact, batch, st);
+      }
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

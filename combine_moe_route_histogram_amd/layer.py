@@ -9,11 +9,12 @@ from __future__ import annotations
 
 import torch
 
-from . import (BF16, F32, Dims, moe_combine, moe_combine_bwd, moe_decode, moe_decode_mx,
-               moe_decode_workspace_bytes, moe_dispatch, moe_dispatch_bwd, moe_dispatch_ffn,
-               moe_expert_ffn_bwd, moe_expert_ffn_bwd_data, moe_expert_ffn_bwd_weight,
-               moe_expert_ffn_down, moe_expert_ffn_up, moe_ffn_combine, moe_mx_bytes, moe_mx_quantize,
-               moe_route, moe_route_bwd, moe_sync_status, moe_workspace_bytes)
+from . import (BF16, F32, Dims, moe_balance, moe_balance_bwd, moe_balance_workspace_bytes, moe_combine,
+               moe_combine_bwd, moe_decode, moe_decode_mx, moe_decode_workspace_bytes, moe_dispatch,
+               moe_dispatch_bwd, moe_dispatch_ffn, moe_expert_ffn_bwd, moe_expert_ffn_bwd_data,
+               moe_expert_ffn_bwd_weight, moe_expert_ffn_down, moe_expert_ffn_up, moe_ffn_combine,
+               moe_muon, moe_muon_workspace_bytes, moe_mx_bytes, moe_mx_quantize, moe_route,
+               moe_route_bwd, moe_sync_status, moe_workspace_bytes)
 
 
 def make_dims(T, H, E, K, I, n_shared=0, dtype="bf16", I_shared=None) -> Dims:
@@ -79,9 +80,11 @@ def forward(b: Buffers, p: dict, fused: bool = False, stream=None):
         moe_combine(d, b.y, b.slot, b.topk_w, b.out, stream)
 
 
-def backward(b: Buffers, p: dict, fused: bool = False, stream=None):
+def backward(b: Buffers, p: dict, fused: bool = False, stream=None, losses=None):
     """combine_bwd -> FFN input grads (B) -> FFN weight grads (W) -> dispatch_bwd -> route_bwd.
-    fused: B and W in one launch, W filling the gaps of B (moe_expert_ffn_bwd)."""
+    fused: B and W in one launch, W filling the gaps of B (moe_expert_ffn_bwd).
+    losses: BalanceBuffers of this step's logits (balance); p["dloss"], the gradients of its two
+    losses, then go into dlogits along with route_bwd's."""
     d = b.d
     moe_combine_bwd(d, p["dout"], b.y, b.slot, b.topk_w, b.dy, b.dtopk_w, stream)
     if fused:
@@ -96,7 +99,11 @@ def backward(b: Buffers, p: dict, fused: bool = False, stream=None):
         moe_expert_ffn_bwd_weight(d, b.x_perm, p["x"], b.h, b.dy, p.get("dout"), b.dab, b.offsets,
                                   b.dw1, b.dw3, b.dw2, b.dws1, b.dws3, b.dws2, b.ws, stream)
     moe_dispatch_bwd(d, b.dx_rows, b.slot, b.dx, stream)
-    moe_route_bwd(d, b.dtopk_w, b.topk_w, b.topk_idx, b.dlogits, stream)
+    if losses is None:
+        moe_route_bwd(d, b.dtopk_w, b.topk_w, b.topk_idx, b.dlogits, stream)
+    else:
+        moe_balance_bwd(d, losses.seq_len, p["logits"], p.get("mask"), losses.counts, losses.tokens, p["dloss"],
+                        b.dtopk_w, b.topk_w, b.topk_idx, b.dlogits, stream)
 
 
 def check(stream=None):
@@ -137,3 +144,54 @@ def quantize_weights(p: dict) -> dict:
             q[name] = torch.empty(moe_mx_bytes(G, K, N), dtype=torch.uint8, device=w.device)
             moe_mx_quantize(G, K, N, w, q[name])
     return q
+
+
+class BalanceBuffers:
+    """Outputs and workspace of the router's losses; seq_len None: the batch is one sequence."""
+
+    def __init__(self, d: Dims, seq_len=None, device="cuda"):
+        self.d = d
+        self.seq_len = n = d.T if seq_len is None else seq_len
+        z = lambda *s, dtype: torch.empty(*s, dtype=dtype, device=device)
+        self.ws = z(max(moe_balance_workspace_bytes(d, n), 256), dtype=torch.uint8)
+        if n < 1:
+            raise ValueError(f"seq_len must be at least 1 (got {n})")
+        S = -(-d.T // n)
+        self.counts = z(S, d.E, dtype=torch.int32)      # picks of each expert in each sequence
+        self.tokens = z(S + 2, dtype=torch.int32)       # of each sequence; all; sequences with any
+        self.probs = z(S, d.E, dtype=torch.float32)     # sums of softmax(logits)
+        self.loss = z(2, dtype=torch.float32)           # load balance; squared log-sum-exp
+
+
+def balance(l: BalanceBuffers, logits, topk_idx, mask=None, stream=None):
+    """The router's losses and per-expert counts of routed tokens (mask: 0 for padding)."""
+    moe_balance(l.d, l.seq_len, logits, topk_idx, mask, l.counts, l.tokens, l.probs, l.loss, l.ws, stream)
+
+
+WEIGHTS = ("w1", "w3", "w2", "ws1", "ws3", "ws2")
+
+
+class MuonState:
+    """Momentum, float32 weights and the shared workspace of the optimizer for the weights in p (made on
+    the current stream).  float32 weights are updated in place, bf16 ones are copies of `master`."""
+
+    def __init__(self, p: dict):
+        self.names = [n for n in WEIGHTS if p.get(n) is not None]
+        self.mom = {n: torch.zeros(p[n].shape, dtype=torch.float32, device=p[n].device) for n in self.names}
+        self.master = {n: p[n].float() for n in self.names}      # float32 weights: p[n] itself
+        need = 256
+        for n in self.names:
+            need = max(need, moe_muon_workspace_bytes(*p[n].shape, BF16 if p[n].dtype == torch.bfloat16 else F32))
+        self.ws = torch.empty(need, dtype=torch.uint8, device=p[self.names[0]].device)
+
+
+def muon_step(m: MuonState, p: dict, b: Buffers, lr, momentum=0.95, weight_decay=0.0, nesterov=True, coef=None,
+              stream=None):
+    """One step of every weight in p from the gradients that backward() left in b.  The orthogonalized
+    update of a matrix [R, C] is scaled by 0.2 sqrt(max(R, C)): entries of 0.2 on average."""
+    for n in m.names:
+        w = p[n]
+        G, R, C = w.shape
+        moe_muon(G, R, C, getattr(b, "d" + n), m.mom[n], m.master[n], w if w.dtype == torch.bfloat16 else None, m.ws,
+                 lr=lr, momentum=momentum, weight_decay=weight_decay, scale=0.2 * max(R, C) ** 0.5, nesterov=nesterov,
+                 coef=coef, stream=stream)

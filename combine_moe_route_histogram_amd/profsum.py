@@ -65,7 +65,8 @@ def _code_only(text: str) -> str:
 
 
 # Sources that hold none of the kernels in CALL_KERNEL, nor anything these are launched by.
-OTHER_SOURCES = {"decode.hip", "decode.hpp", "mx.hip"}
+OTHER_SOURCES = {"decode.hip", "decode.hpp", "mx.hip", "balance.hip", "balance.hpp", "muon.hip", "muon.hpp",
+                 "train_api.hip", "moe_train.h"}
 
 
 def source_fingerprint() -> str:

@@ -432,4 +432,6 @@ int moe_mx_dequantize(int G, int K, int N, int dtype, const void* mx, void* w, v
 }
 #endif
 
+#include "moe_train.h"   /* router losses, update of the experts' weights */
+
 #endif /* MOE_H */
