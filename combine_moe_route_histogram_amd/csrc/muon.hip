@@ -7,13 +7,16 @@
 // so 3 s^2 l + s^3 multiply-adds a step of 4 s^2 l + 2 s^3: bound by the matrix cores where the
 // matrices are large, by the chain of launches where they are small.
 //
-// Numbers.  X is kept as two fp16 parts (22 bits), scaled by 2^10: |x| <= 64 fits, and an
-// element of 1e-5 still has all its bits.  The products take the upper parts (11 bits) with f32
-// sums; a X is formed in f32 from both parts.  The roundings of a product then act on X from the
-// left only, inside its row space, and are not amplified by the steps: 1e-3 to 2e-3 of the
-// result's norm for any rank.  (X in one fp16 part: 2e-2 for rank 64 of 352, as null directions'
-// roundings grow 3.4-fold a step; everything in bf16: 1e-2 for a full rank and 0.2 for that one.)
-// The exact form takes three products, lo hi + hi lo + hi hi, of X, A and B in two parts each.
+// Numbers.  X is kept in fp16, scaled by 2^10 (|x| <= 64 fits, an element of 1e-5 still has all
+// its bits), at first as two parts hi + lo (22 bits).  The products take the upper parts (11 bits)
+// with f32 sums; a X is formed in f32 from both parts.  The roundings of a product then act on X
+// from the left only, inside its row space, while a rounding of X itself has null directions, which
+// every later step makes |a| times larger.  So X drops its lower part when what the steps left
+// can make of it is small (kDropLow), and from there on a is part of B's diagonal: X <- (a I + B) X
+// without a second look at X.  That is 1e-3 to 3e-3 of the result's norm for any rank (no lower parts
+// at all: 2e-2 for rank 64 of 352, 7e-2 for rank 4; everything in bf16: 1e-2 for a full rank and 0.2,
+// 0.6 for those), with 40 % fewer bytes for X than two parts all the way.
+// The exact form takes three products, lo hi + hi lo + hi hi, of X, A and a I + B in two parts each.
 #include "muon.hpp"
 
 #include "gemm_tile.hpp"
@@ -28,7 +31,8 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 constexpr float kXScale = 1024.f;   // of stored X
 constexpr float kAScale = 256.f;    // of stored A and B
 
-enum NewtonKind { kGram, kPoly, kStep, kOut, kUpdate };
+// kAdd: kStep that adds a X from both parts of X
+enum NewtonKind { kGram, kPoly, kStep, kAdd, kOut, kUpdate };
 
 // One product of a batch of matrices.  Operands and results are [batch][rows][ld] fp16 planes.
 struct Product {
@@ -37,11 +41,11 @@ struct Product {
   int lda, ldb, k_len;
   int m_len, n_len;         // padded sizes of the result
   int mt, nt, per, tiles;   // tile grid, tiles of a matrix and of all
-  const uint16_t *ch, *cl;  // what the epilogue adds: A (kPoly) or X (kStep, kOut, kUpdate)
-  uint16_t *oh, *ol;        // kGram, kPoly, kStep
+  const uint16_t *ch, *cl;  // what the epilogue adds: A (kPoly) or X (kAdd)
+  uint16_t *oh, *ol;        // kGram, kPoly, kStep, kAdd; ol NULL: upper parts only
   int64_t o_mat;
   int ldo;                  // of ch, cl, oh, ol
-  float a, b, c;
+  float a, b, c;            // kPoly: a for the diagonal, or 0
   // kOut, kUpdate
   bool tall, bf16;
   int R, C, g0;
@@ -52,9 +56,9 @@ struct Product {
   float lr, weight_decay, scale;
 };
 
-template <int BM_, int BN_, int WGM_, int WGN_, bool B_MN_>
+template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int STAGES_, bool B_MN_>
 struct NsCfg {
-  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, STAGES = 2, BK = 64;
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, BK = BK_, STAGES = STAGES_;
   static constexpr bool B_MN = B_MN_;
   static constexpr int NW = WGM * WGN, NT = NW * kWave;
   static constexpr int WM = BM / WGM, WN = BN / WGN, MI = WM / 32, NJ = WN / 32;
@@ -73,12 +77,12 @@ __device__ __forceinline__ void split16(const float* v, u32x2& hi, u32x2& lo) {
   hi = __builtin_bit_cast(u32x2, h);
   lo = __builtin_bit_cast(u32x2, l);
 }
-__device__ __forceinline__ void join16(const uint16_t* hp, const uint16_t* lp, float* v) {
-  const f16x4 h = __builtin_bit_cast(f16x4, *reinterpret_cast<const u32x2*>(hp));
+__device__ __forceinline__ void join16(const u32x2& hi, const u32x2* lo, float* v) {
+  const f16x4 h = __builtin_bit_cast(f16x4, hi);
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
-  if (lp) {
-    const f16x4 l = __builtin_bit_cast(f16x4, *reinterpret_cast<const u32x2*>(lp));
+  if (lo) {
+    const f16x4 l = __builtin_bit_cast(f16x4, *lo);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += (float)l[e];
   }
@@ -119,22 +123,45 @@ __device__ __forceinline__ void emit4(const Product& p, int64_t g, int row, int 
 }
 
 // Accumulators to results: 32 x 64 blocks through the wave's LDS region, as in the layer's tiles.
+// What is added is loaded one block ahead (unconditional loads, clamped into the matrix: a branch
+// for each would make the waits conservative).
 template <int KIND, bool EXACT, class C>
 __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int m0, int n0, bool mirror,
                                                 const f32x16 (&acc)[C::MI][C::NJ],
-                                                uint8_t* const (&stages)[4], int wave, int lane) {
+                                                uint8_t* const (&stages)[4], int wm, int wn, int wave,
+                                                int lane) {
   constexpr int kRps = C::STAGE_BYTES / kEpiRegionBytes;
   static_assert(kRps >= 1 && (C::NW + kRps - 1) / kRps <= C::STAGES, "epilogue regions fit in the slices");
-  const int wm = wave / C::WGN, wn = wave % C::WGN;
-  uint8_t* const rbase = wave / kRps == 0 ? stages[0] : stages[1];
-  float* reg = reinterpret_cast<float*>(rbase + (wave % kRps) * kEpiRegionBytes);
+  constexpr int kBlocks = C::MI * (C::NJ / 2);
+  constexpr bool kSym = KIND == kGram || KIND == kPoly, kLast = KIND == kOut || KIND == kUpdate;
+  constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kAdd || (KIND == kPoly && EXACT);
+  const int rs = wave / kRps;
+  uint8_t* const rbase = rs == 0 ? stages[0] : rs == 1 ? stages[1] : rs == 2 ? stages[2] : stages[3];
+  float* reg = reinterpret_cast<float*>(rbase + (wave - rs * kRps) * kEpiRegionBytes);
   float lr = 0.f;
   if constexpr (KIND == kUpdate) lr = p.lr_dev ? *p.lr_dev : p.lr;
   const int64_t obase = g * p.o_mat;
+  const bool turn = kSym ? mirror : kLast && p.tall;
+  u32x2 aux_h[2][kAux ? 8 : 1], aux_l[2][kAuxLow ? 8 : 1];
+  auto load_aux = [&](int blk, int buf) {
+    const int mb = m0 + wm * C::WM + 32 * (blk / (C::NJ / 2)), nb = n0 + wn * C::WN + 64 * (blk % (C::NJ / 2));
+#pragma unroll
+    for (int pass = 0; pass < 8; ++pass) {
+      const int m = min(mb, p.m_len - 32) + pass * 4 + (lane >> 4), n = min(nb, p.n_len - 64) + 4 * (lane & 15);
+      const int64_t at = obase + (int64_t)m * p.ldo + n;
+      aux_h[buf][pass] = *reinterpret_cast<const u32x2*>(p.ch + at);
+      if constexpr (kAuxLow) aux_l[buf][pass] = *reinterpret_cast<const u32x2*>(p.cl + at);
+    }
+  };
+  if constexpr (kAux) load_aux(0, 0);
 #pragma unroll
   for (int i = 0; i < C::MI; ++i) {
 #pragma unroll
     for (int hc = 0; hc < C::NJ / 2; ++hc) {
+      const int blk = i * (C::NJ / 2) + hc;
+      if constexpr (kAux) {
+        if (blk + 1 < kBlocks) load_aux(blk + 1, (blk + 1) & 1);
+      }
       const int mb = m0 + wm * C::WM + 32 * i, nb = n0 + wn * C::WN + 64 * hc;
       if (mb >= p.m_len || nb >= p.n_len) continue;   // the sizes are whole blocks
 #pragma unroll
@@ -144,41 +171,40 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
         reg[row * kEpiPitch + 32 + (lane & 31)] = acc[i][2 * hc + 1][r];
       }
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the wave's own region is written
-      const bool turn = KIND == kGram || KIND == kPoly ? mirror : KIND != kStep && p.tall;
 #pragma unroll
       for (int pass = 0; pass < 8; ++pass) {
         const int q = pass * 4 + (lane >> 4), c4 = 4 * (lane & 15);
         const f32x4 s = *reinterpret_cast<const f32x4*>(reg + q * kEpiPitch + c4);
-        const int64_t at = obase + (int64_t)(mb + q) * p.ldo + nb + c4;
+        const int m = mb + q, n = nb + c4;
         float v[4], x[4];
+        if constexpr (kAux) join16(aux_h[blk & 1][pass], kAuxLow ? &aux_l[blk & 1][pass] : nullptr, x);
         if constexpr (KIND == kGram) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = s[e] * (kAScale / (kXScale * kXScale));
         } else if constexpr (KIND == kPoly) {
-          join16(p.ch + at, EXACT ? p.cl + at : nullptr, x);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = p.b * x[e] + p.c * (s[e] * (1.f / kAScale));
-        } else {
-          join16(p.ch + at, p.cl + at, x);
+          for (int e = 0; e < 4; ++e)
+            v[e] = p.b * x[e] + p.c * (s[e] * (1.f / kAScale)) + (m == n + e ? p.a * kAScale : 0.f);
+        } else if constexpr (KIND == kAdd) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = p.a * x[e] + s[e] * (1.f / kAScale);
-          if constexpr (KIND != kStep) {
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= 1.f / kXScale;
-          }
+          for (int e = 0; e < 4; ++e) v[e] = s[e] * (kLast ? 1.f / (kAScale * kXScale) : 1.f / kAScale);
         }
-        if constexpr (KIND == kGram || KIND == kPoly || KIND == kStep) {
+        if constexpr (!kLast) {
+          const int64_t at = obase + (int64_t)m * p.ldo + n;
           u32x2 hi, lo;
           split16(v, hi, lo);
           *reinterpret_cast<u32x2*>(p.oh + at) = hi;
-          if (EXACT || KIND == kStep) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
+          if (EXACT || (!kSym && p.ol)) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
         } else if (!turn) {
-          emit4<KIND>(p, p.g0 + g, mb + q, nb + c4, v, lr);
+          emit4<KIND>(p, p.g0 + g, m, n, v, lr);
         }
-        if (KIND != kStep && turn)
+        if ((kSym || kLast) && turn)
           *reinterpret_cast<f32x4*>(reg + q * kEpiPitch + c4) = f32x4{v[0], v[1], v[2], v[3]};
       }
-      if (KIND != kStep && turn) {   // the block's transpose: 64 rows of 32
+      if ((kSym || kLast) && turn) {   // the block's transpose: 64 rows of 32
         __builtin_amdgcn_s_waitcnt(0xC07F);
 #pragma unroll
         for (int pass = 0; pass < 8; ++pass) {
@@ -186,13 +212,13 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = reg[(m4 + e) * kEpiPitch + n];
-          if constexpr (KIND == kGram || KIND == kPoly) {
+          if constexpr (kSym) {
             const int64_t at = obase + (int64_t)(nb + n) * p.ldo + mb + m4;
             u32x2 hi, lo;
             split16(v, hi, lo);
             *reinterpret_cast<u32x2*>(p.oh + at) = hi;
             if (EXACT) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
-          } else if constexpr (KIND != kStep) {
+          } else if constexpr (kLast) {
             emit4<KIND>(p, p.g0 + g, nb + n, mb + m4, v, lr);
           }
         }
@@ -232,7 +258,9 @@ void newton_kernel(Product p) {
   const int m_valid = min(C::BM, p.m_len - m0), n_valid = min(C::BN, p.n_len - n0);
   const int64_t a0 = g * p.a_mat + (int64_t)m0 * p.lda;
   const int64_t b0 = g * p.b_mat + (C::B_MN ? (int64_t)n0 : (int64_t)n0 * p.ldb);
-  const int wm = wave / C::WGN, wn = wave % C::WGN;
+  // a tile with half of its columns valid keeps a wave with work on every SIMD (see wave_block)
+  const bool spread = C::WGM == 2 && C::WGN == 4 && n_valid <= C::BN / 2 && m_valid > C::BM / 2;
+  const int wm = spread ? wave % C::WGM : wave / C::WGN, wn = spread ? wave / C::WGM : wave % C::WGN;
 
   DmaOperand<C::BM, C::NW, false, 1, false, BK> da;
   DmaOperand<C::BN, C::NW, C::B_MN, 1, false, BK> db;
@@ -260,6 +288,11 @@ void newton_kernel(Product p) {
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
   constexpr int kLoads = decltype(da)::kPerWave + decltype(db)::kPerWave;
   const int nk_pad = (nk + S - 1) / S * S;
+  auto wait_slices = [&](int pending) {   // at most `pending` later slices outstanding
+    if (S >= 4 && pending >= 2) wait_vmcnt<(S >= 4 ? 2 : 0) * kLoads>();
+    else if (S >= 3 && pending >= 1) wait_vmcnt<(S >= 3 ? 1 : 0) * kLoads>();
+    else wait_vmcnt<0>();
+  };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(ring[i], i);
 
@@ -299,7 +332,7 @@ void newton_kernel(Product p) {
     for (int i = 0; i < MI; ++i) av[1][i] = zero;   // "previous step" of slice 0: adds zeros
 #pragma unroll
     for (int j = 0; j < NJ; ++j) bv[1][j] = zero;
-    wait_vmcnt<0>();
+    wait_slices(S - 2);
     lds_barrier();
     for (int kt0 = 0; kt0 < nk_pad; kt0 += S) {
 #pragma unroll
@@ -315,7 +348,7 @@ void newton_kernel(Product p) {
             interleave_step<0, NA * NJ, kReads, 0>();
           __builtin_amdgcn_sched_barrier(0);
         }
-        wait_vmcnt<0>();
+        wait_slices(min(S - 2, nk_pad - 2 - (kt0 + i)));
         lds_barrier();
       }
     }
@@ -324,7 +357,7 @@ void newton_kernel(Product p) {
   const int na = wn * C::WN >= n_valid ? 0 : max(0, min(MI, (m_valid - wm * C::WM + 31) / 32));
   with_count<MI>(__builtin_amdgcn_readfirstlane(na), loop);
   __syncthreads();
-  newton_epilogue<KIND, EXACT, C>(p, g, m0, n0, kSym && tm != tn, acc, ring, wave, lane);
+  newton_epilogue<KIND, EXACT, C>(p, g, m0, n0, kSym && tm != tn, acc, ring, wm, wn, wave, lane);
 }
 
 // --------------------------------------------------------- before the products
@@ -379,11 +412,11 @@ __global__ __launch_bounds__(256) void newton_squares_kernel(Source s) {
   if (tid == 0) s.sums[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X = U / |U| as two fp16 parts, zeros in the padding: one 64 x 64 tile of X for each block.  Tall
+// X = U / |U| in fp16 parts, zeros in the padding: one 64 x 64 tile of X for each block.  Tall
 // matrices are turned on the way, through LDS.
 template <int V>
 __global__ __launch_bounds__(256) void newton_start_kernel(Source s, bool tall, int sp, int lp, uint16_t* xh,
-                                                           uint16_t* xl) {
+                                                           uint16_t* xl) {   // xl NULL: upper parts only
   __shared__ float tile[64][65];
   const int tid = threadIdx.x, lane = tid & 63;
   const int ct = lp / 64, per = ct * (sp / 64);
@@ -445,7 +478,7 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Source s, bool tall, 
     split16(v, hi, lo);
     const int64_t at = (b * sp + x) * lp + y;
     *reinterpret_cast<u32x2*>(xh + at) = hi;
-    *reinterpret_cast<u32x2*>(xl + at) = lo;
+    if (xl) *reinterpret_cast<u32x2*>(xl + at) = lo;
   }
 }
 
@@ -466,14 +499,35 @@ hipError_t product_with(Product p, int batch, hipStream_t st) {
 
 template <int KIND>
 hipError_t product(const Product& p, bool exact, int batch, hipStream_t st) {
-  constexpr bool kMn = KIND == kStep || KIND == kOut || KIND == kUpdate;
-  using Big = NsCfg<256, 256, 2, 4, kMn>;
-  using Small = NsCfg<128, 128, 2, 2, kMn>;
+  constexpr bool kMn = KIND != kGram && KIND != kPoly;
+#ifndef NS_BIG_STEP
+#define NS_BIG_STEP 256, 256, 2, 4, 64, 2
+#endif
+#ifndef NS_BIG_SYM
+#define NS_BIG_SYM 256, 256, 2, 4, 64, 2
+#endif
+  using Big = std::conditional_t<kMn, NsCfg<NS_BIG_STEP, true>, NsCfg<NS_BIG_SYM, false>>;
+  using Small = NsCfg<128, 128, 2, 2, 64, 2, kMn>;
   const int64_t mt = (p.m_len + 255) / 256, nt = (p.n_len + 255) / 256;
   const int64_t tiles = batch * (kMn ? mt * nt : mt * (mt + 1) / 2);
-  if (tiles >= 256)
-    return exact ? product_with<KIND, true, Big>(p, batch, st) : product_with<KIND, false, Big>(p, batch, st);
-  return exact ? product_with<KIND, true, Small>(p, batch, st) : product_with<KIND, false, Small>(p, batch, st);
+  if constexpr (KIND != kAdd) {
+    if (exact)
+      return tiles >= 256 ? product_with<KIND, true, Big>(p, batch, st) : product_with<KIND, true, Small>(p, batch, st);
+  }
+  return tiles >= 256 ? product_with<KIND, false, Big>(p, batch, st) : product_with<KIND, false, Small>(p, batch, st);
+}
+
+// Whether X keeps its lower part for step k: a rounding of X (2^-12 of an element) has null
+// directions, which the steps from k on make up to |a_k a_k+1 ...| times larger.  Up to
+// kDropLow that stays at 3e-3 of the norm, next to 1e-3 to 2e-3 of the products' own roundings; for the
+// last step it is only its own |a|.
+constexpr float kDropLow = 12.f;
+bool keeps_low(const NewtonCall& c, int k) {
+  if (c.p.exact) return true;
+  if (k == c.steps - 1) return false;
+  float grow = 1.f;
+  for (int j = k; j < c.steps; ++j) grow *= fmaxf(1.f, fabsf(c.coef[j][0]));
+  return grow > kDropLow;
 }
 
 }  // namespace
@@ -532,16 +586,19 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
     const int64_t want = (n + 4095) / 4096;   // 16 elements or more to a thread
     s.parts = (int)(want < kNormParts ? want : kNormParts);
     const unsigned tiles = (unsigned)((int64_t)batch * (p.sp / 64) * (p.lp / 64));
+    uint16_t* const xl0 = keeps_low(c, 0) ? at(p.xl[0]) : nullptr;
     const dim3 sq(s.parts, batch);
     if (n % 4 == 0) newton_squares_kernel<4><<<sq, 256, 0, st>>>(s);
     else newton_squares_kernel<1><<<sq, 256, 0, st>>>(s);
-    if (p.C % 4 == 0) newton_start_kernel<4><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), at(p.xl[0]));
-    else newton_start_kernel<1><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), at(p.xl[0]));
+    if (p.C % 4 == 0) newton_start_kernel<4><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), xl0);
+    else newton_start_kernel<1><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), xl0);
     for (int k = 0; k < c.steps; ++k) {
       const uint16_t *xh = at(p.xh[k & 1]), *xl = at(p.xl[k & 1]);
       const int64_t x_mat = (int64_t)p.sp * p.lp, a_mat = (int64_t)p.sp * p.sp;
+      const bool last = k + 1 == c.steps, add = !p.exact && keeps_low(c, k);
       Product q{};
-      q.a = c.coef[k][0]; q.b = c.coef[k][1]; q.c = c.coef[k][2];
+      q.b = c.coef[k][1]; q.c = c.coef[k][2];
+      q.a = add ? 0.f : c.coef[k][0];
       q.ah = xh; q.al = xl; q.bh = xh; q.bl = xl;
       q.a_mat = q.b_mat = x_mat;
       q.lda = q.ldb = q.k_len = p.lp;
@@ -556,16 +613,17 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
       q.oh = bh; q.ol = bl;
       e = product<kPoly>(q, p.exact, batch, st);
       if (e != hipSuccess) return e;
+      q.a = c.coef[k][0];
       q.ah = bh; q.al = bl; q.bh = xh; q.bl = xl;
       q.a_mat = a_mat; q.b_mat = x_mat;
       q.lda = q.k_len = p.sp; q.ldb = p.lp;
       q.n_len = p.lp;
       q.ch = xh; q.cl = xl;
       q.o_mat = x_mat; q.ldo = p.lp;
-      if (k + 1 < c.steps) {
+      if (!last) {
         q.oh = at(p.xh[(k + 1) & 1]);
-        q.ol = at(p.xl[(k + 1) & 1]);
-        e = product<kStep>(q, p.exact, batch, st);
+        q.ol = keeps_low(c, k + 1) ? at(p.xl[(k + 1) & 1]) : nullptr;
+        e = add ? product<kAdd>(q, p.exact, batch, st) : product<kStep>(q, p.exact, batch, st);
       } else {
         q.tall = p.tall; q.bf16 = c.bf16;
         q.R = p.R; q.C = p.C; q.g0 = g0;

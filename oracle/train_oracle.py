@@ -96,7 +96,10 @@ def _chain(p, q):
 
 
 def newton_model(u, exact, coef=COEF):
-    """The iteration as the products round it: X in two fp16 parts, factors of one part (exact: two)."""
+    """The iteration as the products round it.  X has two fp16 parts, of which the lower one is dropped from
+    the step on whose |a|, with those of the later steps, make at most 12 (never in the exact form, always
+    for the last step otherwise); a X is added from both parts, or, once there is one part and in the exact form,
+    a is part of B's diagonal.  Factors have one part (exact: two)."""
     x = np.asarray(u, np.float64)
     tall = x.shape[0] > x.shape[1]
     if tall:
@@ -109,12 +112,18 @@ def newton_model(u, exact, coef=COEF):
             return _chain(np.concatenate([p[1], p[0], p[0]], 1), np.concatenate([q[0], q[1], q[0]], 0))
         return _chain(p[0], q[0])
     f = np.float32
-    for a, b, c in coef:
-        xs = _parts(x, 1024)
+    for k, (a, b, c) in enumerate(coef):
+        low = exact or (k + 1 < len(coef) and np.prod([max(1.0, abs(s[0])) for s in coef[k:]]) > 12)
+        xs = _parts(x, 1024) if low else (_half(x, 1024), np.zeros_like(x))
         A = _parts(mul(xs, (xs[0].T, xs[1].T)), 256)
         whole = A[0] + A[1] if exact else A[0]
-        B = _parts(f(b) * whole + f(c) * mul(A, A), 256)
-        x = f(a) * (xs[0] + xs[1]) + mul(B, xs)
+        add = low and not exact
+        B = f(b) * whole + f(c) * mul(A, A)
+        if not add:
+            B = B + f(a) * np.eye(len(B), dtype=f)
+        x = mul(_parts(B, 256), xs)
+        if add:
+            x = f(a) * (xs[0] + xs[1]) + x
     return x.T if tall else x
 
 
