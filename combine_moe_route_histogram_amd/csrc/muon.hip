@@ -43,8 +43,9 @@ struct Product {
   int mt, nt, per, tiles;   // tile grid, tiles of a matrix and of all
   const uint16_t *ch, *cl;  // what the epilogue adds: A (kPoly) or X (kAdd)
   uint16_t *oh, *ol;        // kGram, kPoly, kStep, kAdd; ol NULL: upper parts only
+  uint16_t *th, *tl;        // small tiles, kStep and kAdd: the result's transpose
   int64_t o_mat;
-  int ldo;                  // of ch, cl, oh, ol
+  int ldo, ldt;             // of ch, cl, oh, ol; of th, tl
   float a, b, c;            // kPoly: a for the diagonal, or 0
   // kOut, kUpdate
   bool tall, bf16;
@@ -122,6 +123,20 @@ __device__ __forceinline__ void emit4(const Product& p, int64_t g, int row, int 
   }
 }
 
+// Result of four elements of row m from column n on: their sums s and the values x that are added.
+template <int KIND>
+__device__ __forceinline__ void finish4(const Product& p, int m, int n, const float* s, const float* x, float* v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (KIND == kGram) v[e] = s[e] * (kAScale / (kXScale * kXScale));
+    else if constexpr (KIND == kPoly)
+      v[e] = p.b * x[e] + p.c * (s[e] * (1.f / kAScale)) + (m == n + e ? p.a * kAScale : 0.f);
+    else if constexpr (KIND == kAdd) v[e] = p.a * x[e] + s[e] * (1.f / kAScale);
+    else if constexpr (KIND == kStep) v[e] = s[e] * (1.f / kAScale);
+    else v[e] = s[e] * (1.f / (kAScale * kXScale));
+  }
+}
+
 // Accumulators to results: 32 x 64 blocks through the wave's LDS region, as in the layer's tiles.
 // What is added is loaded one block ahead (unconditional loads, clamped into the matrix: a branch
 // for each would make the waits conservative).
@@ -178,20 +193,8 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
         const int m = mb + q, n = nb + c4;
         float v[4], x[4];
         if constexpr (kAux) join16(aux_h[blk & 1][pass], kAuxLow ? &aux_l[blk & 1][pass] : nullptr, x);
-        if constexpr (KIND == kGram) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = s[e] * (kAScale / (kXScale * kXScale));
-        } else if constexpr (KIND == kPoly) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = p.b * x[e] + p.c * (s[e] * (1.f / kAScale)) + (m == n + e ? p.a * kAScale : 0.f);
-        } else if constexpr (KIND == kAdd) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = p.a * x[e] + s[e] * (1.f / kAScale);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = s[e] * (kLast ? 1.f / (kAScale * kXScale) : 1.f / kAScale);
-        }
+        const float sum[4] = {s[0], s[1], s[2], s[3]};
+        finish4<KIND>(p, m, n, sum, x, v);
         if constexpr (!kLast) {
           const int64_t at = obase + (int64_t)m * p.ldo + n;
           u32x2 hi, lo;
@@ -228,6 +231,14 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
   }
 }
 
+// Tile r of the upper triangle (tm <= tn), column by column.
+__device__ __forceinline__ void triangle(int r, int& tm, int& tn) {
+  tn = (int)((sqrtf(8.f * (float)r + 1.f) - 1.f) * 0.5f);
+  while (tn * (tn + 1) / 2 > r) --tn;
+  while ((tn + 1) * (tn + 2) / 2 <= r) ++tn;
+  tm = r - tn * (tn + 1) / 2;
+}
+
 // One tile of a product; same ring of LDS slices and order of instructions as the layer's tiles
 // (run_tile_bf16), on fp16.
 template <int KIND, bool EXACT, class C>
@@ -246,11 +257,8 @@ void newton_kernel(Product p) {
   const int64_t g = L / p.per;
   const int r = L - (int)g * p.per;
   int tm, tn;
-  if constexpr (kSym) {   // columns of the upper triangle: tm <= tn
-    tn = (int)((sqrtf(8.f * (float)r + 1.f) - 1.f) * 0.5f);
-    while (tn * (tn + 1) / 2 > r) --tn;
-    while ((tn + 1) * (tn + 2) / 2 <= r) ++tn;
-    tm = r - tn * (tn + 1) / 2;
+  if constexpr (kSym) {
+    triangle(r, tm, tn);
   } else {
     band_order(r, p.mt, p.nt, 8, tm, tn);
   }
@@ -360,6 +368,172 @@ void newton_kernel(Product p) {
   newton_epilogue<KIND, EXACT, C>(p, g, m0, n0, kSym && tm != tn, acc, ring, wm, wn, wave, lane);
 }
 
+// Tiles of few or small matrices, where a launch is over in microseconds and the time is that of its
+// longest chain: T x T tiles for many blocks, k split over the block's four waves (slices of 64 k in
+// turn).  Each wave copies its own slices to LDS, with no barrier, one or two ahead; copies of whole
+// 128-byte row pieces, as fragments read from memory touch 32 rows at 32 bytes each and take twice
+// the time.  Both operands lie along k (X is kept with its transpose); the waves' sums meet in LDS in a fixed
+// order.
+template <int KIND, bool EXACT, int T>
+__global__ __launch_bounds__(256) void newton_small_kernel(Product p) {
+  constexpr bool kSym = KIND == kGram || KIND == kPoly, kLast = KIND == kOut || KIND == kUpdate;
+  constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kAdd || (KIND == kPoly && EXACT);
+  constexpr int B = T / 32;                       // 32-wide blocks of a side
+  constexpr int P = EXACT ? 2 : 1;                // parts of a factor
+  constexpr int D = T == 32 ? 2 : 1;              // slices of a wave in LDS
+  constexpr int kPlane = T * 64 * 2, kSlice = 2 * P * kPlane, kPart = 4 * T * (T + 1) * 4;
+  // separate LDS objects, so that the copies into one do not hold up reads of the other
+  __shared__ __align__(16) uint8_t ring0[4 * kSlice > kPart ? 4 * kSlice : kPart];
+  __shared__ __align__(16) uint8_t ring1[D > 1 ? 4 * kSlice : 16];
+  float (*const part)[T][T + 1] = reinterpret_cast<float (*)[T][T + 1]>(ring0);   // after the products
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
+  const int first = (int)((int64_t)p.tiles * xcd / kXcds);
+  const int L = first + idx;
+  if (L >= (int)((int64_t)p.tiles * (xcd + 1) / kXcds)) return;
+  const int64_t g = L / p.per;
+  const int r = L - (int)g * p.per;
+  int tm, tn;
+  if constexpr (kSym) {
+    triangle(r, tm, tn);
+  } else {
+    tm = r % p.mt;
+    tn = r / p.mt;
+  }
+  const int m0 = tm * T, n0 = tn * T;
+
+  f32x16 acc[B][B];
+#pragma unroll
+  for (int i = 0; i < B; ++i)
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+  DmaOperand<T, 1, false, 1, false, 64> da, db;
+  da.init(p.lda, T, 0, lane);
+  db.init(p.ldb, T, 0, lane);
+  constexpr int kLoads = P * (decltype(da)::kPerWave + decltype(db)::kPerWave);
+  const int64_t a0 = g * p.a_mat + (int64_t)m0 * p.lda, b0 = g * p.b_mat + (int64_t)n0 * p.ldb;
+  const int n_slices = p.k_len / 64;
+  auto issue = [&](uint8_t* st, int c) {
+    da.issue(st, p.ah + a0 + c * 64, nullptr, 0, true, 0);
+    db.issue(st + P * kPlane, p.bh + b0 + c * 64, nullptr, 0, true, 0);
+    if constexpr (EXACT) {
+      da.issue(st + kPlane, p.al + a0 + c * 64, nullptr, 0, true, 0);
+      db.issue(st + 3 * kPlane, p.bl + b0 + c * 64, nullptr, 0, true, 0);
+    }
+  };
+  auto multiply = [&](const uint8_t* st) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      f16x8 av[P][B], bv[P][B];
+#pragma unroll
+      for (int h = 0; h < P; ++h)
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          const int row = 32 * i + (lane & 31), ch = 2 * ks + (lane >> 5);
+          av[h][i] = __builtin_bit_cast(f16x8, kc_frag<64>(st + h * kPlane, row, ch));
+          bv[h][i] = __builtin_bit_cast(f16x8, kc_frag<64>(st + (P + h) * kPlane, row, ch));
+        }
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          if constexpr (EXACT) {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[1][i], bv[0][j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[0][i], bv[1][j], acc[i][j], 0, 0, 0);
+          }
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[0][i], bv[0][j], acc[i][j], 0, 0, 0);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slice is read before it is refilled
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  uint8_t* const st0 = ring0 + wave * kSlice;
+  uint8_t* const st1 = ring1 + (D > 1 ? wave * kSlice : 0);
+  if (wave < n_slices) issue(st0, wave);
+  if (D > 1 && wave + 4 < n_slices) issue(st1, wave + 4);
+  for (int c = wave; c < n_slices; c += 4 * D) {
+    if (D > 1 && c + 4 < n_slices) wait_vmcnt<kLoads>(); else wait_vmcnt<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(st0);
+    if (c + 4 * D < n_slices) issue(st0, c + 4 * D);
+    if (D > 1 && c + 4 < n_slices) {
+      if (c + 8 < n_slices) wait_vmcnt<kLoads>(); else wait_vmcnt<0>();
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(st1);
+      if (c + 12 < n_slices) issue(st1, c + 12);
+    }
+  }
+  // what is added: loaded before the sums meet
+  constexpr int kTurns = T * T / 1024, kCols = T / 4;
+  const int64_t obase = g * p.o_mat;
+  u32x2 aux_h[kAux ? kTurns : 1], aux_l[kAuxLow ? kTurns : 1];
+#pragma unroll
+  for (int it = 0; it < kTurns; ++it) {
+    const int64_t at = obase + (int64_t)(m0 + it * (1024 / T) + tid / kCols) * p.ldo + n0 + 4 * (tid % kCols);
+    if constexpr (kAux) aux_h[it] = *reinterpret_cast<const u32x2*>(p.ch + at);
+    if constexpr (kAuxLow) aux_l[it] = *reinterpret_cast<const u32x2*>(p.cl + at);
+  }
+  __syncthreads();                                // every wave is done with its slices
+#pragma unroll
+  for (int i = 0; i < B; ++i)
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        part[wave][32 * i + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)][32 * j + (lane & 31)] = acc[i][j][q];
+  __syncthreads();
+  float lr = 0.f;
+  if constexpr (KIND == kUpdate) lr = p.lr_dev ? *p.lr_dev : p.lr;
+  const bool turn = kSym ? tm != tn : kLast ? p.tall : true;   // a step writes X and its transpose
+#pragma unroll
+  for (int it = 0; it < kTurns; ++it) {
+    const int row = it * (1024 / T) + tid / kCols, col = 4 * (tid % kCols);
+    const int m = m0 + row, n = n0 + col;
+    float s[4], x[4], v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s[e] = (part[0][row][col + e] + part[1][row][col + e]) + (part[2][row][col + e] + part[3][row][col + e]);
+    if constexpr (kAux) join16(aux_h[it], kAuxLow ? &aux_l[it] : nullptr, x);
+    finish4<KIND>(p, m, n, s, x, v);
+    if constexpr (!kLast) {
+      const int64_t at = obase + (int64_t)m * p.ldo + n;
+      u32x2 hi, lo;
+      split16(v, hi, lo);
+      *reinterpret_cast<u32x2*>(p.oh + at) = hi;
+      if (EXACT || (!kSym && p.ol)) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
+    } else if (!turn) {
+      emit4<KIND>(p, p.g0 + g, m, n, v, lr);
+    }
+    if (turn) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[0][row][col + e] = v[e];   // read by this thread alone so far
+    }
+  }
+  if (!turn) return;
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < kTurns; ++it) {
+    const int n = it * (1024 / T) + tid / kCols, m4 = 4 * (tid % kCols);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = part[0][m4 + e][n];
+    if constexpr (!kLast) {
+      u32x2 hi, lo;
+      split16(v, hi, lo);
+      uint16_t* const th = kSym ? p.oh + obase : p.th + g * p.o_mat;
+      uint16_t* const tl = kSym ? p.ol + obase : p.tl + g * p.o_mat;
+      const int64_t at = (int64_t)(n0 + n) * (kSym ? p.ldo : p.ldt) + m0 + m4;
+      *reinterpret_cast<u32x2*>(th + at) = hi;
+      if (EXACT) *reinterpret_cast<u32x2*>(tl + at) = lo;
+    } else {
+      emit4<KIND>(p, p.g0 + g, n0 + n, m0 + m4, v, lr);
+    }
+  }
+}
+
 // --------------------------------------------------------- before the products
 
 struct Source {
@@ -412,18 +586,23 @@ __global__ __launch_bounds__(256) void newton_squares_kernel(Source s) {
   if (tid == 0) s.sums[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X = U / |U| in fp16 parts, zeros in the padding: one 64 x 64 tile of X for each block.  Tall
-// matrices are turned on the way, through LDS.
+// X = U / |U| in fp16 parts, zeros in the padding: one 64 x 64 tile of the matrix for each block.  Its
+// own orientation goes straight from registers, the other one through LDS: X is the transpose of a
+// tall matrix; th and tl (small matrices) take the transpose of X.
+struct Start {
+  bool tall;
+  int sp, lp;
+  uint16_t *xh, *xl, *th, *tl;   // xl, tl NULL: upper parts only; th NULL: X alone
+};
 template <int V>
-__global__ __launch_bounds__(256) void newton_start_kernel(Source s, bool tall, int sp, int lp, uint16_t* xh,
-                                                           uint16_t* xl) {   // xl NULL: upper parts only
+__global__ __launch_bounds__(256) void newton_start_kernel(Source s, Start d) {
   __shared__ float tile[64][65];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int ct = lp / 64, per = ct * (sp / 64);
+  const int rp = d.tall ? d.lp : d.sp, cp = d.tall ? d.sp : d.lp;
+  const int ct = cp / 64, per = ct * (rp / 64);
   const int64_t b = blockIdx.x / per;
   const int rem = (int)(blockIdx.x - b * per);
-  const int x0 = rem / ct * 64, y0 = rem % ct * 64;    // of X: row, column
-  const int r0 = tall ? y0 : x0, c0 = tall ? x0 : y0;  // of the matrix
+  const int r0 = rem / ct * 64, c0 = rem % ct * 64;
   const int64_t base = (s.g0 + b) * s.R * s.C;
   float u[4][4];
 #pragma unroll
@@ -457,29 +636,34 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Source s, bool tall, 
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, kWave);
   // zeros stay zeros; an infinity or NaN anywhere makes the whole matrix NaN
   const double inv = sum == 0.0 ? 0.0 : sum < (double)INFINITY ? (double)kXScale / sqrt(sum) : (double)NAN;
-  if (tall) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) tile[(tid >> 4) + 16 * j][4 * (tid & 15) + e] = u[j][e];
-    __syncthreads();
+    for (int e = 0; e < 4; ++e) u[j][e] = (float)((double)u[j][e] * inv);
+  auto store = [&](uint16_t* hp, uint16_t* lp, int rows, int ld, int x0, int y0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+      u32x2 hi, lo;
+      split16(u[j], hi, lo);
+      const int64_t at = (b * rows + x0 + (tid >> 4) + 16 * j) * ld + y0 + 4 * (tid & 15);
+      *reinterpret_cast<u32x2*>(hp + at) = hi;
+      if (lp) *reinterpret_cast<u32x2*>(lp + at) = lo;
+    }
+  };
+  uint16_t *const own_h = d.tall ? d.th : d.xh, *const own_l = d.tall ? d.tl : d.xl;
+  uint16_t *const turned_h = d.tall ? d.xh : d.th, *const turned_l = d.tall ? d.xl : d.tl;
+  if (own_h) store(own_h, own_l, rp, cp, r0, c0);
+  if (!turned_h) return;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[j][e] = tile[4 * (tid & 15) + e][(tid >> 4) + 16 * j];
-  }
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int x = x0 + (tid >> 4) + 16 * j, y = y0 + 4 * (tid & 15);
-    float v[4];
+    for (int e = 0; e < 4; ++e) tile[(tid >> 4) + 16 * j][4 * (tid & 15) + e] = u[j][e];
+  __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)((double)u[j][e] * inv);
-    u32x2 hi, lo;
-    split16(v, hi, lo);
-    const int64_t at = (b * sp + x) * lp + y;
-    *reinterpret_cast<u32x2*>(xh + at) = hi;
-    if (xl) *reinterpret_cast<u32x2*>(xl + at) = lo;
-  }
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[j][e] = tile[4 * (tid & 15) + e][(tid >> 4) + 16 * j];
+  store(turned_h, turned_l, cp, rp, c0, r0);
 }
 
 // ---------------------------------------------------------------------- host
@@ -497,24 +681,38 @@ hipError_t product_with(Product p, int batch, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int KIND>
-hipError_t product(const Product& p, bool exact, int batch, hipStream_t st) {
+template <int KIND, bool EXACT, int T>
+hipError_t product_small(Product p, int batch, hipStream_t st) {
+  p.mt = p.m_len / T;
+  p.nt = p.n_len / T;
+  p.per = KIND == kGram || KIND == kPoly ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
+  p.tiles = p.per * batch;
+  const unsigned grid = (unsigned)kXcds * ((p.tiles + kXcds - 1) / kXcds);
+  newton_small_kernel<KIND, EXACT, T><<<grid, 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <int KIND, bool EXACT>
+hipError_t product(const Product& p, bool small, int batch, hipStream_t st) {
   constexpr bool kMn = KIND != kGram && KIND != kPoly;
-#ifndef NS_BIG_STEP
-#define NS_BIG_STEP 256, 256, 2, 4, 64, 2
-#endif
-#ifndef NS_BIG_SYM
-#define NS_BIG_SYM 256, 256, 2, 4, 64, 2
-#endif
-  using Big = std::conditional_t<kMn, NsCfg<NS_BIG_STEP, true>, NsCfg<NS_BIG_SYM, false>>;
-  using Small = NsCfg<128, 128, 2, 2, 64, 2, kMn>;
-  const int64_t mt = (p.m_len + 255) / 256, nt = (p.n_len + 255) / 256;
-  const int64_t tiles = batch * (kMn ? mt * nt : mt * (mt + 1) / 2);
-  if constexpr (KIND != kAdd) {
-    if (exact)
-      return tiles >= 256 ? product_with<KIND, true, Big>(p, batch, st) : product_with<KIND, true, Small>(p, batch, st);
+  using Big = NsCfg<256, 256, 2, 4, 64, 2, kMn>;
+  using Mid = NsCfg<128, 128, 2, 2, 64, 2, kMn>;
+  auto tiles = [&](int t) {
+    const int64_t mt = (p.m_len + t - 1) / t, nt = (p.n_len + t - 1) / t;
+    return batch * (kMn ? mt * nt : mt * (mt + 1) / 2);
+  };
+  // 32 x 32 tiles until there are two for each CU: whole calls of [512, 512] 95 us with them and 148
+  // with 64 x 64 ones (f32), of [1024, 1024] 296 and 223
+  if (small)
+    return tiles(32) <= 512 ? product_small<KIND, EXACT, 32>(p, batch, st) : product_small<KIND, EXACT, 64>(p, batch, st);
+  return tiles(256) >= 256 ? product_with<KIND, EXACT, Big>(p, batch, st) : product_with<KIND, EXACT, Mid>(p, batch, st);
+}
+template <int KIND>
+hipError_t product(const Product& q, const NewtonPlan& p, int batch, hipStream_t st) {
+  if constexpr (KIND != kAdd) {   // the exact form has a in B's diagonal
+    if (p.exact) return product<KIND, true>(q, p.small, batch, st);
   }
-  return tiles >= 256 ? product_with<KIND, false, Big>(p, batch, st) : product_with<KIND, false, Small>(p, batch, st);
+  return product<KIND, false>(q, p.small, batch, st);
 }
 
 // Whether X keeps its lower part for step k: a rounding of X (2^-12 of an element) has null
@@ -540,7 +738,11 @@ NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
   p.l = p.tall ? R : C;
   p.sp = up(p.s, kNewtonPad);
   p.lp = up(p.l, kNewtonPad);
-  p.exact = !bf16;
+  p.exact = !bf16 || p.s < kNewtonFewRows;
+  // Small tiles where 256 x 256 and 128 x 128 ones leave CUs without work, unless k is long: whole calls of
+  // 8 [512, 1024] 178 us with them and 206 without (bf16), 32 [256, 256] 119 and 139; of [2048, 2048] 451 and 414,
+  // of 128 [256, 256] 289 and 218.
+  p.small = (int64_t)G * (p.sp / 64) * (p.lp / 64) <= 1024 && p.sp <= 1024;
   // About 2048 tiles of 256 x 256 to a launch: 8 rounds over the 256 CUs, of which the last one
   // is partly empty; more would only take memory (at most 2^30 elements of X, or one matrix).
   const int64_t t = (p.sp + 255) / 256, tiles = t * (t + 1) / 2;
@@ -560,6 +762,8 @@ NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
   for (int i = 0; i < 2; ++i) {
     p.xh[i] = take(x);
     p.xl[i] = take(x);
+    p.th[i] = take(p.small ? x : 0);
+    p.tl[i] = take(p.small && p.exact ? x : 0);
   }
   p.ah = take(a);
   p.bh = take(a);
@@ -586,12 +790,13 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
     const int64_t want = (n + 4095) / 4096;   // 16 elements or more to a thread
     s.parts = (int)(want < kNormParts ? want : kNormParts);
     const unsigned tiles = (unsigned)((int64_t)batch * (p.sp / 64) * (p.lp / 64));
-    uint16_t* const xl0 = keeps_low(c, 0) ? at(p.xl[0]) : nullptr;
+    Start d{p.tall, p.sp, p.lp, at(p.xh[0]), keeps_low(c, 0) ? at(p.xl[0]) : nullptr,
+            p.small ? at(p.th[0]) : nullptr, p.small && p.exact ? at(p.tl[0]) : nullptr};
     const dim3 sq(s.parts, batch);
     if (n % 4 == 0) newton_squares_kernel<4><<<sq, 256, 0, st>>>(s);
     else newton_squares_kernel<1><<<sq, 256, 0, st>>>(s);
-    if (p.C % 4 == 0) newton_start_kernel<4><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), xl0);
-    else newton_start_kernel<1><<<tiles, 256, 0, st>>>(s, p.tall, p.sp, p.lp, at(p.xh[0]), xl0);
+    if (p.C % 4 == 0) newton_start_kernel<4><<<tiles, 256, 0, st>>>(s, d);
+    else newton_start_kernel<1><<<tiles, 256, 0, st>>>(s, d);
     for (int k = 0; k < c.steps; ++k) {
       const uint16_t *xh = at(p.xh[k & 1]), *xl = at(p.xl[k & 1]);
       const int64_t x_mat = (int64_t)p.sp * p.lp, a_mat = (int64_t)p.sp * p.sp;
@@ -604,32 +809,37 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
       q.lda = q.ldb = q.k_len = p.lp;
       q.m_len = q.n_len = p.sp;
       q.oh = ah; q.ol = al; q.o_mat = a_mat; q.ldo = p.sp;
-      hipError_t e = product<kGram>(q, p.exact, batch, st);
+      hipError_t e = product<kGram>(q, p, batch, st);
       if (e != hipSuccess) return e;
       q.ah = ah; q.al = al; q.bh = ah; q.bl = al;
       q.a_mat = q.b_mat = a_mat;
       q.lda = q.ldb = q.k_len = p.sp;
       q.ch = ah; q.cl = al;
       q.oh = bh; q.ol = bl;
-      e = product<kPoly>(q, p.exact, batch, st);
+      e = product<kPoly>(q, p, batch, st);
       if (e != hipSuccess) return e;
       q.a = c.coef[k][0];
-      q.ah = bh; q.al = bl; q.bh = xh; q.bl = xl;
+      q.ah = bh; q.al = bl;
+      q.bh = p.small ? at(p.th[k & 1]) : xh;
+      q.bl = p.small ? at(p.tl[k & 1]) : xl;
       q.a_mat = a_mat; q.b_mat = x_mat;
-      q.lda = q.k_len = p.sp; q.ldb = p.lp;
+      q.lda = q.k_len = p.sp; q.ldb = p.small ? p.sp : p.lp;
       q.n_len = p.lp;
       q.ch = xh; q.cl = xl;
       q.o_mat = x_mat; q.ldo = p.lp;
       if (!last) {
         q.oh = at(p.xh[(k + 1) & 1]);
         q.ol = keeps_low(c, k + 1) ? at(p.xl[(k + 1) & 1]) : nullptr;
-        e = add ? product<kAdd>(q, p.exact, batch, st) : product<kStep>(q, p.exact, batch, st);
+        q.th = at(p.th[(k + 1) & 1]);
+        q.tl = at(p.tl[(k + 1) & 1]);
+        q.ldt = p.sp;
+        e = add ? product<kAdd>(q, p, batch, st) : product<kStep>(q, p, batch, st);
       } else {
         q.tall = p.tall; q.bf16 = c.bf16;
         q.R = p.R; q.C = p.C; q.g0 = g0;
         q.out = c.out; q.master = c.master; q.w = c.w;
         q.lr_dev = c.lr_dev; q.lr = c.lr; q.weight_decay = c.weight_decay; q.scale = c.scale;
-        e = c.out ? product<kOut>(q, p.exact, batch, st) : product<kUpdate>(q, p.exact, batch, st);
+        e = c.out ? product<kOut>(q, p, batch, st) : product<kUpdate>(q, p, batch, st);
       }
       if (e != hipSuccess) return e;
     }

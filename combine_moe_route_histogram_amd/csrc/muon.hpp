@@ -11,6 +11,9 @@ namespace moe {
 constexpr int kNewtonMaxDim = 1 << 20;
 constexpr int64_t kNewtonMaxMatrix = (int64_t)1 << 32;   // elements: keeps tile and block counts in 31 bits
 constexpr int kNewtonPad = 64;       // of both sides of a stored matrix: whole k slices, zero-filled
+// Fewer rows (or columns) than this take factors of two parts whatever the type: their roundings do
+// not average out (up to 4e-3 of the norm), and the call's time is that of its launches.
+constexpr int kNewtonFewRows = 32;
 constexpr int kNormParts = 256;      // partial sums of a matrix's squares
 
 // Sizes of one call.  A matrix is worked on as X [s, l] with s <= l (the
@@ -20,9 +23,10 @@ struct NewtonPlan {
   bool tall;           // R > C
   int s, l, sp, lp;
   bool exact;          // factors of two fp16 parts (22 bits)
+  bool small;          // small tiles, X kept with its transpose
   int batch;           // matrices worked on at a time
   // workspace sections (byte offsets)
-  size_t parts, xh[2], xl[2], ah, al, bh, bl, total;
+  size_t parts, xh[2], xl[2], th[2], tl[2], ah, al, bh, bl, total;
 };
 NewtonPlan newton_plan(int G, int R, int C, bool bf16);
 

@@ -79,10 +79,12 @@ size_t moe_muon_workspace_bytes(int G, int R, int C, int dtype);
  * dtype MOE_BF16: products of 11-bit (fp16) factors with f32 sums, X itself in 22
  * bits as long as later steps would enlarge its roundings: the result is off by
  * 1e-3 to 3e-3 of its norm, low ranks included (before its rounding to bf16).
- * MOE_F32: factors of 22 bits, as exact as f32 arithmetic.
+ * MOE_F32, and matrices with fewer than 32 rows or columns: factors of 22 bits, as
+ * exact as f32 arithmetic.
  * Any G >= 1 and R, C >= 1 up to 2^20 with R*C <= 2^32 and G*R*C <= 2^39.  A matrix of zeros gives zeros; an infinity
  * or NaN makes its own matrix NaN and no other.  The scale of a matrix has no
- * effect, down to subnormal entries. */
+ * effect, down to subnormal entries.  A matrix's bits depend on its values and on G, R
+ * and C, not on the other matrices. */
 int moe_orthogonalize(int G, int R, int C, int dtype, const moe_newton* n, const float* g, void* out,
                       void* ws, size_t ws_bytes, void* stream);
 
