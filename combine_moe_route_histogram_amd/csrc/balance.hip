@@ -7,8 +7,8 @@
 // Both passes read the logits once and are bound by that read where T E is
 // large, and by their two launches where it is small.
 //
-// A row is spread over a group of G lanes with V consecutive experts each (one
-// 16-byte load where E is a multiple of 4), so the softmax takes log2(G)
+// A row is spread over a group of G lanes with 4 consecutive experts each (one
+// 16-byte load, of whatever alignment), so the softmax takes log2(G)
 // exchanges and a wave works on 64 / G rows at a time: 8 rows and 3 exchanges
 // for 32 experts.  The sums over tokens stay in the lanes' registers until the
 // end of a chunk; chunks' sums are joined in a fixed order (no float atomics).
@@ -19,40 +19,78 @@ namespace moe {
 
 namespace {
 
+// Exchanges inside groups of G lanes without LDS: within 16 lanes by DPP (neighbours, pairs, then the
+// mirror images of 8 and of 16 lanes, whose quads and halves hold one value by then), beyond by swapping
+// rows of 16 and of 32 lanes.  Every lane is active.  (ds_bpermute, which a shuffle compiles to, takes
+// about ten times as long: losses of 131072 tokens 15.6 us with it, see below.)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int G, class Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+  if constexpr (G >= 2) v = op(v, dpp<0xB1>(v));     // quad_perm 1 0 3 2
+  if constexpr (G >= 4) v = op(v, dpp<0x4E>(v));     // quad_perm 2 3 0 1
+  if constexpr (G >= 8) v = op(v, dpp<0x141>(v));    // row_half_mirror
+  if constexpr (G >= 16) v = op(v, dpp<0x140>(v));   // row_mirror
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (G >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return v;
+}
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = G / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
+  return group_reduce<G>(v, [](float x, float y) { return fmaxf(x, y); });
 }
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<G>(v, [](float x, float y) { return x + y; });
+}
+
+// 16 bytes at an address that is a multiple of 4 (rows of E floats need not be 16-byte aligned).
+struct __attribute__((packed, aligned(4))) Loose4 { uint32_t v[4]; };
+__device__ __forceinline__ u32x4 ld16_loose(const void* p) {
+  const Loose4 l = *static_cast<const Loose4*>(p);
+  return u32x4{l.v[0], l.v[1], l.v[2], l.v[3]};
+}
+__device__ __forceinline__ void st16_loose(void* p, const u32x4& v) {
+  *static_cast<Loose4*>(p) = Loose4{{v[0], v[1], v[2], v[3]}};
+}
+// Words [at, at + 4) of a row of n, `none` for those past its end.
+__device__ __forceinline__ u32x4 load_row4(const void* row, int at, int n, bool valid, uint32_t none) {
+  const uint32_t* const p = static_cast<const uint32_t*>(row) + at;
+  u32x4 v = {none, none, none, none};
+  if (valid && at + 4 <= n) {
+    v = ld16_loose(p);
+  } else if (valid && at < n) {
 #pragma unroll
-  for (int o = G / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
+    for (int i = 0; i < 3; ++i)
+      if (at + i < n) v[i] = p[i];
+  }
   return v;
 }
 
-// The experts of a lane: V consecutive ones (NI = 1), or NI single ones 64 apart (V = 1).
-template <int G, int V, int NI>
+// A lane's four experts of a row: G lanes hold it.
+template <int G>
 struct Row {
-  static constexpr int N = V * NI;
+  static constexpr int N = 4;
   static constexpr int kRows = kWave / G;   // rows of a wave at a time
   float v[N];
-  __device__ static __forceinline__ int expert(int gl, int i) { return V > 1 ? gl * V + i : gl + i * G; }
+  __device__ static __forceinline__ int expert(int gl, int i) { return gl * 4 + i; }
   // l[e] of one row; -inf beyond E
-  __device__ __forceinline__ void load(const float* __restrict__ row, int E, int gl, bool valid) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = -INFINITY;
-    if constexpr (V == 4) {
-      if (valid && gl * 4 < E) Elem<float>::unpack(ld16(row + gl * 4), v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (valid && expert(gl, i) < E) v[i] = row[expert(gl, i)];
-    }
+  __device__ __forceinline__ void load(const float* row, int E, int gl, bool valid) {
+    Elem<float>::unpack(load_row4(row, gl * 4, E, valid, 0xFF800000u), v);
   }
-  // v <- softmax; returns the log-sum-exp.  (NaN and +inf rows end as NaN: fmaxf passes over a
-  // NaN, its own exponential does not.)
+  // v <- softmax; returns the log-sum-exp.  The hardware's exponential, logarithm and reciprocal (1 ulp
+  // each; the argument (l - max) log2 e carries one rounding of each factor, and z is in [1, E]): the
+  // libraries' forms would make these kernels wait for the vector units instead of memory (256 experts:
+  // 61 us for 131072 tokens).  NaN and +inf rows end as NaN: fmaxf passes over a NaN, its own
+  // exponential does not.
   __device__ __forceinline__ float softmax() {
     float m = v[0];
 #pragma unroll
@@ -61,44 +99,80 @@ struct Row {
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      v[i] = expf(v[i] - m);
+      v[i] = __builtin_amdgcn_exp2f((v[i] - m) * 1.44269504f);
       z += v[i];
     }
     z = group_sum<G>(z);
-    const float inv = 1.0f / z;
+    const float inv = __builtin_amdgcn_rcpf(z);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] *= inv;
-    return m + logf(z);
+    return fmaf(__builtin_amdgcn_logf(z), 0.693147181f, m);
   }
 };
 
-// Tokens [t0, t1) of one sequence by one wave: sums of p (acc, in the lanes of the first group
-// after the exchange), of lse^2 and the number of tokens (every lane); picks counted into hist
-// (LDS, cleared by the caller).
-template <int G, int V, int NI>
+// Tokens [t0, t1) of one sequence by one wave (at most 64): sums of p (acc, in the lanes of the first
+// group after the exchange), of lse^2 and the number of tokens (every lane); picks counted into hist
+// (LDS, cleared by the caller).  A wave has few rows and each pass over them would wait for memory, so
+// several are loaded ahead.
+template <int G>
 __device__ __forceinline__ void wave_sums(const BalanceArgs& a, int64_t t0, int64_t t1, int lane,
-                                          float (&acc)[V * NI], float& zsum, int& n, int* hist) {
-  using R = Row<G, V, NI>;
+                                          float (&acc)[4], float& zsum, int& n, int* hist) {
+  using R = Row<G>;
+  constexpr int U = G < 8 ? G : 8;                 // of the G passes over 64 rows
   const int gl = lane & (G - 1), sub = lane / G;
+  const int rows = (int)(t1 - t0);
+  const float* const l0 = a.logits + t0 * a.E;
+  const uint8_t* const m0 = a.mask ? a.mask + t0 : nullptr;
+  // picks: K to a token, the first ones loaded ahead of the rows
+  constexpr int kAhead = 4;
+  const int n_pairs = rows * a.K;
+  const int32_t* const i0 = a.topk_idx + t0 * a.K;
+  int pick[kAhead];
+  bool pick_on[kAhead];
+  auto load_pick = [&](int q, int& e, bool& on) {
+    on = q < n_pairs;
+    e = on ? i0[q] : -1;
+    if (m0 && on) on = m0[(unsigned)q / (unsigned)a.K] != 0;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load_pick(lane + kWave * i, pick[i], pick_on[i]);
 #pragma unroll
   for (int i = 0; i < R::N; ++i) acc[i] = 0.f;
   zsum = 0.f;
   n = 0;
-  for (int64_t t = t0; t < t1; t += R::kRows) {
-    const int64_t tok = t + sub;
-    const bool in = tok < t1;
-    const bool used = in && (!a.mask || a.mask[tok] != 0);
-    R r;
-    r.load(a.logits + tok * a.E, a.E, gl, in);
-    const float lse = r.softmax();
-    if (used) {
+  for (int t = 0; t < rows; t += R::kRows * U) {
+    R r[U];
+    bool used[U];
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) acc[i] += r.v[i];
-      if (gl == 0) {
-        zsum += lse * lse;
-        ++n;
+    for (int u = 0; u < U; ++u) {
+      const int row = t + u * R::kRows + sub;
+      const bool in = row < rows;
+      r[u].load(l0 + (int64_t)row * a.E, a.E, gl, in);
+      used[u] = in && (!m0 || m0[row] != 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float lse = r[u].softmax();
+      if (used[u]) {
+#pragma unroll
+        for (int i = 0; i < R::N; ++i) acc[i] += r[u].v[i];
+        if (gl == 0) {
+          zsum += lse * lse;
+          ++n;
+        }
       }
     }
+  }
+  auto count = [&](int e, bool on) {
+    if (on && (unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) count(pick[i], pick_on[i]);
+  for (int q = lane + kWave * kAhead; q < n_pairs; q += kWave) {
+    int e;
+    bool on;
+    load_pick(q, e, on);
+    count(e, on);
   }
 #pragma unroll
   for (int o = G; o < kWave; o <<= 1)
@@ -107,13 +181,6 @@ __device__ __forceinline__ void wave_sums(const BalanceArgs& a, int64_t t0, int6
   zsum = wave_sum(zsum);
 #pragma unroll
   for (int o = kWave / 2; o >= 1; o >>= 1) n += __shfl_xor(n, o, kWave);
-  // picks, K to a token
-  const int64_t n_pairs = (t1 - t0) * a.K;
-  for (int64_t q = lane; q < n_pairs; q += kWave) {
-    const int64_t tok = t0 + q / a.K;
-    const int e = a.topk_idx[t0 * a.K + q];
-    if ((unsigned)e < (unsigned)a.E && (!a.mask || a.mask[tok] != 0)) atomicAdd(&hist[e], 1);
-  }
 }
 
 // The sequence's balance loss from its sums, by one wave (or the first wave of a block).
@@ -122,9 +189,9 @@ __device__ __forceinline__ float sequence_loss(const BalanceArgs& a, int n, floa
 }
 
 // Short sequences: one wave for each, all of its results.
-template <int G, int V, int NI>
+template <int G>
 __global__ __launch_bounds__(256) void balance_short_kernel(BalanceArgs a) {
-  using R = Row<G, V, NI>;
+  using R = Row<G>;
   __shared__ int hists[4][kMaxExperts];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   int* const hist = hists[wave];   // of this wave alone: LDS keeps a wave's accesses in order
@@ -134,7 +201,7 @@ __global__ __launch_bounds__(256) void balance_short_kernel(BalanceArgs a) {
     float acc[R::N], zsum;
     int n;
     const int64_t t0 = s * a.seq_len;
-    wave_sums<G, V, NI>(a, t0, min<int64_t>(a.T, t0 + a.seq_len), lane, acc, zsum, n, hist);
+    wave_sums<G>(a, t0, min<int64_t>(a.T, t0 + a.seq_len), lane, acc, zsum, n, hist);
     __builtin_amdgcn_wave_barrier();
     float dot = 0.f;
     if (lane < G) {
@@ -159,11 +226,11 @@ __global__ __launch_bounds__(256) void balance_short_kernel(BalanceArgs a) {
   }
 }
 
-// Long sequences: one block for each chunk of kBalanceChunk tokens, 64 of them for each of its
+// Long sequences: one block for each chunk of tokens, a share of at most 64 of them for each of its
 // waves.  A sequence of one chunk is finished here, others leave their sums to the next launch.
-template <int G, int V, int NI>
+template <int G>
 __global__ __launch_bounds__(kBalanceThreads) void balance_chunk_kernel(BalanceArgs a) {
-  using R = Row<G, V, NI>;
+  using R = Row<G>;
   constexpr int NW = kBalanceThreads / kWave;
   __shared__ float part[NW][kMaxExperts];
   __shared__ int hist[kMaxExperts];
@@ -175,11 +242,11 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_chunk_kernel(BalanceA
   for (int e = tid; e < a.E; e += kBalanceThreads) hist[e] = 0;
   __syncthreads();
   const int64_t s0 = (int64_t)s * a.seq_len, s1 = min<int64_t>(a.T, s0 + a.seq_len);
-  const int64_t t0 = min(s1, s0 + (int64_t)c * kBalanceChunk + wave * (kBalanceChunk / NW));
-  const int64_t t1 = min(s1, t0 + kBalanceChunk / NW);
+  const int64_t t0 = min(s1, s0 + (int64_t)c * a.chunk + wave * (a.chunk / NW));
+  const int64_t t1 = min(s1, t0 + a.chunk / NW);
   float acc[R::N], zsum;
   int n;
-  wave_sums<G, V, NI>(a, t0, t1, lane, acc, zsum, n, hist);
+  wave_sums<G>(a, t0, t1, lane, acc, zsum, n, hist);
   if (lane < G) {
 #pragma unroll
     for (int i = 0; i < R::N; ++i)
@@ -293,66 +360,83 @@ __global__ __launch_bounds__(kBalanceJoin) void balance_mean_kernel(BalanceArgs 
 }
 
 // Sequences of several chunks: block (s, b) joins the chunks' sums of 32 experts of sequence s,
-// 32 chunks side by side; the last block to end takes the means.  Which block that is has no
-// effect on the result.
+// 32 chunks side by side.  A single block ends with the losses; of several the last one to end takes
+// the means, and which one that is has no effect on the result.
 __global__ __launch_bounds__(kBalanceJoin) void balance_join_kernel(BalanceArgs a) {
-  constexpr int NR = kBalanceJoin / 32;
-  __shared__ __align__(16) float pp[NR][33];
-  __shared__ int cc[NR][33];
-  __shared__ int last;
-  const int tid = threadIdx.x, col = tid & 31, row = tid >> 5;
+  constexpr int NW = kBalanceJoin / kWave, NR = kBalanceJoin / 32;
+  __shared__ __align__(16) float pp[NW][32];
+  __shared__ int cc[NW][32];
+  __shared__ float zz;
+  __shared__ int nn, last;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, col = tid & 31, row = tid >> 5;
   const int s = blockIdx.x / a.eb, b = blockIdx.x - s * a.eb;
   const int e = b * 32 + col;
   float p = 0.f;
   int c = 0;
   if (e < a.E) {
     const int64_t base = (int64_t)s * a.cps * a.E + e;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = row; i < a.cps; i += NR) {
       p += a.part_p[base + (int64_t)i * a.E];
       c += a.part_c[base + (int64_t)i * a.E];
     }
   }
-  pp[row][col] = p;
-  cc[row][col] = c;
-  float z = 0.f;
-  int n = 0;
-  if (b == 0 && tid < kWave) {
-    for (int i = tid; i < a.cps; i += kWave) {
+  if (b == 0 && wave == NW - 1) {
+    float z = 0.f;
+    int n = 0;
+#pragma unroll 4
+    for (int i = lane; i < a.cps; i += kWave) {
       z += a.part_z[(int64_t)s * a.cps + i];
       n += a.part_n[(int64_t)s * a.cps + i];
     }
     z = wave_sum(z);
 #pragma unroll
     for (int o = kWave / 2; o >= 1; o >>= 1) n += __shfl_xor(n, o, kWave);
+    if (lane == 0) {
+      zz = z;
+      nn = n;
+    }
+  }
+  p += __shfl_xor(p, 32, kWave);
+  c += __shfl_xor(c, 32, kWave);
+  if (lane < 32) {
+    pp[wave][lane] = p;
+    cc[wave][lane] = c;
   }
   __syncthreads();
-  if (tid < kWave) {
-    float dot = 0.f;
-    if (tid < 32) {
-      p = 0.f;
-      c = 0;
-      for (int r = 0; r < NR; ++r) {
-        p += pp[r][tid];
-        c += cc[r][tid];
-      }
-      if (e < a.E) {
-        a.probs[(int64_t)s * a.E + e] = p;
-        a.counts[(int64_t)s * a.E + e] = c;
-      }
-      dot = (float)c * p;
+  if (wave == 0) {
+    p = 0.f;
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < NW / 2; ++w) {
+      p += pp[w + (lane >> 5) * (NW / 2)][col];
+      c += cc[w + (lane >> 5) * (NW / 2)][col];
     }
-    dot = wave_sum(dot);
-    if (tid == 0) {
-      // read by the last block, on any XCD: agent-coherent stores, then the count
-      __hip_atomic_store(a.seq_loss + (int64_t)s * a.eb + b, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (b == 0) {
-        __hip_atomic_store(a.seq_z + s, z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(a.tokens + s, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    p += __shfl_xor(p, 32, kWave);
+    c += __shfl_xor(c, 32, kWave);
+    if (lane < 32 && e < a.E) {
+      a.probs[(int64_t)s * a.E + e] = p;
+      a.counts[(int64_t)s * a.E + e] = c;
+    }
+    const float dot = wave_sum(lane < 32 ? (float)c * p : 0.f);
+    if (lane == 0) {
+      if (gridDim.x == 1) {
+        a.tokens[0] = a.tokens[1] = nn;
+        a.tokens[2] = nn > 0;
+        a.loss[0] = sequence_loss(a, nn, dot);
+        a.loss[1] = nn ? zz / (float)nn : 0.f;
+        last = 0;
+      } else {
+        // read by the last block, on any XCD: agent-coherent stores, then the count
+        __hip_atomic_store(a.seq_loss + (int64_t)s * a.eb + b, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (b == 0) {
+          __hip_atomic_store(a.seq_z + s, zz, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(a.tokens + s, nn, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __builtin_amdgcn_s_waitcnt(0);
+        const int before = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        last = before == (int)gridDim.x - 1;
       }
-      __builtin_amdgcn_s_waitcnt(0);
-      const int before = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = before == (int)gridDim.x - 1;
     }
   }
   __syncthreads();
@@ -363,117 +447,114 @@ __global__ __launch_bounds__(kBalanceJoin) void balance_join_kernel(BalanceArgs 
 
 // ------------------------------------------------------------------ gradient
 
-template <int G, int V, int NI, bool kRoute>
+template <int G, bool kRoute>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
-  using R = Row<G, V, NI>;
+  using R = Row<G>;
+  constexpr int U = kBwdRows;                      // rows of a lane group in flight
+  constexpr int kPicks = 8;                        // of a row, loaded ahead (the same address in its lanes)
   const int lane = threadIdx.x & (kWave - 1);
   const int gl = lane & (G - 1), sub = lane / G;
-  const int64_t step = (int64_t)gridDim.x * 4 * R::kRows;
-  const float total = (float)a.tokens[a.S], some = (float)a.tokens[a.S + 1];
-  const float g0 = a.dloss[0] * ((float)a.E / (float)a.K) / some;
-  const float g1 = 2.f * a.dloss[1] / total;
+  const int64_t step = (int64_t)gridDim.x * 4 * R::kRows * U;
   // the loop's bound is of the wave's first row: all lanes take part in the exchanges
-  for (int64_t tw = ((int64_t)blockIdx.x * 4 + threadIdx.x / kWave) * R::kRows; tw < a.T; tw += step) {
-    const int64_t t = tw + sub;
-    const bool in = t < a.T;
-    const bool used = in && (!a.mask || a.mask[t] != 0);
-    const int64_t s = in ? t / a.seq_len : 0;
-    R r;
-    r.load(a.logits + t * a.E, a.E, gl, in);
-    const float lse = r.softmax();
-    const float n = (float)a.tokens[s];
-    const float f = g0 / (n * n);
-    float q[R::N], dot = 0.f;
+  for (int64_t tw = ((int64_t)blockIdx.x * 4 + threadIdx.x / kWave) * R::kRows * U; tw < a.T; tw += step) {
+    R r[U], q[U];
+    bool in[U], used[U];
+    float n[U], pw[U][kPicks], pd[U][kPicks];
+    int pe[U][kPicks];
 #pragma unroll
-    for (int i = 0; i < R::N; ++i) q[i] = 0.f;
-    const int32_t* crow = a.counts + s * a.E;
-    if constexpr (V == 4) {
-      if (gl * 4 < a.E) {
-        const int4 c = *reinterpret_cast<const int4*>(crow + gl * 4);
-        q[0] = f * (float)c.x; q[1] = f * (float)c.y; q[2] = f * (float)c.z; q[3] = f * (float)c.w;
-      }
-    } else {
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = tw + u * R::kRows + sub;
+      in[u] = t < a.T;
+      r[u].load(a.logits + t * a.E, a.E, gl, in[u]);
+      used[u] = in[u] && (!a.mask || a.mask[t] != 0);
+      if constexpr (kRoute) {                       // the first picks; more below
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (R::expert(gl, i) < a.E) q[i] = f * (float)crow[R::expert(gl, i)];
-    }
+        for (int h = 0; h < kPicks; h += 4) {       // the same address in a row's lanes; uniform in K
+          const int64_t at = t * a.K;
+          const bool on = in[u] && h < a.K;
+          Elem<float>::unpack(load_row4(a.topk_w + at, h, a.K, on, 0u), pw[u] + h);
+          Elem<float>::unpack(load_row4(a.dtopk_w + at, h, a.K, on, 0u), pd[u] + h);
+          const u32x4 e = load_row4(a.topk_idx + at, h, a.K, on, 0xFFFFFFFFu);
 #pragma unroll
-    for (int i = 0; i < R::N; ++i) dot = fmaf(r.v[i], q[i], dot);
-    dot = group_sum<G>(dot);
-    const float add = g1 * lse - dot;
-    float out[R::N];
-#pragma unroll
-    for (int i = 0; i < R::N; ++i) out[i] = used ? r.v[i] * (q[i] + add) : 0.f;
-    if constexpr (kRoute) {   // w_k (dw_k - sum_j w_j dw_j) for the picked experts
-      float inner = 0.f;
-      for (int k0 = 0; k0 < a.K; k0 += G) {
-        const int k = k0 + gl;
-        if (in && k < a.K) inner = fmaf(a.topk_w[t * a.K + k], a.dtopk_w[t * a.K + k], inner);
-      }
-      inner = group_sum<G>(inner);
-      for (int k0 = 0; k0 < a.K; k0 += G) {
-        const int k = k0 + gl;
-        int e = -1;
-        float v = 0.f;
-        if (in && k < a.K) {
-          e = a.topk_idx[t * a.K + k];
-          v = a.topk_w[t * a.K + k] * (a.dtopk_w[t * a.K + k] - inner);
-        }
-        const int m = min(G, a.K - k0);
-        for (int j = 0; j < m; ++j) {
-          const int ej = __shfl(e, (lane & ~(G - 1)) + j, kWave);
-          const float vj = __shfl(v, (lane & ~(G - 1)) + j, kWave);
-#pragma unroll
-          for (int i = 0; i < R::N; ++i) out[i] += R::expert(gl, i) == ej ? vj : 0.f;
+          for (int i = 0; i < 4; ++i) pe[u][h + i] = (int)e[i];
         }
       }
-    }
-    if (in) {
-      float* dst = a.dlogits + t * a.E;
-      if constexpr (V == 4) {
-        if (gl * 4 < a.E) st16(dst + gl * 4, Elem<float>::pack(out));
-      } else {
+      const int64_t s = in[u] ? a.seq.of((uint32_t)t) : 0;
+      n[u] = (float)a.tokens[s];
+      const u32x4 c = load_row4(a.counts + s * a.E, gl * 4, a.E, true, 0u);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if (R::expert(gl, i) < a.E) dst[R::expert(gl, i)] = out[i];
+      for (int i = 0; i < 4; ++i) q[u].v[i] = (float)(int)c[i];
+    }
+    const float g0 = a.dloss[0] * ((float)a.E / (float)a.K) / (float)a.tokens[a.S + 1];
+    const float g1 = 2.f * a.dloss[1] / (float)a.tokens[a.S];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = tw + u * R::kRows + sub;
+      const float lse = r[u].softmax();
+      const float f = g0 / (n[u] * n[u]);
+      float dot = 0.f, out[R::N];
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) {
+        q[u].v[i] *= f;
+        dot = fmaf(r[u].v[i], q[u].v[i], dot);
+      }
+      dot = group_sum<G>(dot);
+      const float add = g1 * lse - dot;
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) out[i] = used[u] ? r[u].v[i] * (q[u].v[i] + add) : 0.f;
+      if constexpr (kRoute) {   // w_k (dw_k - sum_j w_j dw_j) for the picked experts
+        float inner = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPicks; ++k) inner = fmaf(pw[u][k], pd[u][k], inner);
+        const int64_t at = t * a.K;
+        if (in[u])
+          for (int k = kPicks; k < a.K; ++k) inner = fmaf(a.topk_w[at + k], a.dtopk_w[at + k], inner);
+        auto add_pick = [&](int e, float v) {
+#pragma unroll
+          for (int i = 0; i < R::N; ++i) out[i] += R::expert(gl, i) == e ? v : 0.f;
+        };
+#pragma unroll
+        for (int k = 0; k < kPicks; ++k) add_pick(pe[u][k], pw[u][k] * (pd[u][k] - inner));
+        if (in[u])
+          for (int k = kPicks; k < a.K; ++k) add_pick(a.topk_idx[at + k], a.topk_w[at + k] * (a.dtopk_w[at + k] - inner));
+      }
+      if (in[u]) {
+        float* dst = a.dlogits + t * a.E + gl * 4;
+        if (gl * 4 + 4 <= a.E) {
+          st16_loose(dst, Elem<float>::pack(out));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            if (gl * 4 + i < a.E) dst[i] = out[i];
+        }
       }
     }
   }
 }
 
-// Lanes of a row: the power of two that holds E / 4 (16-byte loads) or E experts.
+// Lanes of a row: the power of two that holds E / 4.
 template <class F>
 hipError_t with_row(int E, F&& f) {
-#define MOE_ROW(G, V, NI) return f(std::integral_constant<int, G>{}, std::integral_constant<int, V>{}, std::integral_constant<int, NI>{})
-  if (E % 4 == 0) {
-    const int q = E / 4;
-    if (q <= 1) MOE_ROW(1, 4, 1);
-    if (q <= 2) MOE_ROW(2, 4, 1);
-    if (q <= 4) MOE_ROW(4, 4, 1);
-    if (q <= 8) MOE_ROW(8, 4, 1);
-    if (q <= 16) MOE_ROW(16, 4, 1);
-    if (q <= 32) MOE_ROW(32, 4, 1);
-    MOE_ROW(64, 4, 1);
-  }
-  if (E <= 4) MOE_ROW(4, 1, 1);
-  if (E <= 16) MOE_ROW(16, 1, 1);
-  if (E <= 64) MOE_ROW(64, 1, 1);
-  if (E <= 128) MOE_ROW(64, 1, 2);
-  MOE_ROW(64, 1, 4);
-#undef MOE_ROW
+  if (E <= 4) return f(std::integral_constant<int, 1>{});
+  if (E <= 8) return f(std::integral_constant<int, 2>{});
+  if (E <= 16) return f(std::integral_constant<int, 4>{});
+  if (E <= 32) return f(std::integral_constant<int, 8>{});
+  if (E <= 64) return f(std::integral_constant<int, 16>{});
+  if (E <= 128) return f(std::integral_constant<int, 32>{});
+  return f(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
-  return with_row(a.E, [&](auto g, auto v, auto ni) {
-    constexpr int G = decltype(g)::value, V = decltype(v)::value, NI = decltype(ni)::value;
+  return with_row(a.E, [&](auto g) {
+    constexpr int G = decltype(g)::value;
     if (a.seq_len <= kBalanceShort) {
       const int blocks = a.S / 4 + (a.S % 4 != 0);
-      balance_short_kernel<G, V, NI><<<blocks < 65536 ? blocks : 65536, 256, 0, st>>>(a);
+      balance_short_kernel<G><<<blocks < 65536 ? blocks : 65536, 256, 0, st>>>(a);
       balance_mean_kernel<<<1, kBalanceJoin, 0, st>>>(a);
     } else {
-      balance_chunk_kernel<G, V, NI><<<a.S * a.cps, kBalanceThreads, 0, st>>>(a);
+      balance_chunk_kernel<G><<<a.S * a.cps, kBalanceThreads, 0, st>>>(a);
       if (a.cps == 1)
         balance_mean_kernel<<<1, kBalanceJoin, 0, st>>>(a);
       else
@@ -484,15 +565,15 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_balance_bwd(const BalanceBwdArgs& a, hipStream_t st) {
-  return with_row(a.E, [&](auto g, auto v, auto ni) {
-    constexpr int G = decltype(g)::value, V = decltype(v)::value, NI = decltype(ni)::value;
-    const int64_t rows = 4 * (kWave / G);
+  return with_row(a.E, [&](auto g) {
+    constexpr int G = decltype(g)::value;
+    const int64_t rows = 4 * (kWave / G) * kBwdRows;
     const int64_t blocks = (a.T + rows - 1) / rows;
     const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192);
     if (a.topk_idx)
-      balance_bwd_kernel<G, V, NI, true><<<grid, 256, 0, st>>>(a);
+      balance_bwd_kernel<G, true><<<grid, 256, 0, st>>>(a);
     else
-      balance_bwd_kernel<G, V, NI, false><<<grid, 256, 0, st>>>(a);
+      balance_bwd_kernel<G, false><<<grid, 256, 0, st>>>(a);
     return hipGetLastError();
   });
 }

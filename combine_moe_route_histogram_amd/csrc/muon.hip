@@ -374,13 +374,12 @@ void newton_kernel(Product p) {
 // 128-byte row pieces, as fragments read from memory touch 32 rows at 32 bytes each and take twice
 // the time.  Both operands lie along k (X is kept with its transpose); the waves' sums meet in LDS in a fixed
 // order.
-template <int KIND, bool EXACT, int T>
+template <int KIND, bool EXACT, int T, int D>   // D: slices of a wave in LDS
 __global__ __launch_bounds__(256) void newton_small_kernel(Product p) {
   constexpr bool kSym = KIND == kGram || KIND == kPoly, kLast = KIND == kOut || KIND == kUpdate;
   constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kAdd || (KIND == kPoly && EXACT);
   constexpr int B = T / 32;                       // 32-wide blocks of a side
   constexpr int P = EXACT ? 2 : 1;                // parts of a factor
-  constexpr int D = T == 32 ? 2 : 1;              // slices of a wave in LDS
   constexpr int kPlane = T * 64 * 2, kSlice = 2 * P * kPlane, kPart = 4 * T * (T + 1) * 4;
   // separate LDS objects, so that the copies into one do not hold up reads of the other
   __shared__ __align__(16) uint8_t ring0[4 * kSlice > kPart ? 4 * kSlice : kPart];
@@ -681,14 +680,14 @@ hipError_t product_with(Product p, int batch, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int KIND, bool EXACT, int T>
+template <int KIND, bool EXACT, int T, int D>
 hipError_t product_small(Product p, int batch, hipStream_t st) {
   p.mt = p.m_len / T;
   p.nt = p.n_len / T;
   p.per = KIND == kGram || KIND == kPoly ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
   p.tiles = p.per * batch;
   const unsigned grid = (unsigned)kXcds * ((p.tiles + kXcds - 1) / kXcds);
-  newton_small_kernel<KIND, EXACT, T><<<grid, 256, 0, st>>>(p);
+  newton_small_kernel<KIND, EXACT, T, D><<<grid, 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -702,9 +701,15 @@ hipError_t product(const Product& p, bool small, int batch, hipStream_t st) {
     return batch * (kMn ? mt * nt : mt * (mt + 1) / 2);
   };
   // 32 x 32 tiles until there are two for each CU: whole calls of [512, 512] 95 us with them and 148
-  // with 64 x 64 ones (f32), of [1024, 1024] 296 and 223
-  if (small)
-    return tiles(32) <= 512 ? product_small<KIND, EXACT, 32>(p, batch, st) : product_small<KIND, EXACT, 64>(p, batch, st);
+  // with 64 x 64 ones (f32), of [1024, 1024] 296 and 223.  Two slices of two parts take a CU's LDS, so they
+  // are for one tile on a CU: 5 [264, 416] 128 us with two, 110 with one; [64, 14336] 246 and 293.
+  if (small) {
+    if (tiles(32) > 512) return product_small<KIND, EXACT, 64, 1>(p, batch, st);
+    if constexpr (EXACT) {
+      if (tiles(32) > 256) return product_small<KIND, EXACT, 32, 1>(p, batch, st);
+    }
+    return product_small<KIND, EXACT, 32, 2>(p, batch, st);
+  }
   return tiles(256) >= 256 ? product_with<KIND, EXACT, Big>(p, batch, st) : product_with<KIND, EXACT, Mid>(p, batch, st);
 }
 template <int KIND>

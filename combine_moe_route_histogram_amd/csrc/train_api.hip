@@ -30,13 +30,21 @@ int sequences(const moe_dims* d, int seq_len) { return d->T / seq_len + (d->T % 
 
 // Workspace sections (byte offsets).
 struct BalanceLayout {
-  int S, cps, eb;
+  int S, chunk, cps, eb;
   size_t part_p, part_c, part_z, part_n, seq_loss, seq_z, ticket, total;
 };
 BalanceLayout balance_layout(const moe_dims* d, int seq_len) {
   BalanceLayout L;
   L.S = sequences(d, seq_len);
-  L.cps = seq_len <= kBalanceShort ? 1 : (seq_len + kBalanceChunk - 1) / kBalanceChunk;
+  // chunks of 64 tokens for each wave where that makes two blocks for each CU, else smaller ones (a
+  // wave's tokens are one chain): 131072 tokens, 256 experts 50 us with 256 chunks, 40 with 512, 51 with 2048,
+  // as the joining launch has more to read
+  L.chunk = kBalanceChunk;
+  L.cps = 1;
+  if (seq_len > kBalanceShort) {
+    while (L.chunk > 64 && (int64_t)L.S * ((seq_len + L.chunk - 1) / L.chunk) < 512) L.chunk /= 2;
+    L.cps = (seq_len + L.chunk - 1) / L.chunk;
+  }
   L.eb = (d->E + 31) / 32;
   const size_t chunks = L.cps > 1 ? (size_t)L.S * L.cps : 0;
   size_t off = 0;
@@ -117,7 +125,8 @@ int moe_balance(const moe_dims* d, int seq_len, const float* logits, const int32
   const BalanceLayout L = balance_layout(d, seq_len);
   MOE_TRY(check_ws_bytes(ws, ws_bytes, L.total));
   BalanceArgs a{};
-  a.T = d->T; a.E = d->E; a.K = d->K; a.seq_len = seq_len; a.S = L.S; a.cps = L.cps; a.eb = L.eb;
+  a.T = d->T; a.E = d->E; a.K = d->K; a.seq_len = seq_len; a.S = L.S; a.chunk = L.chunk;
+  a.cps = L.cps; a.eb = L.eb;
   a.logits = logits; a.topk_idx = topk_idx; a.mask = mask;
   a.counts = counts; a.tokens = tokens; a.probs = probs; a.loss = loss;
   a.part_p = ws_at<float>(ws, L.part_p);
@@ -146,7 +155,8 @@ int moe_balance_bwd(const moe_dims* d, int seq_len, const float* logits, const u
   }
   MOE_TRY(check_ptr(dlogits, "dlogits"));
   BalanceBwdArgs a{};
-  a.T = d->T; a.E = d->E; a.K = d->K; a.seq_len = seq_len; a.S = sequences(d, seq_len);
+  a.T = d->T; a.E = d->E; a.K = d->K; a.S = sequences(d, seq_len);
+  a.seq = DivBy((uint32_t)seq_len);
   a.logits = logits; a.mask = mask; a.counts = counts; a.tokens = tokens; a.dloss = dloss;
   a.dtopk_w = dtopk_w; a.topk_w = topk_w; a.topk_idx = topk_idx; a.dlogits = dlogits;
   return hip_status(launch_balance_bwd(a, as_stream(stream)), "moe_balance_bwd");
