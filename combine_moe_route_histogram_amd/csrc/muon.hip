@@ -67,7 +67,7 @@ struct NsCfg {
   static_assert(NJ % 2 == 0, "the epilogue takes two 32-column blocks at a time");
 };
 
-// v as two fp16 parts
+// Four or eight values as two fp16 parts.
 __device__ __forceinline__ void split16(const float* v, u32x2& hi, u32x2& lo) {
   f16x4 h, l;
 #pragma unroll
@@ -87,6 +87,24 @@ __device__ __forceinline__ void join16(const u32x2& hi, const u32x2* lo, float* 
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += (float)l[e];
   }
+}
+
+__device__ __forceinline__ void split16(const float* v, u32x4& hi, u32x4& lo) {
+  u32x2 h0, h1, l0, l1;
+  split16(v, h0, l0);
+  split16(v + 4, h1, l1);
+  hi = u32x4{h0[0], h0[1], h1[0], h1[1]};
+  lo = u32x4{l0[0], l0[1], l1[0], l1[1]};
+}
+__device__ __forceinline__ void join16(const u32x4& hi, const u32x4* lo, float* v) {
+  const u32x2 h0 = {hi[0], hi[1]}, h1 = {hi[2], hi[3]};
+  u32x2 l0, l1;
+  if (lo) {
+    l0 = u32x2{(*lo)[0], (*lo)[1]};
+    l1 = u32x2{(*lo)[2], (*lo)[3]};
+  }
+  join16(h0, lo ? &l0 : nullptr, v);
+  join16(h1, lo ? &l1 : nullptr, v + 4);
 }
 
 // Four results of row `row` from column `col` on, of matrix g of the user's tensors.
@@ -137,9 +155,26 @@ __device__ __forceinline__ void finish4(const Product& p, int m, int n, const fl
   }
 }
 
-// Accumulators to results: 32 x 64 blocks through the wave's LDS region, as in the layer's tiles.
-// What is added is loaded one block ahead (unconditional loads, clamped into the matrix: a branch
-// for each would make the waits conservative).
+// The transpose of a 32 x 64 block of fp16 that lies in LDS (rows of kTurnPitch bytes), to 64 rows of 32
+// at dst.  The LDS transpose read hands a lane 4 consecutive rows of one column; with row groups 8 g and 8 g + 4
+// for the lanes of group g, 4 lanes store 64 bytes of a row.
+constexpr int kTurnPitch = 144;
+__device__ __forceinline__ void store_turned(const uint8_t* block, uint16_t* dst, int64_t ld, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const uint8_t* const at = block + (8 * g + (i >> 2)) * kTurnPitch + 8 * (i & 3);
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb) {
+    const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(at + 32 * cb));
+    const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(at + 4 * kTurnPitch + 32 * cb));
+    const i16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    *reinterpret_cast<u32x4*>(dst + (int64_t)(16 * cb + i) * ld + 8 * g) = __builtin_bit_cast(u32x4, v);
+  }
+}
+
+// Accumulators to results: 32 x 64 blocks through the wave's LDS region, 8 columns of a row for each
+// lane.  What is added is loaded one block ahead (unconditional loads, clamped into the matrix: a branch
+// for each would make the waits conservative).  All LDS accesses are of words: a block of fp16 is
+// written over floats that were read before it.
 template <int KIND, bool EXACT, class C>
 __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int m0, int n0, bool mirror,
                                                 const f32x16 (&acc)[C::MI][C::NJ],
@@ -152,20 +187,22 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
   constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kAdd || (KIND == kPoly && EXACT);
   const int rs = wave / kRps;
   uint8_t* const rbase = rs == 0 ? stages[0] : rs == 1 ? stages[1] : rs == 2 ? stages[2] : stages[3];
-  float* reg = reinterpret_cast<float*>(rbase + (wave - rs * kRps) * kEpiRegionBytes);
+  uint8_t* const region = rbase + (wave - rs * kRps) * kEpiRegionBytes;
+  uint32_t* const reg = reinterpret_cast<uint32_t*>(region);
   float lr = 0.f;
   if constexpr (KIND == kUpdate) lr = p.lr_dev ? *p.lr_dev : p.lr;
   const int64_t obase = g * p.o_mat;
   const bool turn = kSym ? mirror : kLast && p.tall;
-  u32x2 aux_h[2][kAux ? 8 : 1], aux_l[2][kAuxLow ? 8 : 1];
+  const int q0 = lane >> 3, c8 = 8 * (lane & 7);
+  u32x4 aux_h[2][kAux ? 4 : 1], aux_l[2][kAuxLow ? 4 : 1];
   auto load_aux = [&](int blk, int buf) {
     const int mb = m0 + wm * C::WM + 32 * (blk / (C::NJ / 2)), nb = n0 + wn * C::WN + 64 * (blk % (C::NJ / 2));
 #pragma unroll
-    for (int pass = 0; pass < 8; ++pass) {
-      const int m = min(mb, p.m_len - 32) + pass * 4 + (lane >> 4), n = min(nb, p.n_len - 64) + 4 * (lane & 15);
+    for (int pass = 0; pass < 4; ++pass) {
+      const int m = min(mb, p.m_len - 32) + pass * 8 + q0, n = min(nb, p.n_len - 64) + c8;
       const int64_t at = obase + (int64_t)m * p.ldo + n;
-      aux_h[buf][pass] = *reinterpret_cast<const u32x2*>(p.ch + at);
-      if constexpr (kAuxLow) aux_l[buf][pass] = *reinterpret_cast<const u32x2*>(p.cl + at);
+      aux_h[buf][pass] = ld16(p.ch + at);
+      if constexpr (kAuxLow) aux_l[buf][pass] = ld16(p.cl + at);
     }
   };
   if constexpr (kAux) load_aux(0, 0);
@@ -182,46 +219,64 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        reg[row * kEpiPitch + (lane & 31)] = acc[i][2 * hc][r];
-        reg[row * kEpiPitch + 32 + (lane & 31)] = acc[i][2 * hc + 1][r];
+        reg[row * kEpiPitch + (lane & 31)] = __float_as_uint(acc[i][2 * hc][r]);
+        reg[row * kEpiPitch + 32 + (lane & 31)] = __float_as_uint(acc[i][2 * hc + 1][r]);
       }
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the wave's own region is written
+      // a block of bf16 results inside the matrix, rows of whole 16 bytes
+      const bool turn16 = KIND == kOut && p.bf16 && p.C % 8 == 0 && mb + 32 <= p.C && nb + 64 <= p.R;
+      u32x4 low[kSym && EXACT ? 4 : 1];
 #pragma unroll
-      for (int pass = 0; pass < 8; ++pass) {
-        const int q = pass * 4 + (lane >> 4), c4 = 4 * (lane & 15);
-        const f32x4 s = *reinterpret_cast<const f32x4*>(reg + q * kEpiPitch + c4);
-        const int m = mb + q, n = nb + c4;
-        float v[4], x[4];
+      for (int pass = 0; pass < 4; ++pass) {
+        const int q = pass * 8 + q0, m = mb + q, n = nb + c8;
+        float s[8], v[8], x[8];
+        Elem<float>::unpack(*reinterpret_cast<const u32x4*>(reg + q * kEpiPitch + c8), s);
+        Elem<float>::unpack(*reinterpret_cast<const u32x4*>(reg + q * kEpiPitch + c8 + 4), s + 4);
         if constexpr (kAux) join16(aux_h[blk & 1][pass], kAuxLow ? &aux_l[blk & 1][pass] : nullptr, x);
-        const float sum[4] = {s[0], s[1], s[2], s[3]};
-        finish4<KIND>(p, m, n, sum, x, v);
+        finish4<KIND>(p, m, n, s, x, v);
+        finish4<KIND>(p, m, n + 4, s + 4, x + 4, v + 4);
         if constexpr (!kLast) {
           const int64_t at = obase + (int64_t)m * p.ldo + n;
-          u32x2 hi, lo;
+          u32x4 hi, lo;
           split16(v, hi, lo);
-          *reinterpret_cast<u32x2*>(p.oh + at) = hi;
-          if (EXACT || (!kSym && p.ol)) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
+          st16(p.oh + at, hi);
+          if (EXACT || (!kSym && p.ol)) st16(p.ol + at, lo);
+          if constexpr (kSym) {
+            if (turn) *reinterpret_cast<u32x4*>(region + q * kTurnPitch + 2 * c8) = hi;
+            if constexpr (EXACT) low[pass] = lo;
+          }
         } else if (!turn) {
           emit4<KIND>(p, p.g0 + g, m, n, v, lr);
+          emit4<KIND>(p, p.g0 + g, m, n + 4, v + 4, lr);
+        } else if (KIND == kOut && turn16) {
+          *reinterpret_cast<u32x4*>(region + q * kTurnPitch + 2 * c8) = Elem<uint16_t>::pack(v);
+        } else {
+          *reinterpret_cast<u32x4*>(reg + q * kEpiPitch + c8) = Elem<float>::pack(v);
+          *reinterpret_cast<u32x4*>(reg + q * kEpiPitch + c8 + 4) = Elem<float>::pack(v + 4);
         }
-        if ((kSym || kLast) && turn)
-          *reinterpret_cast<f32x4*>(reg + q * kEpiPitch + c4) = f32x4{v[0], v[1], v[2], v[3]};
       }
       if ((kSym || kLast) && turn) {   // the block's transpose: 64 rows of 32
         __builtin_amdgcn_s_waitcnt(0xC07F);
+        if constexpr (kSym) {
+          const int64_t at = obase + (int64_t)nb * p.ldo + mb;
+          store_turned(region, p.oh + at, p.ldo, lane);
+          if constexpr (EXACT) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);
 #pragma unroll
-        for (int pass = 0; pass < 8; ++pass) {
-          const int n = pass * 8 + (lane >> 3), m4 = 4 * (lane & 7);
-          float v[4];
+            for (int pass = 0; pass < 4; ++pass)
+              *reinterpret_cast<u32x4*>(region + (pass * 8 + q0) * kTurnPitch + 2 * c8) = low[pass];
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            store_turned(region, p.ol + at, p.ldo, lane);
+          }
+        } else if (KIND == kOut && turn16) {
+          store_turned(region, static_cast<uint16_t*>(p.out) + ((p.g0 + g) * p.R + nb) * p.C + mb, p.C, lane);
+        } else if constexpr (kLast) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = reg[(m4 + e) * kEpiPitch + n];
-          if constexpr (kSym) {
-            const int64_t at = obase + (int64_t)(nb + n) * p.ldo + mb + m4;
-            u32x2 hi, lo;
-            split16(v, hi, lo);
-            *reinterpret_cast<u32x2*>(p.oh + at) = hi;
-            if (EXACT) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
-          } else if constexpr (kLast) {
+          for (int pass = 0; pass < 8; ++pass) {
+            const int n = pass * 8 + (lane >> 3), m4 = 4 * (lane & 7);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(reg[(m4 + e) * kEpiPitch + n]);
             emit4<KIND>(p, p.g0 + g, nb + n, mb + m4, v, lr);
           }
         }
@@ -239,6 +294,22 @@ __device__ __forceinline__ void triangle(int r, int& tm, int& tn) {
   tm = r - tn * (tn + 1) / 2;
 }
 
+// Tile of this block.  Consecutive blocks go to different XCDs; each XCD takes a run of tiles, which
+// share operands in its L2.  (The edge tiles of all matrices at the end of the run, to even out its last
+// round, read their operands anew: 64 [2048, 1408] matrices 6.5 -> 6.8 ms.  The last round in half tiles: no
+// change, the clock rises as CUs fall idle.)
+template <bool kSym>
+__device__ __forceinline__ bool tile_of(const Product& p, int64_t& g, int& tm, int& tn) {
+  const int xcd = blockIdx.x % kXcds, first = (int)((int64_t)p.tiles * xcd / kXcds);
+  const int L = first + blockIdx.x / kXcds;
+  if (L >= (int)((int64_t)p.tiles * (xcd + 1) / kXcds)) return false;
+  g = L / p.per;
+  const int r = L - (int)g * p.per;
+  if constexpr (kSym) triangle(r, tm, tn);
+  else band_order(r, p.mt, p.nt, 8, tm, tn);
+  return true;
+}
+
 // One tile of a product; same ring of LDS slices and order of instructions as the layer's tiles
 // (run_tile_bf16), on fp16.
 template <int KIND, bool EXACT, class C>
@@ -249,19 +320,9 @@ void newton_kernel(Product p) {
   constexpr int MI = C::MI, NJ = C::NJ, BK = C::BK, S = C::STAGES, KS = BK / 16;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  // consecutive blocks go to different XCDs; each XCD takes a run of tiles, which share operands in its L2
-  const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
-  const int first = (int)((int64_t)p.tiles * xcd / kXcds);
-  const int L = first + idx;
-  if (L >= (int)((int64_t)p.tiles * (xcd + 1) / kXcds)) return;
-  const int64_t g = L / p.per;
-  const int r = L - (int)g * p.per;
+  int64_t g;
   int tm, tn;
-  if constexpr (kSym) {
-    triangle(r, tm, tn);
-  } else {
-    band_order(r, p.mt, p.nt, 8, tm, tn);
-  }
+  if (!tile_of<kSym>(p, g, tm, tn)) return;
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int m_valid = min(C::BM, p.m_len - m0), n_valid = min(C::BN, p.n_len - n0);
   const int64_t a0 = g * p.a_mat + (int64_t)m0 * p.lda;
@@ -387,19 +448,9 @@ __global__ __launch_bounds__(256) void newton_small_kernel(Product p) {
   float (*const part)[T][T + 1] = reinterpret_cast<float (*)[T][T + 1]>(ring0);   // after the products
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
-  const int first = (int)((int64_t)p.tiles * xcd / kXcds);
-  const int L = first + idx;
-  if (L >= (int)((int64_t)p.tiles * (xcd + 1) / kXcds)) return;
-  const int64_t g = L / p.per;
-  const int r = L - (int)g * p.per;
+  int64_t g;
   int tm, tn;
-  if constexpr (kSym) {
-    triangle(r, tm, tn);
-  } else {
-    tm = r % p.mt;
-    tn = r / p.mt;
-  }
+  if (!tile_of<kSym>(p, g, tm, tn)) return;
   const int m0 = tm * T, n0 = tn * T;
 
   f32x16 acc[B][B];
@@ -669,14 +720,15 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Source s, Start d) {
 
 inline int up(int v, int to) { return (v + to - 1) / to * to; }
 
+unsigned xcd_grid(int tiles) { return (unsigned)kXcds * ((tiles + kXcds - 1) / kXcds); }
+
 template <int KIND, bool EXACT, class C>
 hipError_t product_with(Product p, int batch, hipStream_t st) {
   p.mt = (p.m_len + C::BM - 1) / C::BM;
   p.nt = (p.n_len + C::BN - 1) / C::BN;
   p.per = KIND == kGram || KIND == kPoly ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
   p.tiles = p.per * batch;
-  const unsigned grid = (unsigned)kXcds * ((p.tiles + kXcds - 1) / kXcds);
-  newton_kernel<KIND, EXACT, C><<<grid, C::NT, 0, st>>>(p);
+  newton_kernel<KIND, EXACT, C><<<xcd_grid(p.tiles), C::NT, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -686,8 +738,7 @@ hipError_t product_small(Product p, int batch, hipStream_t st) {
   p.nt = p.n_len / T;
   p.per = KIND == kGram || KIND == kPoly ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
   p.tiles = p.per * batch;
-  const unsigned grid = (unsigned)kXcds * ((p.tiles + kXcds - 1) / kXcds);
-  newton_small_kernel<KIND, EXACT, T, D><<<grid, 256, 0, st>>>(p);
+  newton_small_kernel<KIND, EXACT, T, D><<<xcd_grid(p.tiles), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
