@@ -110,7 +110,7 @@ struct Row {
   }
 };
 
-// Tokens [t0, t1) of one sequence by one wave (at most 64): sums of p (acc, in the lanes of the first
+// Tokens [t0, t1) of one sequence by one wave: sums of p (acc, in the lanes of the first
 // group after the exchange), of lse^2 and the number of tokens (every lane); picks counted into hist
 // (LDS, cleared by the caller).  A wave has few rows and each pass over them would wait for memory, so
 // several are loaded ahead.
@@ -188,13 +188,99 @@ __device__ __forceinline__ float sequence_loss(const BalanceArgs& a, int n, floa
   return n > 0 ? (float)a.E / (float)a.K * (dot / ((float)n * (float)n)) : 0.f;
 }
 
-// Short sequences: one wave for each, all of its results.
+// A block's sums over its sequences, from those of its four waves.
+__device__ __forceinline__ void block_sums(const BalanceArgs& a, float loss, float z, int n, int some, int lane,
+                                           int wave) {
+  __shared__ float sums[4][2];
+  __shared__ int numbers[4][2];
+  if (lane == 0) {
+    sums[wave][0] = loss;
+    sums[wave][1] = z;
+    numbers[wave][0] = n;
+    numbers[wave][1] = some;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.seq_loss[blockIdx.x] = (sums[0][0] + sums[1][0]) + (sums[2][0] + sums[3][0]);
+    a.seq_z[blockIdx.x] = (sums[0][1] + sums[1][1]) + (sums[2][1] + sums[3][1]);
+    a.seq_n[blockIdx.x] = (numbers[0][0] + numbers[1][0]) + (numbers[2][0] + numbers[3][0]);
+    a.seq_some[blockIdx.x] = (numbers[0][1] + numbers[1][1]) + (numbers[2][1] + numbers[3][1]);
+  }
+}
+
+// Sequences of a few tokens: one lane group for each (131072 sequences of one token, 32 experts: 174 us
+// with a wave for each).
+template <int G>
+__global__ __launch_bounds__(256) void balance_few_kernel(BalanceArgs a) {
+  using R = Row<G>;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int gl = lane & (G - 1), sub = lane / G;
+  float loss_sum = 0.f, z_sum = 0.f;
+  int n_sum = 0, some = 0;
+  // the bounds are of the wave's first sequence and the longest: all lanes take part in the exchanges
+  for (int64_t s0 = ((int64_t)blockIdx.x * 4 + wave) * R::kRows; s0 < a.S; s0 += (int64_t)gridDim.x * 4 * R::kRows) {
+    const int64_t s = s0 + sub;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    int count[4] = {0, 0, 0, 0}, n = 0;
+    for (int j = 0; j < a.seq_len; ++j) {
+      const int64_t t = s * a.seq_len + j;
+      const bool in = s < a.S && t < a.T;
+      const bool used = in && (!a.mask || a.mask[t] != 0);
+      R r;
+      r.load(a.logits + t * a.E, a.E, gl, in);
+      const float lse = r.softmax();
+      if (used) {
+        ++n;
+        if (gl == 0) z_sum += lse * lse;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += r.v[i];
+        for (int k = 0; k < a.K; k += 4) {
+          const u32x4 e = load_row4(a.topk_idx + t * a.K, k, a.K, true, 0xFFFFFFFFu);
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) count[i] += (int)e[h] == R::expert(gl, i);
+        }
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = R::expert(gl, i);
+      if (s < a.S && e < a.E) {
+        a.probs[s * a.E + e] = acc[i];
+        a.counts[s * a.E + e] = count[i];
+        dot = fmaf((float)count[i], acc[i], dot);
+      }
+    }
+    dot = group_sum<G>(dot);
+    if (gl == 0 && s < a.S) {
+      a.tokens[s] = n;
+      loss_sum += sequence_loss(a, n, dot);
+      n_sum += n;
+      some += n > 0;
+    }
+  }
+  loss_sum = wave_sum(loss_sum);
+  z_sum = wave_sum(z_sum);
+#pragma unroll
+  for (int o = kWave / 2; o >= 1; o >>= 1) {
+    n_sum += __shfl_xor(n_sum, o, kWave);
+    some += __shfl_xor(some, o, kWave);
+  }
+  block_sums(a, loss_sum, z_sum, n_sum, some, lane, wave);
+}
+
+// Short sequences: one wave for each, all of its results; the block's sums over its sequences go to the
+// next launch (one sequence a block left that with 131072 sequences of one token: 25 us).
 template <int G>
 __global__ __launch_bounds__(256) void balance_short_kernel(BalanceArgs a) {
   using R = Row<G>;
   __shared__ int hists[4][kMaxExperts];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   int* const hist = hists[wave];   // of this wave alone: LDS keeps a wave's accesses in order
+  float loss_sum = 0.f, z_sum = 0.f;
+  int n_sum = 0, some = 0;
   for (int64_t s = (int64_t)blockIdx.x * 4 + wave; s < a.S; s += (int64_t)gridDim.x * 4) {
     for (int e = lane; e < a.E; e += kWave) hist[e] = 0;
     __builtin_amdgcn_wave_barrier();
@@ -217,13 +303,14 @@ __global__ __launch_bounds__(256) void balance_short_kernel(BalanceArgs a) {
       }
     }
     dot = wave_sum(dot);
-    if (lane == 0) {
-      a.tokens[s] = n;
-      a.seq_loss[s] = sequence_loss(a, n, dot);
-      a.seq_z[s] = zsum;
-    }
+    if (lane == 0) a.tokens[s] = n;
+    loss_sum += sequence_loss(a, n, dot);
+    z_sum += zsum;
+    n_sum += n;
+    some += n > 0;
     __builtin_amdgcn_wave_barrier();
   }
+  block_sums(a, loss_sum, z_sum, n_sum, some, lane, wave);
 }
 
 // Long sequences: one block for each chunk of tokens, a share of at most 64 of them for each of its
@@ -294,17 +381,19 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_chunk_kernel(BalanceA
   }
 }
 
-// Means over the sequences, by one block: losses, the number of tokens and of sequences with any.
-// kShared: the sequences' sums were written by other blocks of this launch.
+// Means over the sequences, by one block: losses, the number of tokens and of sequences with any.  Its
+// entries are the sequences, or the short sequences' blocks.  kShared: the sequences' sums were written by
+// other blocks of this launch.
 template <bool kShared>
 __device__ __forceinline__ void finish(const BalanceArgs& a, float* lds_f, int* lds_i) {
   constexpr int NW = kBalanceJoin / kWave;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   double l = 0.0, z = 0.0;
   int n = 0, some = 0;
-  for (int s = tid; s < a.S; s += kBalanceJoin) {
+#pragma unroll 2
+  for (int s = tid; s < a.entries; s += kBalanceJoin) {
     float ls, zs;
-    int ns;
+    int ns, any;
     if constexpr (kShared) {
       ls = 0.f;
       for (int b = 0; b < a.eb; ++b)
@@ -312,15 +401,17 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, float* lds_f, int* 
       zs = __hip_atomic_load(a.seq_z + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       ns = __hip_atomic_load(a.tokens + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       ls = sequence_loss(a, ns, ls);
+      any = ns > 0;
     } else {
       ls = a.seq_loss[s];
       zs = a.seq_z[s];
-      ns = a.tokens[s];
+      ns = a.seq_n[s];
+      any = a.seq_some ? a.seq_some[s] : ns > 0;
     }
     l += ls;
     z += zs;
     n += ns;
-    some += ns > 0;
+    some += any;
   }
 #pragma unroll
   for (int o = kWave / 2; o >= 1; o >>= 1) {
@@ -532,16 +623,17 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
   }
 }
 
-// Lanes of a row: the power of two that holds E / 4.
 template <class F>
 hipError_t with_row(int E, F&& f) {
-  if (E <= 4) return f(std::integral_constant<int, 1>{});
-  if (E <= 8) return f(std::integral_constant<int, 2>{});
-  if (E <= 16) return f(std::integral_constant<int, 4>{});
-  if (E <= 32) return f(std::integral_constant<int, 8>{});
-  if (E <= 64) return f(std::integral_constant<int, 16>{});
-  if (E <= 128) return f(std::integral_constant<int, 32>{});
-  return f(std::integral_constant<int, 64>{});
+  switch (balance_lanes(E)) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 8: return f(std::integral_constant<int, 8>{});
+    case 16: return f(std::integral_constant<int, 16>{});
+    case 32: return f(std::integral_constant<int, 32>{});
+    default: return f(std::integral_constant<int, 64>{});
+  }
 }
 
 }  // namespace
@@ -549,9 +641,11 @@ hipError_t with_row(int E, F&& f) {
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
   return with_row(a.E, [&](auto g) {
     constexpr int G = decltype(g)::value;
-    if (a.seq_len <= kBalanceShort) {
-      const int blocks = a.S / 4 + (a.S % 4 != 0);
-      balance_short_kernel<G><<<blocks < 65536 ? blocks : 65536, 256, 0, st>>>(a);
+    if (a.by == kByGroup) {
+      balance_few_kernel<G><<<a.entries, 256, 0, st>>>(a);
+      balance_mean_kernel<<<1, kBalanceJoin, 0, st>>>(a);
+    } else if (a.by == kByWave) {
+      balance_short_kernel<G><<<a.entries, 256, 0, st>>>(a);
       balance_mean_kernel<<<1, kBalanceJoin, 0, st>>>(a);
     } else {
       balance_chunk_kernel<G><<<a.S * a.cps, kBalanceThreads, 0, st>>>(a);

@@ -30,30 +30,41 @@ int sequences(const moe_dims* d, int seq_len) { return d->T / seq_len + (d->T % 
 
 // Workspace sections (byte offsets).
 struct BalanceLayout {
-  int S, chunk, cps, eb;
-  size_t part_p, part_c, part_z, part_n, seq_loss, seq_z, ticket, total;
+  int S, by, chunk, cps, eb, entries;
+  size_t part_p, part_c, part_z, part_n, seq_loss, seq_z, seq_n, seq_some, ticket, total;
 };
 BalanceLayout balance_layout(const moe_dims* d, int seq_len) {
   BalanceLayout L;
   L.S = sequences(d, seq_len);
-  // chunks of 64 tokens for each wave where that makes two blocks for each CU, else smaller ones (a
+  // Chunks of up to 64 tokens for each of 8 waves where that makes two blocks for each CU, else smaller ones (a
   // wave's tokens are one chain): 131072 tokens, 256 experts 50 us with 256 chunks, 40 with 512, 51 with 2048,
-  // as the joining launch has more to read
-  L.chunk = kBalanceChunk;
+  // as the joining launch has more to read.
+  L.chunk = seq_len < kBalanceChunk ? (seq_len + 7) / 8 * 8 : kBalanceChunk;
   L.cps = 1;
-  if (seq_len > kBalanceShort) {
-    while (L.chunk > 64 && (int64_t)L.S * ((seq_len + L.chunk - 1) / L.chunk) < 512) L.chunk /= 2;
+  if (L.by == kByChunk) {
+    while (L.chunk > 64 && (int64_t)L.S * ((seq_len + L.chunk - 1) / L.chunk) < 512) L.chunk = (L.chunk / 2 + 7) / 8 * 8;
     L.cps = (seq_len + L.chunk - 1) / L.chunk;
   }
   L.eb = (d->E + 31) / 32;
+  L.entries = L.S;
+  // a lane group or a wave for a sequence, or blocks for chunks of it
+  L.by = seq_len <= kBalanceFew ? kByGroup
+       : seq_len <= kBalanceShort || (seq_len <= kBalanceShortMany && L.S >= kBalanceMany) ? kByWave : kByChunk;
+  if (L.by != kByChunk) {
+    const int per = seq_len <= kBalanceFew ? 4 * (64 / balance_lanes(d->E)) : 4;
+    const int blocks = L.S / per + (L.S % per != 0);
+    L.entries = blocks < kBalanceShortBlocks ? blocks : kBalanceShortBlocks;
+  }
   const size_t chunks = L.cps > 1 ? (size_t)L.S * L.cps : 0;
   size_t off = 0;
   L.part_p = off;   off = align_up(off + chunks * d->E * 4);
   L.part_c = off;   off = align_up(off + chunks * d->E * 4);
   L.part_z = off;   off = align_up(off + chunks * 4);
   L.part_n = off;   off = align_up(off + chunks * 4);
-  L.seq_loss = off; off = align_up(off + (size_t)L.S * (L.cps > 1 ? L.eb : 1) * 4);
-  L.seq_z = off;    off = align_up(off + (size_t)L.S * 4);
+  L.seq_loss = off; off = align_up(off + (size_t)L.entries * (L.cps > 1 ? L.eb : 1) * 4);
+  L.seq_z = off;    off = align_up(off + (size_t)L.entries * 4);
+  L.seq_n = off;    off = align_up(off + (size_t)L.entries * 4);
+  L.seq_some = off; off = align_up(off + (size_t)L.entries * 4);
   L.ticket = off;   off = align_up(off + 4);
   L.total = off;
   return L;
@@ -126,7 +137,7 @@ int moe_balance(const moe_dims* d, int seq_len, const float* logits, const int32
   MOE_TRY(check_ws_bytes(ws, ws_bytes, L.total));
   BalanceArgs a{};
   a.T = d->T; a.E = d->E; a.K = d->K; a.seq_len = seq_len; a.S = L.S; a.chunk = L.chunk;
-  a.cps = L.cps; a.eb = L.eb;
+  a.cps = L.cps; a.eb = L.eb; a.entries = L.entries;
   a.logits = logits; a.topk_idx = topk_idx; a.mask = mask;
   a.counts = counts; a.tokens = tokens; a.probs = probs; a.loss = loss;
   a.part_p = ws_at<float>(ws, L.part_p);
@@ -135,6 +146,9 @@ int moe_balance(const moe_dims* d, int seq_len, const float* logits, const int32
   a.part_n = ws_at<int32_t>(ws, L.part_n);
   a.seq_loss = ws_at<float>(ws, L.seq_loss);
   a.seq_z = ws_at<float>(ws, L.seq_z);
+  a.by = L.by;
+  a.seq_n = L.by != kByChunk ? ws_at<int32_t>(ws, L.seq_n) : tokens;
+  a.seq_some = L.by != kByChunk ? ws_at<int32_t>(ws, L.seq_some) : nullptr;
   a.ticket = ws_at<int32_t>(ws, L.ticket);
   return hip_status(launch_balance(a, as_stream(stream)), "moe_balance");
 }

@@ -20,7 +20,7 @@ SHAPES = [
     (64, 16, 4, 64, 0.0), (65, 12, 2, 65, 0.3), (300, 17, 6, 7, 0.2), (511, 64, 6, 511, 0.0), (513, 63, 6, 513, 0.1),
     (513, 64, 8, 512, 0.1), (1025, 20, 20, 1025, 0.5), (1500, 32, 4, 700, 0.0), (2000, 65, 3, 2000, 0.1),
     (900, 128, 8, 65, 0.1), (700, 130, 7, 700, 0.0), (600, 255, 8, 600, 0.2), (600, 256, 256, 550, 0.2),
-    (3000, 8, 2, 1030, 0.9),
+    (3000, 8, 2, 1030, 0.9), (20000, 4, 1, 1, 0.5), (20001, 6, 2, 2, 0.1), (1000, 70, 9, 8, 0.3), (999, 256, 12, 9, 0.3), (123, 130, 130, 5, 0.2), (68000, 3, 1, 66, 0.1), (115000, 2, 2, 112, 0.0),
 ]
 
 
@@ -57,7 +57,8 @@ def _forward(l, idx, mask, n, guard=0):
 def _check_forward(b, ref, l, mask, S, E):
     """p is off by the argument's rounding in exp (|l - max| EPS), 2 ulp of exp and of the division; a
     sum of n non-negative terms by EPS for each addition in its longest chain: 64 rows of a wave, 6
-    exchanges, 8 waves, and 64 chunks with their 32 rows."""
+    exchanges, 8 waves, and 64 chunks with their 32 rows; a mean over the sequences by 16 for a wave's or a
+    thread's share of them."""
     used = l[mask.astype(bool)] if mask is not None else l
     span = float(np.ptp(used, axis=1).max()) if used.size else 0.0
     rel = EPS * (span + 8 + 64 + 6 + 8 + 64 + 32)
@@ -65,7 +66,7 @@ def _check_forward(b, ref, l, mask, S, E):
     assert np.array_equal(host(b.tokens).ravel()[:S + 2], ref["tokens"])
     probs, loss = host(b.probs).ravel()[:S * E].reshape(S, E), host(b.loss).ravel()[:2]
     assert np.all(np.abs(probs - ref["probs"]) <= rel * ref["probs"] + 1e-37)
-    assert abs(loss[0] - ref["loss"][0]) <= (rel + EPS * (16 + E)) * ref["loss"][0]
+    assert abs(loss[0] - ref["loss"][0]) <= (rel + EPS * (32 + E)) * ref["loss"][0]
     # lse = max + log(sum): off by EPS (|max| + |log| + 4); its square by twice |lse| of that
     top = float(np.abs(used).max()) + np.log(E) + 4 if used.size else 0.0
     assert abs(loss[1] - ref["loss"][1]) <= 2 * top * top * 4 * EPS + rel * ref["loss"][1]
