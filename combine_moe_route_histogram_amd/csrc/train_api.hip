@@ -36,20 +36,21 @@ struct BalanceLayout {
 BalanceLayout balance_layout(const moe_dims* d, int seq_len) {
   BalanceLayout L;
   L.S = sequences(d, seq_len);
+  // a lane group or a wave for a sequence, or blocks for chunks of it
+  L.by = seq_len <= kBalanceFew ? kByGroup
+       : seq_len <= kBalanceShort || (seq_len <= kBalanceShortMany && L.S >= kBalanceMany) ? kByWave : kByChunk;
   // Chunks of up to 64 tokens for each of 8 waves where that makes two blocks for each CU, else smaller ones (a
   // wave's tokens are one chain): 131072 tokens, 256 experts 50 us with 256 chunks, 40 with 512, 51 with 2048,
-  // as the joining launch has more to read.
+  // as the joining launch has more to read.  Not where there are many sequences, each with joining blocks of its
+  // own (30000 tokens, 256 experts in sequences of 70: 18 us, 66 in two chunks each).
   L.chunk = seq_len < kBalanceChunk ? (seq_len + 7) / 8 * 8 : kBalanceChunk;
   L.cps = 1;
   if (L.by == kByChunk) {
-    while (L.chunk > 64 && (int64_t)L.S * ((seq_len + L.chunk - 1) / L.chunk) < 512) L.chunk = (L.chunk / 2 + 7) / 8 * 8;
+    while (L.chunk > 64 && L.S < 64 && (int64_t)L.S * ((seq_len + L.chunk - 1) / L.chunk) < 512) L.chunk = (L.chunk / 2 + 7) / 8 * 8;
     L.cps = (seq_len + L.chunk - 1) / L.chunk;
   }
   L.eb = (d->E + 31) / 32;
   L.entries = L.S;
-  // a lane group or a wave for a sequence, or blocks for chunks of it
-  L.by = seq_len <= kBalanceFew ? kByGroup
-       : seq_len <= kBalanceShort || (seq_len <= kBalanceShortMany && L.S >= kBalanceMany) ? kByWave : kByChunk;
   if (L.by != kByChunk) {
     const int per = seq_len <= kBalanceFew ? 4 * (64 / balance_lanes(d->E)) : 4;
     const int blocks = L.S / per + (L.S % per != 0);
