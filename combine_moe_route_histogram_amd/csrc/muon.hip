@@ -9,11 +9,11 @@
 //
 // Numbers.  X is kept in fp16, scaled by 2^10 (|x| <= 64 fits, an element of 1e-5 still has all
 // its bits), at first as two parts hi + lo (22 bits).  The products take the upper parts (11 bits)
-// with f32 sums; a X is formed in f32 from both parts.  The roundings of a product then act on X
+// with f32 sums, a is part of B's diagonal, and what that leaves of X, a times the lower part, is
+// added in f32.  The roundings of a product then act on X
 // from the left only, inside its row space, while a rounding of X itself has null directions, which
 // every later step makes |a| times larger.  So X drops its lower part when what the steps left
-// can make of it is small (kDropLow), and from there on a is part of B's diagonal: X <- (a I + B) X
-// without a second look at X.  That is 1e-3 to 3e-3 of the result's norm for any rank (no lower parts
+// can make of it is small (kDropLow).  That is 1e-3 to 3e-3 of the result's norm for any rank (no lower parts
 // at all: 2e-2 for rank 64 of 352, 7e-2 for rank 4; everything in bf16: 1e-2 for a full rank and 0.2,
 // 0.6 for those), with 40 % fewer bytes for X than two parts all the way.
 // The exact form takes three products, lo hi + hi lo + hi hi, of X, A and a I + B in two parts each.
@@ -31,7 +31,7 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 constexpr float kXScale = 1024.f;   // of stored X
 constexpr float kAScale = 256.f;    // of stored A and B
 
-// kAdd: kStep that adds a X from both parts of X
+// kAdd: kStep that adds a times the lower part of X
 enum NewtonKind { kGram, kPoly, kStep, kAdd, kOut, kUpdate };
 
 // One product of a batch of matrices.  Operands and results are [batch][rows][ld] fp16 planes.
@@ -41,12 +41,12 @@ struct Product {
   int lda, ldb, k_len;
   int m_len, n_len;         // padded sizes of the result
   int mt, nt, per, tiles;   // tile grid, tiles of a matrix and of all
-  const uint16_t *ch, *cl;  // what the epilogue adds: A (kPoly) or X (kAdd)
+  const uint16_t *ch, *cl;  // what the epilogue adds: A (kPoly), the lower part of X (kAdd: ch)
   uint16_t *oh, *ol;        // kGram, kPoly, kStep, kAdd; ol NULL: upper parts only
   uint16_t *th, *tl;        // small tiles, kStep and kAdd: the result's transpose
   int64_t o_mat;
   int ldo, ldt;             // of ch, cl, oh, ol; of th, tl
-  float a, b, c;            // kPoly: a for the diagonal, or 0
+  float a, b, c;
   // kOut, kUpdate
   bool tall, bf16;
   int R, C, g0;
@@ -184,7 +184,7 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
   static_assert(kRps >= 1 && (C::NW + kRps - 1) / kRps <= C::STAGES, "epilogue regions fit in the slices");
   constexpr int kBlocks = C::MI * (C::NJ / 2);
   constexpr bool kSym = KIND == kGram || KIND == kPoly, kLast = KIND == kOut || KIND == kUpdate;
-  constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kAdd || (KIND == kPoly && EXACT);
+  constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kPoly && EXACT;
   const int rs = wave / kRps;
   uint8_t* const rbase = rs == 0 ? stages[0] : rs == 1 ? stages[1] : rs == 2 ? stages[2] : stages[3];
   uint8_t* const region = rbase + (wave - rs * kRps) * kEpiRegionBytes;
@@ -438,7 +438,7 @@ void newton_kernel(Product p) {
 template <int KIND, bool EXACT, int T, int D>   // D: slices of a wave in LDS
 __global__ __launch_bounds__(256) void newton_small_kernel(Product p) {
   constexpr bool kSym = KIND == kGram || KIND == kPoly, kLast = KIND == kOut || KIND == kUpdate;
-  constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kAdd || (KIND == kPoly && EXACT);
+  constexpr bool kAux = KIND == kPoly || KIND == kAdd, kAuxLow = KIND == kPoly && EXACT;
   constexpr int B = T / 32;                       // 32-wide blocks of a side
   constexpr int P = EXACT ? 2 : 1;                // parts of a factor
   constexpr int kPlane = T * 64 * 2, kSlice = 2 * P * kPlane, kPart = 4 * T * (T + 1) * 4;
@@ -663,14 +663,15 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Source s, Start d) {
     if (r < s.R && c < s.C) {
       const int64_t at = base + (int64_t)r * s.C + c;
       float m[4] = {0.f, 0.f, 0.f, 0.f};
+      const bool grad = !s.mom || s.nesterov;
       if constexpr (V == 4) {
-        Elem<float>::unpack(ld16(s.g + at), u[j]);
+        if (grad) Elem<float>::unpack(ld16(s.g + at), u[j]);
         if (s.mom) Elem<float>::unpack(ld16(s.mom + at), m);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (c + e < s.C) {
-            u[j][e] = s.g[at + e];
+            if (grad) u[j][e] = s.g[at + e];
             if (s.mom) m[e] = s.mom[at + e];
           }
       }
@@ -859,7 +860,7 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
       const bool last = k + 1 == c.steps, add = !p.exact && keeps_low(c, k);
       Product q{};
       q.b = c.coef[k][1]; q.c = c.coef[k][2];
-      q.a = add ? 0.f : c.coef[k][0];
+      q.a = c.coef[k][0];
       q.ah = xh; q.al = xl; q.bh = xh; q.bl = xl;
       q.a_mat = q.b_mat = x_mat;
       q.lda = q.ldb = q.k_len = p.lp;
@@ -874,14 +875,13 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
       q.oh = bh; q.ol = bl;
       e = product<kPoly>(q, p, batch, st);
       if (e != hipSuccess) return e;
-      q.a = c.coef[k][0];
       q.ah = bh; q.al = bl;
       q.bh = p.small ? at(p.th[k & 1]) : xh;
       q.bl = p.small ? at(p.tl[k & 1]) : xl;
       q.a_mat = a_mat; q.b_mat = x_mat;
       q.lda = q.k_len = p.sp; q.ldb = p.small ? p.sp : p.lp;
       q.n_len = p.lp;
-      q.ch = xh; q.cl = xl;
+      q.ch = xl;
       q.o_mat = x_mat; q.ldo = p.lp;
       if (!last) {
         q.oh = at(p.xh[(k + 1) & 1]);

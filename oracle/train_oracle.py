@@ -98,8 +98,8 @@ def _chain(p, q):
 def newton_model(u, exact, coef=COEF):
     """The iteration as the products round it.  X has two fp16 parts, of which the lower one is dropped from
     the step on whose |a|, with those of the later steps, make at most 12 (never in the exact form, always
-    for the last step otherwise); a X is added from both parts, or, once there is one part and in the exact form,
-    a is part of B's diagonal.  Factors have one part (exact: two)."""
+    for the last step otherwise).  a is part of B's diagonal; a times the lower part is added.  Factors have one
+    part (exact: two)."""
     x = np.asarray(u, np.float64)
     tall = x.shape[0] > x.shape[1]
     if tall:
@@ -117,13 +117,10 @@ def newton_model(u, exact, coef=COEF):
         xs = _parts(x, 1024) if low else (_half(x, 1024), np.zeros_like(x))
         A = _parts(mul(xs, (xs[0].T, xs[1].T)), 256)
         whole = A[0] + A[1] if exact else A[0]
-        add = low and not exact
-        B = f(b) * whole + f(c) * mul(A, A)
-        if not add:
-            B = B + f(a) * np.eye(len(B), dtype=f)
+        B = f(b) * whole + f(c) * mul(A, A) + f(a) * np.eye(len(A[0]), dtype=f)
         x = mul(_parts(B, 256), xs)
-        if add:
-            x = f(a) * (xs[0] + xs[1]) + x
+        if low and not exact:
+            x = f(a) * xs[1] + x
     return x.T if tall else x
 
 
