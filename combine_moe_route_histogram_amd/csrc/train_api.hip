@@ -19,8 +19,12 @@ int check_ws_bytes(const void* ws, size_t ws_bytes, size_t need) {
 
 // ---- router losses
 
+constexpr int kBalanceMaxTokens = 1 << 28;   // a launch holds less than 2^32 threads
+
 int check_balance(const moe_dims* d, int seq_len) {
   MOE_TRY(check_dims(d));
+  if (d->T > kBalanceMaxTokens)
+    return fail(MOE_EUNSUPPORTED, "the router's losses take at most %d tokens (T=%d)", kBalanceMaxTokens, d->T);
   if (seq_len < 1 || seq_len > d->T)
     return fail(MOE_EINVAL, "seq_len must be in [1, T] (got seq_len=%d, T=%d)", seq_len, d->T);
   return MOE_OK;

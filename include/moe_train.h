@@ -31,7 +31,7 @@ extern "C" {
  *           in any state; calls that overlap in time need separate ones.
  * Without any token both losses are 0.  A logit of -inf takes its expert out of a
  * row.  A row of only -inf, or with +inf or NaN, makes its sequence's probs, and
- * the losses, NaN.  Uses T, E and K of the dims (all are checked).
+ * the losses, NaN.  Uses T, E and K of the dims (all are checked); T <= 2^28.
  * Errors: MOE_EINVAL for seq_len outside [1, T], MOE_EWORKSPACE. */
 size_t moe_balance_workspace_bytes(const moe_dims* d, int seq_len);
 int moe_balance(const moe_dims* d, int seq_len, const float* logits, const int32_t* topk_idx,

@@ -302,6 +302,43 @@ def test_captured_step_replays():
             assert torch.equal(t, x)
 
 
+def test_gradient_over_the_tokens_of_two_ranks():
+    """Two halves of a batch, each with the counts and tokens of both, give the rows of the whole batch's
+    gradient (same arithmetic for a row: same bits)."""
+    T, E, K = 1200, 24, 3
+    l, idx, mask, w, dw = _case(T, E, K, 0.2, 71)
+    d, b = _forward(l, idx, mask, T)
+    dloss = torch.tensor([0.4, 0.3], device="cuda")
+    want = _backward(d, T, _cuda(l), _cuda(mask), b.counts, b.tokens, dloss, [_cuda(x) for x in (dw, w, idx)])
+    cut = 500
+    halves = [slice(0, cut), slice(cut, T)]
+    ranks = [_forward(l[h], idx[h], mask[h], len(l[h])) for h in halves]
+    counts = ranks[0][1].counts + ranks[1][1].counts
+    tokens = ranks[0][1].tokens + ranks[1][1].tokens
+    tokens[2] = 1
+    assert torch.equal(counts, b.counts) and torch.equal(tokens, b.tokens)
+    for h, (dr, _) in zip(halves, ranks):
+        got = _backward(dr, dr.T, _cuda(l[h]), _cuda(mask[h]), counts, tokens, dloss, [_cuda(x[h]) for x in (dw, w, idx)])
+        assert torch.equal(got, want[h])
+
+
+def test_two_calls_at_once():
+    """Two batches on two streams, each with its own buffers."""
+    cases = [_case(3000, 32, 4, 0.1, 81), _case(2500, 100, 6, 0.3, 82)]
+    want = [_forward(l, i, m, 700)[1] for l, i, m, _, _ in cases]
+    dev = [[_cuda(a) for a in c[:3]] for c in cases]
+    bufs = [L.BalanceBuffers(b.d, 700) for b in want]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, (l, i, m), s in zip(bufs, dev, streams):
+            L.balance(b, l, i, m, stream=s)
+    torch.cuda.synchronize()
+    for b, w in zip(bufs, want):
+        for n in ("counts", "tokens", "probs", "loss"):
+            assert torch.equal(getattr(b, n), getattr(w, n)), n
+
+
 def test_a_layer_step_with_losses():
     """forward, losses, backward of a whole layer: dlogits is route_bwd's plus the losses' gradient, and
     everything else keeps its bits."""

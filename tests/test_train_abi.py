@@ -65,7 +65,8 @@ def _balance_bwd(lib, d, seq_len=16, **over):
     return lib.moe_balance_bwd(ctypes.byref(d), seq_len, *[over.get(n, P) for n in names], None)
 
 
-@pytest.mark.parametrize("kw,status", [(dict(T=0), 1), (dict(E=257), 2), (dict(K=9), 2), (dict(K=0), 2), (dict(H=4), 2)])
+@pytest.mark.parametrize("kw,status", [(dict(T=0), 1), (dict(E=257), 2), (dict(K=9), 2), (dict(K=0), 2), (dict(H=4), 2),
+                                       (dict(T=(1 << 28) + 1), 2)])
 def test_balance_bad_dims(lib, kw, status):
     d = _dims(**kw)
     assert _balance(lib, d, 1) == status and _balance_bwd(lib, d, 1) == status
