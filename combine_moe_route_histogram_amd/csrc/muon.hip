@@ -107,23 +107,29 @@ __device__ __forceinline__ void join16(const u32x4& hi, const u32x4* lo, float* 
   join16(h1, lo ? &l1 : nullptr, v + 4);
 }
 
-// Four results of row `row` from column `col` on, of matrix g of the user's tensors.
+// master <- keep master - gain O, and its bf16 copy.
+struct UpdateScale { float keep, gain; };
+__device__ __forceinline__ void update4(const Product& p, const UpdateScale& u, int64_t at, const f32x4& m, const float* v) {
+  float x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = u.keep * m[e] - u.gain * v[e];
+  *reinterpret_cast<f32x4*>(p.master + at) = f32x4{x[0], x[1], x[2], x[3]};
+  if (p.w) st_bf16x4(p.w + at, x);
+}
+
+// Four results of row `row` from column `col` on, of matrix g of the user's tensors.  m: the four
+// elements of master, if they were loaded ahead.
 template <int KIND>
-__device__ __forceinline__ void emit4(const Product& p, int64_t g, int row, int col, const float* v, float lr) {
+__device__ __forceinline__ void emit4(const Product& p, int64_t g, int row, int col, const float* v,
+                                      const UpdateScale& u, const f32x4* m = nullptr) {
   if (row >= p.R || col >= p.C) return;
   const int64_t at = (g * p.R + row) * p.C + col;
-  const float keep = 1.f - lr * p.weight_decay, gain = lr * p.scale;
   if (p.C % 4 == 0) {   // aligned: 16-byte f32, 8-byte bf16
     if constexpr (KIND == kOut) {
       if (p.bf16) st_bf16x4(static_cast<uint16_t*>(p.out) + at, v);
       else *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at) = f32x4{v[0], v[1], v[2], v[3]};
     } else {
-      f32x4 m = *reinterpret_cast<const f32x4*>(p.master + at);
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = keep * m[e] - gain * v[e];
-      *reinterpret_cast<f32x4*>(p.master + at) = f32x4{x[0], x[1], x[2], x[3]};
-      if (p.w) st_bf16x4(p.w + at, x);
+      update4(p, u, at, m ? *m : *reinterpret_cast<const f32x4*>(p.master + at), v);
     }
     return;
   }
@@ -134,11 +140,15 @@ __device__ __forceinline__ void emit4(const Product& p, int64_t g, int row, int 
       if (p.bf16) static_cast<uint16_t*>(p.out)[at + e] = (uint16_t)f32_to_bf16(v[e]);
       else static_cast<float*>(p.out)[at + e] = v[e];
     } else {
-      const float x = keep * p.master[at + e] - gain * v[e];
+      const float x = u.keep * p.master[at + e] - u.gain * v[e];
       p.master[at + e] = x;
       if (p.w) p.w[at + e] = (uint16_t)f32_to_bf16(x);
     }
   }
+}
+__device__ __forceinline__ UpdateScale update_scale(const Product& p) {
+  const float lr = p.lr_dev ? *p.lr_dev : p.lr;
+  return {1.f - lr * p.weight_decay, lr * p.scale};
 }
 
 // Result of four elements of row m from column n on: their sums s and the values x that are added.
@@ -189,8 +199,8 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
   uint8_t* const rbase = rs == 0 ? stages[0] : rs == 1 ? stages[1] : rs == 2 ? stages[2] : stages[3];
   uint8_t* const region = rbase + (wave - rs * kRps) * kEpiRegionBytes;
   uint32_t* const reg = reinterpret_cast<uint32_t*>(region);
-  float lr = 0.f;
-  if constexpr (KIND == kUpdate) lr = p.lr_dev ? *p.lr_dev : p.lr;
+  UpdateScale scale = {};
+  if constexpr (KIND == kUpdate) scale = update_scale(p);
   const int64_t obase = g * p.o_mat;
   const bool turn = kSym ? mirror : kLast && p.tall;
   const int q0 = lane >> 3, c8 = 8 * (lane & 7);
@@ -205,7 +215,24 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
       if constexpr (kAuxLow) aux_l[buf][pass] = ld16(p.cl + at);
     }
   };
+  // master, likewise (a load behind the stores of the block before would wait for them): rows as they are
+  // stored below, clamped into the matrix
+  f32x4 mst[2][KIND == kUpdate ? 8 : 1];
+  const bool ahead = KIND == kUpdate && p.C % 4 == 0;
+  auto load_master = [&](int blk, int buf) {
+    const int mb = m0 + wm * C::WM + 32 * (blk / (C::NJ / 2)), nb = n0 + wn * C::WN + 64 * (blk % (C::NJ / 2));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int row = turn ? nb + j * 8 + (lane >> 3) : mb + (j >> 1) * 8 + q0;
+      const int col = turn ? mb + 4 * (lane & 7) : nb + c8 + 4 * (j & 1);
+      const int64_t at = ((p.g0 + g) * p.R + min(row, p.R - 1)) * p.C + min(col, p.C - 4);
+      mst[buf][j] = *reinterpret_cast<const f32x4*>(p.master + at);
+    }
+  };
   if constexpr (kAux) load_aux(0, 0);
+  if constexpr (KIND == kUpdate) {
+    if (ahead) load_master(0, 0);
+  }
 #pragma unroll
   for (int i = 0; i < C::MI; ++i) {
 #pragma unroll
@@ -213,6 +240,9 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
       const int blk = i * (C::NJ / 2) + hc;
       if constexpr (kAux) {
         if (blk + 1 < kBlocks) load_aux(blk + 1, (blk + 1) & 1);
+      }
+      if constexpr (KIND == kUpdate) {
+        if (ahead && blk + 1 < kBlocks) load_master(blk + 1, (blk + 1) & 1);
       }
       const int mb = m0 + wm * C::WM + 32 * i, nb = n0 + wn * C::WN + 64 * hc;
       if (mb >= p.m_len || nb >= p.n_len) continue;   // the sizes are whole blocks
@@ -246,8 +276,9 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
             if constexpr (EXACT) low[pass] = lo;
           }
         } else if (!turn) {
-          emit4<KIND>(p, p.g0 + g, m, n, v, lr);
-          emit4<KIND>(p, p.g0 + g, m, n + 4, v + 4, lr);
+          constexpr bool kUp = KIND == kUpdate;
+          emit4<KIND>(p, p.g0 + g, m, n, v, scale, kUp ? &mst[blk & 1][2 * pass] : nullptr);
+          emit4<KIND>(p, p.g0 + g, m, n + 4, v + 4, scale, kUp ? &mst[blk & 1][2 * pass + 1] : nullptr);
         } else if (KIND == kOut && turn16) {
           *reinterpret_cast<u32x4*>(region + q * kTurnPitch + 2 * c8) = Elem<uint16_t>::pack(v);
         } else {
@@ -277,7 +308,7 @@ __device__ __forceinline__ void newton_epilogue(const Product& p, int64_t g, int
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(reg[(m4 + e) * kEpiPitch + n]);
-            emit4<KIND>(p, p.g0 + g, nb + n, mb + m4, v, lr);
+            emit4<KIND>(p, p.g0 + g, nb + n, mb + m4, v, scale, KIND == kUpdate ? &mst[blk & 1][pass] : nullptr);
           }
         }
       }
@@ -535,8 +566,8 @@ __global__ __launch_bounds__(256) void newton_small_kernel(Product p) {
       for (int q = 0; q < 16; ++q)
         part[wave][32 * i + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)][32 * j + (lane & 31)] = acc[i][j][q];
   __syncthreads();
-  float lr = 0.f;
-  if constexpr (KIND == kUpdate) lr = p.lr_dev ? *p.lr_dev : p.lr;
+  UpdateScale scale = {};
+  if constexpr (KIND == kUpdate) scale = update_scale(p);
   const bool turn = kSym ? tm != tn : kLast ? p.tall : true;   // a step writes X and its transpose
 #pragma unroll
   for (int it = 0; it < kTurns; ++it) {
@@ -555,7 +586,7 @@ __global__ __launch_bounds__(256) void newton_small_kernel(Product p) {
       *reinterpret_cast<u32x2*>(p.oh + at) = hi;
       if (EXACT || (!kSym && p.ol)) *reinterpret_cast<u32x2*>(p.ol + at) = lo;
     } else if (!turn) {
-      emit4<KIND>(p, p.g0 + g, m, n, v, lr);
+      emit4<KIND>(p, p.g0 + g, m, n, v, scale);
     }
     if (turn) {
 #pragma unroll
@@ -579,7 +610,7 @@ __global__ __launch_bounds__(256) void newton_small_kernel(Product p) {
       *reinterpret_cast<u32x2*>(th + at) = hi;
       if (EXACT) *reinterpret_cast<u32x2*>(tl + at) = lo;
     } else {
-      emit4<KIND>(p, p.g0 + g, n0 + n, m0 + m4, v, lr);
+      emit4<KIND>(p, p.g0 + g, n0 + n, m0 + m4, v, scale);
     }
   }
 }
