@@ -750,6 +750,10 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Source s, Start d) {
 
 // ---------------------------------------------------------------------- host
 
+// Up to so many 64 x 64 tiles a product takes small tiles (for X, which then is kept with its transpose: whole
+// calls of 32 [256, 256] 119 us with small tiles and 139 without).
+constexpr int kSmallTiles = 512;
+
 inline int up(int v, int to) { return (v + to - 1) / to * to; }
 
 unsigned xcd_grid(int tiles) { return (unsigned)kXcds * ((tiles + kXcds - 1) / kXcds); }
@@ -774,6 +778,18 @@ hipError_t product_small(Product p, int batch, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Time of a product in rounds of tiles over 256 CUs: the last round counts in full as long as there are
+// few.  One 256 x 256 tile of a CU takes 1.65 (us for each 64 k), two 128 x 128 ones 1.25, a single one 0.75.
+double rounds(int64_t tiles, int at_once) {
+  return tiles <= 4 * at_once ? (double)((tiles + at_once - 1) / at_once) : (double)tiles / at_once;
+}
+double big_rounds(int64_t tiles) { return 1.65 * rounds(tiles, 256); }
+double mid_rounds(int64_t tiles) { return tiles <= 256 ? 0.75 : 1.25 * rounds(tiles, 512); }
+
+// Tiles by their number.  A and B of 1 [1024, 8192] (us; 256 x 256, 128 x 128 and small tiles): 405, 213, 60 and
+// 66, 34, 15 (f32); of 20 [300, 2000] 38, 23, 16 and 15, 9, 8; of 4 [1000, 1000] 26, 15, 17; of 6 [1100, 1100] 30, 21,
+// 28; of 1 [4096, 4096] the whole call 1476 with 256 x 256, 1800 with 128 x 128.  X of 8 [512, 1024] 17, 10, 16; of
+// 20 [300, 2000] 28, 20, 39; of 3 [700, 5000] f32 56, 60, 113.
 template <int KIND, bool EXACT>
 hipError_t product(const Product& p, bool small, int batch, hipStream_t st) {
   constexpr bool kMn = KIND != kGram && KIND != kPoly;
@@ -783,6 +799,7 @@ hipError_t product(const Product& p, bool small, int batch, hipStream_t st) {
     const int64_t mt = (p.m_len + t - 1) / t, nt = (p.n_len + t - 1) / t;
     return batch * (kMn ? mt * nt : mt * (mt + 1) / 2);
   };
+  if (!kMn) small = tiles(64) <= kSmallTiles;   // both operands lie along k in any case
   // 32 x 32 tiles until there are two for each CU: whole calls of [512, 512] 95 us with them and 148
   // with 64 x 64 ones (f32), of [1024, 1024] 296 and 223.  Two slices of two parts take a CU's LDS, so they
   // are for one tile on a CU: 5 [264, 416] 128 us with two, 110 with one; [64, 14336] 246 and 293.
@@ -793,7 +810,8 @@ hipError_t product(const Product& p, bool small, int batch, hipStream_t st) {
     }
     return product_small<KIND, EXACT, 32, 2>(p, batch, st);
   }
-  return tiles(256) >= 256 ? product_with<KIND, EXACT, Big>(p, batch, st) : product_with<KIND, EXACT, Mid>(p, batch, st);
+  return big_rounds(tiles(256)) <= mid_rounds(tiles(128)) ? product_with<KIND, EXACT, Big>(p, batch, st)
+                                                          : product_with<KIND, EXACT, Mid>(p, batch, st);
 }
 template <int KIND>
 hipError_t product(const Product& q, const NewtonPlan& p, int batch, hipStream_t st) {
@@ -827,10 +845,7 @@ NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
   p.sp = up(p.s, kNewtonPad);
   p.lp = up(p.l, kNewtonPad);
   p.exact = !bf16 || p.s < kNewtonFewRows;
-  // Small tiles where 256 x 256 and 128 x 128 ones leave CUs without work, unless k is long: whole calls of
-  // 8 [512, 1024] 178 us with them and 206 without (bf16), 32 [256, 256] 119 and 139; of [2048, 2048] 451 and 414,
-  // of 128 [256, 256] 289 and 218.
-  p.small = (int64_t)G * (p.sp / 64) * (p.lp / 64) <= 1024 && p.sp <= 1024;
+  p.small = (int64_t)G * (p.sp / 64) * (p.lp / 64) <= kSmallTiles;
   // About 2048 tiles of 256 x 256 to a launch: 8 rounds over the 256 CUs, of which the last one
   // is partly empty; more would only take memory (at most 2^30 elements of X, or one matrix).
   const int64_t t = (p.sp + 255) / 256, tiles = t * (t + 1) / 2;

@@ -23,7 +23,7 @@ struct NewtonPlan {
   bool tall;           // R > C
   int s, l, sp, lp;
   bool exact;          // factors of two fp16 parts (22 bits)
-  bool small;          // small tiles, X kept with its transpose
+  bool small;          // small tiles for X, which is kept with its transpose
   int batch;           // matrices worked on at a time
   // workspace sections (byte offsets)
   size_t parts, xh[2], xl[2], th[2], tl[2], ah, al, bh, bl, total;

@@ -77,6 +77,17 @@ def test_orthogonalize(G, R, C, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,R,C", [(3, 700, 1500), (4, 2100, 400), (60, 500, 520), (61, 400, 330), (1, 1410, 1400), (1, 100, 9000)])
+def test_orthogonalize_with_products_of_different_tiles(G, R, C, dtype):
+    """Stacks whose first two products take other tiles than the third, or all the largest."""
+    print(f"case orthogonalize G={G} R={R} C={C} {dtype}", flush=True)
+    x = _grad(G, R, C, G + R + C)
+    got = _ortho(x, dtype)
+    for g in {0, G - 1}:
+        _check(got[g], x[g], dtype, what=f"matrix {g}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_low_rank(dtype):
     """Gradients of experts with few tokens: null directions must not gather roundings."""
     g = np.random.default_rng(2)
