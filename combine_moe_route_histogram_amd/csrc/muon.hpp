@@ -9,6 +9,7 @@
 namespace moe {
 
 constexpr int kNewtonMaxDim = 1 << 20;
+constexpr int kNewtonMaxStack = 1 << 30;   // a matrix's number plus those worked on at a time stay in 31 bits
 constexpr int64_t kNewtonMaxMatrix = (int64_t)1 << 32;   // elements: keeps tile and block counts in 31 bits
 constexpr int kNewtonPad = 64;       // of both sides of a stored matrix: whole k slices, zero-filled
 // Fewer rows (or columns) than this take factors of two parts whatever the type: their roundings do

@@ -87,6 +87,7 @@ constexpr int kDefaultSteps = 5;
 
 int check_stack(int G, int R, int C, int dtype) {
   if (G < 1) return fail(MOE_EINVAL, "G must be >= 1 (got %d)", G);
+  if (G > kNewtonMaxStack) return fail(MOE_EUNSUPPORTED, "G must be at most %d (got %d)", kNewtonMaxStack, G);
   if (R < 1 || R > kNewtonMaxDim)
     return fail(MOE_EUNSUPPORTED, "R must be in [1, %d] (got %d)", kNewtonMaxDim, R);
   if (C < 1 || C > kNewtonMaxDim)

@@ -116,6 +116,14 @@ def test_stack_bad_sizes(lib, G, R, C, dtype, status):
     assert lib.moe_muon_workspace_bytes(G, R, C, dtype) == 0
 
 
+def test_stack_of_too_many_matrices(lib):
+    """The number of a matrix is counted up by parts of the stack, in 31 bits."""
+    assert lib.moe_muon_workspace_bytes(1 << 30, 1, 1, 1) > 0
+    for G in ((1 << 30) + 1, 2 ** 31 - 1):
+        assert lib.moe_muon_workspace_bytes(G, 1, 1, 1) == 0
+        assert _ortho(lib, G, 1, 1) == 2 and _muon(lib, G, 1, 1) == 2
+
+
 def test_stack_pointers_and_workspace(lib):
     for n in ("g", "out"):
         assert _ortho(lib, **{n: None}) == 1 and n in M.moe_last_error()
