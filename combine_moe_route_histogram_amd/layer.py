@@ -84,7 +84,7 @@ def backward(b: Buffers, p: dict, fused: bool = False, stream=None, losses=None)
     """combine_bwd -> FFN input grads (B) -> FFN weight grads (W) -> dispatch_bwd -> route_bwd.
     fused: B and W in one launch, W filling the gaps of B (moe_expert_ffn_bwd).
     losses: BalanceBuffers of this step's logits (balance); p["dloss"], the gradients of its two
-    losses, then go into dlogits along with route_bwd's."""
+    losses, then go into dlogits along with route_bwd's, with the mask that balance was given."""
     d = b.d
     moe_combine_bwd(d, p["dout"], b.y, b.slot, b.topk_w, b.dy, b.dtopk_w, stream)
     if fused:
@@ -102,7 +102,7 @@ def backward(b: Buffers, p: dict, fused: bool = False, stream=None, losses=None)
     if losses is None:
         moe_route_bwd(d, b.dtopk_w, b.topk_w, b.topk_idx, b.dlogits, stream)
     else:
-        moe_balance_bwd(d, losses.seq_len, p["logits"], p.get("mask"), losses.counts, losses.tokens, p["dloss"],
+        moe_balance_bwd(d, losses.seq_len, p["logits"], losses.mask, losses.counts, losses.tokens, p["dloss"],
                         b.dtopk_w, b.topk_w, b.topk_idx, b.dlogits, stream)
 
 
@@ -161,10 +161,12 @@ class BalanceBuffers:
         self.tokens = z(S + 2, dtype=torch.int32)       # of each sequence; all; sequences with any
         self.probs = z(S, d.E, dtype=torch.float32)     # sums of softmax(logits)
         self.loss = z(2, dtype=torch.float32)           # load balance; squared log-sum-exp
+        self.mask = None                                # of the losses, for their gradient
 
 
 def balance(l: BalanceBuffers, logits, topk_idx, mask=None, stream=None):
     """The router's losses and per-expert counts of routed tokens (mask: 0 for padding)."""
+    l.mask = mask
     moe_balance(l.d, l.seq_len, logits, topk_idx, mask, l.counts, l.tokens, l.probs, l.loss, l.ws, stream)
 
 

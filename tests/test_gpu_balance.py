@@ -365,3 +365,25 @@ def test_a_layer_step_with_losses():
     want = TO.balance_bwd(l, mask, 128, cfg.E, cfg.K, ref["counts"], ref["tokens"], np.array([0.2, 0.1], np.float32))
     want = want + host(before["dlogits"])
     assert np.max(np.abs(host(b.dlogits) - want)) <= 64 * EPS * max(1.0, np.abs(want).max())
+
+
+def test_backward_of_a_layer_takes_the_mask_of_its_losses():
+    """The mask is given once; padding gets no gradient of the losses, and a later call without one has none.
+    w (dw - sum w dw) of two picks, w <= 1: 2 roundings of the sum, 2 of the difference and 2 of the product
+    at most of size max |dw|, on either side; the losses' gradient of a token is 1e-4 and more."""
+    cfg = custom_config(100, 64, 6, 2, 96)
+    p = device_inputs(synth.make_inputs(cfg))
+    d = L.make_dims(cfg.T, cfg.H, cfg.E, cfg.K, cfg.I)
+    b, losses = L.Buffers(d), L.BalanceBuffers(d)
+    L.forward(b, p, fused=True)
+    L.backward(b, p, fused=True)
+    torch.cuda.synchronize()
+    plain = b.dlogits.clone()
+    mask = torch.arange(cfg.T, device="cuda") % 3 != 0
+    p["dloss"] = torch.tensor([0.2, 0.1], device="cuda")
+    for m in (mask, None):
+        L.balance(losses, p["logits"], b.topk_idx, m)
+        L.backward(b, p, fused=True, losses=losses)
+        L.check()
+        same = (b.dlogits - plain).abs().amax(1) <= 12 * EPS * b.dtopk_w.abs().amax(1)
+        assert torch.equal(same, torch.zeros_like(same) if m is None else ~mask)
