@@ -81,10 +81,11 @@ size_t moe_muon_workspace_bytes(int G, int R, int C, int dtype);
  * 1e-3 to 3e-3 of its norm, low ranks included (before its rounding to bf16).
  * MOE_F32, and matrices with fewer than 32 rows or columns: factors of 22 bits, as
  * exact as f32 arithmetic.
- * Any G from 1 to 2^30 and R, C from 1 to 2^20 with R*C <= 2^32 and G*R*C <= 2^39.  A matrix of zeros gives zeros; an infinity
- * or NaN makes its own matrix NaN and no other.  The scale of a matrix has no
- * effect, down to subnormal entries.  A matrix's bits depend on its values and on G, R
- * and C, not on the other matrices. */
+ * Any G from 1 to 2^30 and R, C from 1 to 2^20 with R*C <= 2^32 and G*R*C <= 2^39.  No step but
+ * the last may leave a singular value above 15 (the range of fp16; such a matrix becomes
+ * infinite or NaN).  A matrix of zeros gives zeros; an infinity or NaN makes its own matrix
+ * NaN and no other.  The scale of a matrix has no effect, down to subnormal entries.  A
+ * matrix's bits depend on its values and on G, R and C, not on the other matrices. */
 int moe_orthogonalize(int G, int R, int C, int dtype, const moe_newton* n, const float* g, void* out,
                       void* ws, size_t ws_bytes, void* stream);
 

@@ -113,6 +113,18 @@ def test_other_iterations(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_largest_singular_values(dtype):
+    """A step that leaves a singular value of 15, the largest documented, and ones that bring it back; the last
+    step may leave any."""
+    g = np.random.default_rng(9)
+    x = (g.standard_normal((1, 90, 1)) @ g.standard_normal((1, 1, 150))).astype(np.float32)
+    for coef in (((15.0, 0.0, 0.0), (1.5, -0.5 / 225, 0.0)), ((15.0, 0.0, 0.0), (32.0, 0.0, 0.0))):
+        got = _ortho(x, dtype, coef)
+        assert np.isfinite(got).all()
+        _check(got[0], x[0], dtype, coef)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_scale_has_no_effect(dtype):
     """Powers of two, down to subnormal entries and up to the largest, leave the bits."""
     x = np.sign(_grad(1, 90, 150, 3)) * (1 + np.random.default_rng(1).integers(0, 8, (1, 90, 150)) / 8)
