@@ -17,6 +17,8 @@
 // at all: 2e-2 for rank 64 of 352, 7e-2 for rank 4; everything in bf16: 1e-2 for a full rank and 0.2,
 // 0.6 for those), with 40 % fewer bytes for X than two parts all the way.
 // The exact form takes three products, lo hi + hi lo + hi hi, of X, A and a I + B in two parts each.
+//
+// Matrices of few rows (or columns) have a form of their own, on [s, s] in 64 bits: see newton_few_gram_kernel.
 #include "muon.hpp"
 
 #include "gemm_tile.hpp"
@@ -748,6 +750,262 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Source s, Start d) {
   store(turned_h, turned_l, cp, rp, c0, r0);
 }
 
+// ---------------------------------------------------------------------- few rows
+//
+// With few rows the iteration runs on the rows alone.  Every X_k is a polynomial of A_0 = U U^T / |U|^2 times
+// X_0, so with P_0 = I
+//   B_k = a + b A_k + c A_k^2,   P_k+1 = P_k B_k,   A_k+1 = B_k A_k B_k,   result = P U / |U|:
+// two passes over U and products of [s, s] between them, three launches for 17.  All of these matrices are
+// symmetric and commute.  What a rounding puts into a null direction of A_0 grows by a^2 with every step, as X's
+// own does by a, but nothing keeps it from turning negative: hence 64 bits throughout, and only as long as
+// the product of a^2 leaves 1e-8 of that (kFewGrow).  |U|^2 is the trace.  Bound by the matrix cores' rate in
+// 64 bits (a [64, 64] product 3 us on its CU) and, for fewer rows, by the chain of loads, barriers and launches: of
+// 64 [32, 1000] 8.5 + 15.7 + 9.0 us, of 1 [12, 14336] 5.4 + 11.4 + 4.0, of 64 [64, 14336] 158 + 53 + 317.
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kFewPitch = 4;          // of a row in LDS, beyond its doubles: rows 8 banks apart
+constexpr double kFewGrow = 4096.0;   // largest product of |a|
+
+// Rows of a result: register r of a lane holds row 4 r + lane / 16 of column lane % 16.
+__device__ __forceinline__ f64x4 mfma64(double a, double b, const f64x4& c) {
+  return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+
+struct Few {
+  Source u;
+  bool tall;
+  int s, l, chunk, chunks;
+  double *parts, *poly;   // [G][chunks][tiles][256], [G][16 NB][16 NB]
+};
+
+// Sums of products of rows over `chunk` of l (a quarter to each wave), tiles on and above the diagonal; with
+// momentum, its update on the way.  A lane's element is both operands': X[16 i + lane % 16][k + lane / 16].
+template <int NB>
+__global__ __launch_bounds__(256) void newton_few_gram_kernel(Few f) {
+  constexpr int NT = NB * (NB + 1) / 2;
+  __shared__ double sums[3][NT][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
+  const int64_t g = blockIdx.x / f.chunks;
+  const int c = (int)(blockIdx.x - g * f.chunks);
+  const int64_t base = (f.u.g0 + g) * f.s * f.l;
+  f64x4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = f64x4{0, 0, 0, 0};
+  const int k1 = min(f.l, (c + 1) * f.chunk), per = f.chunk / 4;
+  const int w0 = c * f.chunk + wave * per, w1 = min(k1, w0 + per);
+  for (int k0 = w0; k0 < w1; k0 += 16) {
+    float x[4][NB], m[4][NB];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        // rows are contiguous along k, or (tall) along the rows of X: a lane's four k, or 16 lanes' rows
+        const int r = 16 * i + i16, k = f.tall ? k0 + 4 * e + q : k0 + 4 * q + e;
+        const bool in = r < f.s && k < w1;
+        const int64_t at = base + (f.tall ? (int64_t)k * f.s + r : (int64_t)r * f.l + k);
+        x[e][i] = in ? f.u.g[at] : 0.f;
+        m[e][i] = in && f.u.mom ? f.u.mom[at] : 0.f;
+      }
+    if (f.u.mom) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int r = 16 * i + i16, k = f.tall ? k0 + 4 * e + q : k0 + 4 * q + e;
+          m[e][i] = fmaf(f.u.momentum, m[e][i], x[e][i]);
+          if (r < f.s && k < w1) f.u.mom[base + (f.tall ? (int64_t)k * f.s + r : (int64_t)r * f.l + k)] = m[e][i];
+          x[e][i] = direction(f.u, x[e][i], m[e][i]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      int t = 0;
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i <= j; ++i, ++t) acc[t] = mfma64((double)x[e][i], (double)x[e][j], acc[t]);
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[wave - 1][t][r][lane] = acc[t][r];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  double* const out = f.parts + (int64_t)blockIdx.x * NT * 256 + lane;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      out[t * 256 + r * 64] = (acc[t][r] + sums[0][t][r][lane]) + (sums[1][t][r][lane] + sums[2][t][r][lane]);
+}
+
+struct FewCoef { int steps; float c[16][3]; };
+
+// The iteration on [16 NB, 16 NB], one block for each matrix: the tiles of a product shared out to the waves (up to
+// four on a SIMD, to overlap their chains: 8 [64, 64] 72 us with one, 64 with four), mirrored when they are
+// written.
+template <int NB>
+struct FewWaves { static constexpr int N = NB == 1 ? 2 : NB == 2 ? 4 : 16; };
+template <int NB>
+__global__ __launch_bounds__(64 * FewWaves<NB>::N) void newton_few_steps_kernel(Few f, FewCoef coef) {
+  constexpr int N = 16 * NB, NT = NB * (NB + 1) / 2, W = N + kFewPitch, NW = FewWaves<NB>::N, TW = (2 * NT + NW - 1) / NW;
+  __shared__ double A[N * W], B[N * W], T[N * W], P[N * W];
+  __shared__ double trace;
+  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t g = blockIdx.x;
+  struct Tile { int i, j; };
+  auto tile = [](int t) {   // column by column
+    const int j = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
+    return Tile{t - j * (j + 1) / 2, j};
+  };
+  auto product = [&](const double* x, const double* y, Tile t) {   // symmetric ones: both operands by rows
+    f64x4 s = {0, 0, 0, 0};
+    const double* const xr = x + (16 * t.i + i16) * W + q;
+    const double* const yr = y + (16 * t.j + i16) * W + q;
+#pragma unroll
+    for (int k = 0; k < N; k += 4) s = mfma64(xr[k], yr[k], s);
+    return s;
+  };
+  auto store = [&](double* z, Tile t, const f64x4& v) {
+    const int col = 16 * t.j + i16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * t.i + 4 * r + q;
+      if (row > col) continue;          // a diagonal tile's lower half mirrors its upper one
+      z[row * W + col] = v[r];
+      z[col * W + row] = v[r];
+    }
+  };
+  const double* const parts = f.parts + g * f.chunks * NT * 256 + lane;
+  for (int t = wave; t < NT; t += NW) {
+    f64x4 v = {0, 0, 0, 0};
+    for (int c0 = 0; c0 < f.chunks; c0 += 8) {   // eight at a time, the last ones, too: each wait is a trip to memory
+      double x[8][4];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          x[u][r] = parts[((int64_t)min(c0 + u, f.chunks - 1) * NT + t) * 256 + r * 64];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += c0 + u < f.chunks ? x[u][r] : 0.0;
+    }
+    store(A, tile(t), v);
+  }
+  __syncthreads();
+  if (wave == 0) {
+    double d = lane < N ? A[lane * W + lane] : 0.0;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) d += __shfl_xor(d, o, kWave);
+    if (lane == 0) trace = d;
+  }
+  __syncthreads();
+  const double total = trace;
+  // zeros stay zeros; an infinity or NaN makes the whole matrix NaN
+  const double inv = total == 0.0 ? 0.0 : total < (double)INFINITY ? 1.0 / total : (double)NAN;
+  for (int e = tid; e < N * N; e += 64 * NW) A[e / N * W + e % N] *= inv;
+  __syncthreads();
+  for (int k = 0; k < coef.steps; ++k) {
+    const double a = coef.c[k][0], b = coef.c[k][1], c = coef.c[k][2];
+    for (int t = wave; t < NT; t += NW) {
+      const Tile at = tile(t);
+      f64x4 s = product(A, A, at);
+      const int col = 16 * at.j + i16;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * at.i + 4 * r + q;
+        s[r] = (row == col ? a : 0.0) + b * A[row * W + col] + c * s[r];
+      }
+      store(B, at, s);
+      if (k == 0) store(P, at, s);
+    }
+    __syncthreads();
+    // B A and P B, which waits in registers until P is read
+    const bool last = k + 1 == coef.steps;
+    f64x4 next[TW];
+#pragma unroll
+    for (int n = 0; n < TW; ++n) {
+      const int t = wave + n * NW;
+      if (t < NT && !last) store(T, tile(t), product(B, A, tile(t)));
+      if (t >= NT && t < 2 * NT && k > 0) next[n] = product(P, B, tile(t - NT));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < TW; ++n) {
+      const int t = wave + n * NW;
+      if (t >= NT && t < 2 * NT && k > 0) store(P, tile(t - NT), next[n]);
+    }
+    if (!last)
+      for (int t = wave; t < NT; t += NW) store(A, tile(t), product(T, B, tile(t)));
+    __syncthreads();
+  }
+  const double scale = sqrt(inv);
+  for (int e = tid; e < N * N; e += 64 * NW) f.poly[g * N * N + e] = P[e / N * W + e % N] * scale;
+}
+
+// Result P U, 16 columns to a wave at a time.  The order of the operands is that of the result in memory.
+template <int NB, int KIND>
+__global__ __launch_bounds__(256) void newton_few_apply_kernel(Few f, Product p, int blocks) {
+  constexpr int N = 16 * NB, W = N + kFewPitch;
+  __shared__ double P[N * W];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, q = lane >> 4;
+  const int64_t g = blockIdx.x / blocks, base = (f.u.g0 + g) * f.s * f.l;
+  for (int e = tid; e < N * N; e += 256) P[e / N * W + e % N] = f.poly[g * N * N + e];
+  __syncthreads();
+  UpdateScale scale = {};
+  if constexpr (KIND == kUpdate) scale = update_scale(p);
+  const bool grad = !f.u.mom || f.u.nesterov;
+  for (int64_t n0 = ((blockIdx.x - g * blocks) * 4 + wave) * 16; n0 < f.l; n0 += (int64_t)blocks * 64) {
+    const int64_t n = n0 + i16;
+    f64x4 acc[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) acc[i] = f64x4{0, 0, 0, 0};
+    float x[4 * NB];
+#pragma unroll
+    for (int e = 0; e < 4 * NB; ++e) {
+      const int k = f.tall ? e / 4 * 16 + 4 * q + e % 4 : 4 * e + q;
+      const bool in = k < f.s && n < f.l;
+      const int64_t at = base + (f.tall ? n * f.s + k : k * (int64_t)f.l + n);
+      float u = in && grad ? f.u.g[at] : 0.f;
+      if (f.u.mom) u = direction(f.u, u, in ? f.u.mom[at] : 0.f);
+      x[e] = u;
+    }
+#pragma unroll
+    for (int e = 0; e < 4 * NB; ++e) {
+      const int k = f.tall ? e / 4 * 16 + 4 * q + e % 4 : 4 * e + q;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const double pe = P[(16 * i + i16) * W + k], xe = x[e];
+        acc[i] = f.tall ? mfma64(xe, pe, acc[i]) : mfma64(pe, xe, acc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // tall: rows of the result are columns of X
+        const int64_t row = f.tall ? n0 + 4 * r + q : 16 * i + 4 * r + q, col = f.tall ? 16 * i + i16 : n;
+        if (row >= p.R || col >= p.C) continue;
+        const int64_t at = ((p.g0 + g) * p.R + row) * p.C + col;
+        const float v = (float)acc[i][r];
+        if constexpr (KIND == kOut) {
+          if (p.bf16) static_cast<uint16_t*>(p.out)[at] = (uint16_t)f32_to_bf16(v);
+          else static_cast<float*>(p.out)[at] = v;
+        } else {
+          const float m = scale.keep * p.master[at] - scale.gain * v;
+          p.master[at] = m;
+          if (p.w) p.w[at] = (uint16_t)f32_to_bf16(m);
+        }
+      }
+  }
+}
+
 // ---------------------------------------------------------------------- host
 
 // Up to so many 64 x 64 tiles a product takes small tiles (for X, which then is kept with its transpose: whole
@@ -834,6 +1092,48 @@ bool keeps_low(const NewtonCall& c, int k) {
   return grow > kDropLow;
 }
 
+// What the last launch of a call writes.
+void results(const NewtonCall& c, Product& q) {
+  q.tall = c.p.tall; q.bf16 = c.bf16;
+  q.R = c.p.R; q.C = c.p.C;
+  q.out = c.out; q.master = c.master; q.w = c.w;
+  q.lr_dev = c.lr_dev; q.lr = c.lr; q.weight_decay = c.weight_decay; q.scale = c.scale;
+}
+
+bool few_steps(const NewtonCall& c) {
+  double grow = 1.0;
+  for (int k = 0; k < c.steps; ++k) grow *= fmax(1.0, fabs((double)c.coef[k][0]));
+  return c.p.few && grow <= kFewGrow;
+}
+
+template <int NB>
+hipError_t launch_few(const NewtonCall& c, Source u, hipStream_t st) {
+  const NewtonPlan& p = c.p;
+  Few f{};
+  f.tall = p.tall;
+  f.s = p.s; f.l = p.l; f.chunk = p.chunk; f.chunks = p.chunks;
+  f.parts = static_cast<double*>(c.ws);
+  f.poly = f.parts + (int64_t)p.few_batch * p.chunks * (NB * (NB + 1) / 2) * 256;
+  FewCoef coef;
+  coef.steps = c.steps;
+  for (int k = 0; k < c.steps; ++k)
+    for (int i = 0; i < 3; ++i) coef.c[k][i] = c.coef[k][i];
+  Product q{};
+  results(c, q);
+  for (int g0 = 0; g0 < p.G; g0 += p.few_batch) {
+    const int batch = p.G - g0 < p.few_batch ? p.G - g0 : p.few_batch;
+    const int64_t want = (p.l + 63) / 64, most = 1024 / batch + 1;   // about four blocks of 64 columns to a CU
+    const int blocks = (int)(want < most ? want : most);
+    u.g0 = q.g0 = g0;
+    f.u = u;
+    newton_few_gram_kernel<NB><<<batch * p.chunks, 256, 0, st>>>(f);
+    newton_few_steps_kernel<NB><<<batch, 64 * FewWaves<NB>::N, 0, st>>>(f, coef);
+    if (c.out) newton_few_apply_kernel<NB, kOut><<<batch * blocks, 256, 0, st>>>(f, q, blocks);
+    else newton_few_apply_kernel<NB, kUpdate><<<batch * blocks, 256, 0, st>>>(f, q, blocks);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
 NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
@@ -872,6 +1172,22 @@ NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
   p.bh = take(a);
   p.al = take(p.exact ? a : 0);
   p.bl = take(p.exact ? a : 0);
+  // On the rows alone: 56 to 248 us without, 13 to 20 with (1 [8, 8], 1 [12, 14336]); 64 [48, 14336] 751 (bf16) and
+  // 1076 (f32), 268 and 280.  Products of 64 rows in 64 bits take 50 us: 8 [64, 500] 57 and 66, 68; 1 [64, 2000]
+  // 70 and 84, 74; 64 [64, 3000] 180 and 230, 162.
+  p.few = p.s <= 48 || (p.s <= 64 && p.l >= 2048);
+  if (p.few) {
+    p.few_batch = G < kNewtonFewBatch ? G : kNewtonFewBatch;
+    // a chunk costs its length (18 ns a column for 64 rows) and its sums' reading (0.13 us): about sqrt(l) / 3
+    const int nb = (p.s + 15) / 16;
+    int64_t chunks = (int64_t)(0.375 * sqrt((double)p.l)) + 1;
+    if (chunks > 1024 / p.few_batch + 1) chunks = 1024 / p.few_batch + 1;
+    p.chunk = up((int)((p.l + chunks - 1) / chunks), 64);
+    p.chunks = (p.l + p.chunk - 1) / p.chunk;
+    const size_t each = (size_t)p.chunks * (nb * (nb + 1) / 2) * 256 + (size_t)nb * nb * 256;
+    const size_t need = (size_t)p.few_batch * each * sizeof(double);
+    if (off < need) off = (need + 255) / 256 * 256;
+  }
   p.total = off;
   return p;
 }
@@ -881,6 +1197,19 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
   auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(static_cast<char*>(c.ws) + off); };
   uint16_t *const ah = at(p.ah), *const al = at(p.al), *const bh = at(p.bh), *const bl = at(p.bl);
   const int64_t n = (int64_t)p.R * p.C;
+  if (few_steps(c)) {
+    Source s{};
+    s.g = c.g;
+    s.mom = c.mom;
+    s.momentum = c.momentum;
+    s.nesterov = c.nesterov;
+    switch ((p.s + 15) / 16) {
+      case 1: return launch_few<1>(c, s, st);
+      case 2: return launch_few<2>(c, s, st);
+      case 3: return launch_few<3>(c, s, st);
+      default: return launch_few<4>(c, s, st);
+    }
+  }
   for (int g0 = 0; g0 < p.G; g0 += p.batch) {
     const int batch = p.G - g0 < p.batch ? p.G - g0 : p.batch;
     Source s{};
@@ -937,10 +1266,8 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
         q.ldt = p.sp;
         e = add ? product<kAdd>(q, p, batch, st) : product<kStep>(q, p, batch, st);
       } else {
-        q.tall = p.tall; q.bf16 = c.bf16;
-        q.R = p.R; q.C = p.C; q.g0 = g0;
-        q.out = c.out; q.master = c.master; q.w = c.w;
-        q.lr_dev = c.lr_dev; q.lr = c.lr; q.weight_decay = c.weight_decay; q.scale = c.scale;
+        results(c, q);
+        q.g0 = g0;
         e = c.out ? product<kOut>(q, p, batch, st) : product<kUpdate>(q, p, batch, st);
       }
       if (e != hipSuccess) return e;

@@ -15,6 +15,7 @@ constexpr int kNewtonPad = 64;       // of both sides of a stored matrix: whole 
 // Fewer rows (or columns) than this take factors of two parts whatever the type: their roundings do
 // not average out (up to 4e-3 of the norm), and the call's time is that of its launches.
 constexpr int kNewtonFewRows = 32;
+constexpr int kNewtonFewBatch = 2048;   // matrices of few rows worked on at a time: at most 60 MB of workspace
 constexpr int kNormParts = 256;      // partial sums of a matrix's squares
 
 // Sizes of one call.  A matrix is worked on as X [s, l] with s <= l (the
@@ -25,6 +26,9 @@ struct NewtonPlan {
   int s, l, sp, lp;
   bool exact;          // factors of two fp16 parts (22 bits)
   bool small;          // small tiles for X, which is kept with its transpose
+  bool few;            // few rows: the iteration on [s, s] where its coefficients allow that
+  int few_batch;       // matrices at a time, then
+  int chunk, chunks;   // and in the first pass: columns of a block, blocks of a matrix
   int batch;           // matrices worked on at a time
   // workspace sections (byte offsets)
   size_t parts, xh[2], xl[2], th[2], tl[2], ah, al, bh, bl, total;

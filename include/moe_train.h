@@ -80,7 +80,9 @@ size_t moe_muon_workspace_bytes(int G, int R, int C, int dtype);
  * bits as long as later steps would enlarge its roundings: the result is off by
  * 1e-3 to 3e-3 of its norm, low ranks included (before its rounding to bf16).
  * MOE_F32, and matrices with fewer than 32 rows or columns: factors of 22 bits, as
- * exact as f32 arithmetic.
+ * exact as f32 arithmetic.  Up to 48 rows or columns (64 if the other side has 2048 or more),
+ * where the magnitudes above 1 of the steps' a multiply to at most 4096: 64 bits
+ * up to the result.
  * Any G from 1 to 2^30 and R, C from 1 to 2^20 with R*C <= 2^32 and G*R*C <= 2^39.  No step but
  * the last may leave a singular value above 15 (the range of fp16; such a matrix becomes
  * infinite or NaN).  A matrix of zeros gives zeros; an infinity or NaN makes its own matrix

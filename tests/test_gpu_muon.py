@@ -87,6 +87,74 @@ def test_orthogonalize_with_products_of_different_tiles(G, R, C, dtype):
         _check(got[g], x[g], dtype, what=f"matrix {g}")
 
 
+COEF32 = tuple(tuple(float(np.float32(v)) for v in abc) for abc in TO.COEF)   # as the kernels hold them
+
+
+def _check_few(got, x, dtype, coef=COEF32, what=""):
+    """In 64 bits up to the result: half a step of it, and of float32 on the way to bf16."""
+    ref = TO.newton(x, coef)
+    step = 2.0 ** -24 + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -26)     # eps / 2 of 8 and of 24 bits
+    assert np.linalg.norm(got - ref) <= step * np.linalg.norm(ref), (what, np.linalg.norm(got - ref) / np.linalg.norm(ref))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,R,C", [(1, 1, 1), (2, 1, 9), (3, 15, 17), (2, 16, 4001), (2, 4001, 17), (3, 33, 31), (5, 32, 64),
+                                   (2, 48, 129), (3, 1000, 47), (2, 64, 2048), (1, 2111, 49), (1030, 40, 20), (4100, 3, 5)])
+def test_few_rows_are_as_exact_as_the_result(G, R, C, dtype):
+    print(f"case few rows G={G} R={R} C={C} {dtype}", flush=True)
+    x = _grad(G, R, C, G + R + C)
+    got = _ortho(x, dtype, COEF32)
+    for g in {0, G // 2, G - 1}:
+        _check_few(got[g], x[g], dtype, what=f"matrix {g}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_few_rows_of_low_rank_and_of_other_iterations(dtype):
+    """Null directions under coefficients that make them up to 4096 times larger; zeros, infinities and scales; and
+    more steps than the form for few rows takes, which are worked on like larger matrices."""
+    g = np.random.default_rng(4)
+    for R, C in ((20, 300), (300, 41)):
+        x = np.stack([(g.standard_normal((R, r)) @ g.standard_normal((r, C))).astype(np.float32) for r in (1, 4, 16)])
+        for coef in (COEF32, ((1.5, -0.5, 0.0),) * 16, ((1.875, -1.25, 0.375),) * 13, ((32.0, -30.0, 0.0), (32.0, 0.0, 0.0), (4.0, 1.0, 0.5))):
+            got = _ortho(x, dtype, coef)
+            for i in range(3):
+                _check_few(got[i], x[i], dtype, coef, what=str(coef))
+        for e in (-140, 100):
+            y = np.ldexp(np.sign(x), e).astype(np.float32)
+            assert np.array_equal(_ortho(y, dtype), _ortho(np.sign(x), dtype))
+        bad = x.copy()
+        bad[0], bad[1, 3, 4] = 0, -np.inf
+        got = _ortho(bad, dtype, COEF32)
+        assert (got[0] == 0).all() and np.isnan(got[1]).all()
+        _check_few(got[2], x[2], dtype)
+        long = TO.COEF[:1] * 6 + ((1.5, -0.5, 0.0),) * 4       # 3.44^6 1.5^4 = 8455
+        got = _ortho(x, dtype, long)
+        for i in range(3):
+            _check(got[i], x[i], dtype, long)
+
+
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,R,C", [(3, 45, 500), (2, 1201, 37), (1, 64, 2100), (1, 2500, 50), (2060, 9, 6)])
+def test_muon_steps_of_few_rows(G, R, C, dtype, nesterov):
+    """mom: two roundings a step.  master: three, and lr scale times half a step of the update.  The direction
+    is rounded twice (grad + momentum mom by one fma, of mom's own): 2^-23 of its norm, which the iteration makes larger by
+    at most 485 / 1 of null directions; its part there is below that of 485 2^-23."""
+    print(f"case muon of few rows G={G} R={R} C={C} {dtype} nesterov={nesterov}", flush=True)
+    grads, mom0, w0, mom, master, w = _muon(G, R, C, dtype, nesterov)
+    for g in sorted({0, G // 2, G - 1}):
+        m, x = mom0[g:g + 1].astype(np.float64), w0[g:g + 1].astype(np.float64)
+        allowed, big = 0.0, np.abs(mom0[g]) + sum(np.abs(gr[g]) for gr in grads)
+        for gr in grads:
+            m, x, o = TO.muon(gr[g:g + 1], m, x, **HYPER, nesterov=nesterov)
+            allowed += HYPER["lr"] * HYPER["scale"] * (2.0 ** -23 * np.linalg.norm(o) + 485 * 2.0 ** -23)
+            allowed += 3 * 2.0 ** -24 * np.linalg.norm(x)
+        assert np.all(np.abs(host(mom[g]).astype(np.float64) - m[0]) <= 4 * 2.0 ** -24 * big)
+        assert np.linalg.norm(host(master[g]).astype(np.float64) - x[0]) <= allowed
+    if w is not None:
+        assert torch.equal(w, master.to(torch.bfloat16))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_low_rank(dtype):
     """Gradients of experts with few tokens: null directions must not gather roundings."""

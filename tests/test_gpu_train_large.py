@@ -81,3 +81,28 @@ def test_stack_of_many_elements(dtype):
         # bf16: the result's rounding and the factors' (1e-3 to 3e-3); float32: chains of 2^16 sums of 16 products with
         # half a step each, in five steps that each enlarge it at most 4-fold in sum
         assert off <= (2.0 ** -9 + 3e-3 if dtype == "bf16" else 5 * 4 * (1 << 16) ** 0.5 * EPS), (i, off)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_stack_of_many_elements_and_rows(dtype):
+    """2.3e9 elements of matrices with more rows."""
+    _room(80)
+    G, R, C = 17, 130, 1 << 20
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    g = torch.randn(G, R, C, generator=gen, device="cuda")
+    assert g.numel() > 2 ** 31
+    dt, code = (torch.bfloat16, M.BF16) if dtype == "bf16" else (torch.float32, M.F32)
+    out = torch.empty(G, R, C, dtype=dt, device="cuda")
+    ws = torch.empty(M.moe_muon_workspace_bytes(G, R, C, code), dtype=torch.uint8, device="cuda")
+    print(f"case orthogonalize G={G} R={R} C={C} {dtype}", flush=True)
+    M.moe_orthogonalize(G, R, C, g, out, ws)
+    torch.cuda.synchronize()
+    for i in (0, G - 1):
+        x = g[i].double()
+        x /= x.square().sum().sqrt()
+        for a, b, c in TO.COEF:
+            gram = x @ x.T.contiguous()
+            x = a * x + (b * gram + c * gram @ gram) @ x
+        off = float((out[i].double() - x).norm() / x.norm())
+        # as above
+        assert off <= (2.0 ** -9 + 3e-3 if dtype == "bf16" else 5 * 4 * (1 << 16) ** 0.5 * EPS), (i, off)
