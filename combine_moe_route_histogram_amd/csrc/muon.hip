@@ -31,7 +31,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kXScale = 1024.f;   // of stored X
-constexpr float kAScale = 256.f;    // of stored A and B
+constexpr float kAScale = 256.f;    // of stored A and B (of the last step's B: see last_scale)
 
 // kAdd: kStep that adds a times the lower part of X
 enum NewtonKind { kGram, kPoly, kStep, kAdd, kOut, kUpdate };
@@ -50,6 +50,7 @@ struct Product {
   int ldo, ldt;             // of ch, cl, oh, ol; of th, tl
   float a, b, c;
   // kOut, kUpdate
+  float undo;               // of the scales of B and X
   bool tall, bf16;
   int R, C, g0;
   void* out;
@@ -163,7 +164,7 @@ __device__ __forceinline__ void finish4(const Product& p, int m, int n, const fl
       v[e] = p.b * x[e] + p.c * (s[e] * (1.f / kAScale)) + (m == n + e ? p.a * kAScale : 0.f);
     else if constexpr (KIND == kAdd) v[e] = p.a * x[e] + s[e] * (1.f / kAScale);
     else if constexpr (KIND == kStep) v[e] = s[e] * (1.f / kAScale);
-    else v[e] = s[e] * (1.f / (kAScale * kXScale));
+    else v[e] = s[e] * p.undo;
   }
 }
 
@@ -1092,6 +1093,32 @@ bool keeps_low(const NewtonCall& c, int k) {
   return grow > kDropLow;
 }
 
+// The power of two that the last step's B is stored by, on top of kAScale.  A step before the last leaves singular
+// values of at most 15, so its |B| = |a + b s^2 + c s^4| is at most 15 / s where s is large, and below fp16's 255
+// where s is not (coefficients are at most 32: s < 1.4).  The last step may leave any value, and its B be up to
+// 32 (1 + 15^2 + 15^4).  The largest s that can enter it follows from the coefficients (1 at the start, then the
+// extremes of a s + b s^3 + c s^5), and from that the largest |B|, which takes half of fp16's range: a sum that its
+// roundings enlarge still fits.  1 where |B| stays within 128, as in every iteration that tends to 1.
+float last_scale(const NewtonCall& c) {
+  double s = 1.0;
+  for (int k = 0; k + 1 < c.steps; ++k) {
+    const double a = c.coef[k][0], b = c.coef[k][1], q = c.coef[k][2];
+    const double h = -0.5 * (3.0 * b + copysign(sqrt(fmax(0.0, 9.0 * b * b - 20.0 * a * q)), b));
+    double most = 0.0;
+    for (const double t : {s * s, h / (5.0 * q), a / h})   // s^2: the end, and where a + 3 b t + 5 q t^2 = 0
+      if (t > 0.0 && t <= s * s) most = fmax(most, fabs(a + t * (b + t * q)) * sqrt(t));
+    s = fmin(15.0, most);
+  }
+  const float* const f = c.coef[c.steps - 1];
+  const double a = f[0], b = f[1], q = f[2];
+  double most = fabs(a);
+  for (const double t : {s * s, -b / (2.0 * q)})
+    if (t > 0.0 && t <= s * s) most = fmax(most, fabs(a + t * (b + t * q)));
+  float scale = 1.f;
+  while (most * kAScale * scale > 32768.0) scale *= 0.5f;
+  return scale;
+}
+
 // What the last launch of a call writes.
 void results(const NewtonCall& c, Product& q) {
   q.tall = c.p.tall; q.bf16 = c.bf16;
@@ -1210,6 +1237,7 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
       default: return launch_few<4>(c, s, st);
     }
   }
+  const float last_b = last_scale(c);
   for (int g0 = 0; g0 < p.G; g0 += p.batch) {
     const int batch = p.G - g0 < p.batch ? p.G - g0 : p.batch;
     Source s{};
@@ -1234,8 +1262,8 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
       const int64_t x_mat = (int64_t)p.sp * p.lp, a_mat = (int64_t)p.sp * p.sp;
       const bool last = k + 1 == c.steps, add = !p.exact && keeps_low(c, k);
       Product q{};
-      q.b = c.coef[k][1]; q.c = c.coef[k][2];
-      q.a = c.coef[k][0];
+      const float bs = last ? last_b : 1.f;   // of the stored B
+      q.a = c.coef[k][0] * bs; q.b = c.coef[k][1] * bs; q.c = c.coef[k][2] * bs;
       q.ah = xh; q.al = xl; q.bh = xh; q.bl = xl;
       q.a_mat = q.b_mat = x_mat;
       q.lda = q.ldb = q.k_len = p.lp;
@@ -1267,6 +1295,7 @@ hipError_t launch_newton(const NewtonCall& c, hipStream_t st) {
         e = add ? product<kAdd>(q, p, batch, st) : product<kStep>(q, p, batch, st);
       } else {
         results(c, q);
+        q.undo = 1.f / (kAScale * kXScale * bs);
         q.g0 = g0;
         e = c.out ? product<kOut>(q, p, batch, st) : product<kUpdate>(q, p, batch, st);
       }

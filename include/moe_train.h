@@ -85,7 +85,7 @@ size_t moe_muon_workspace_bytes(int G, int R, int C, int dtype);
  * up to the result.
  * Any G from 1 to 2^30 and R, C from 1 to 2^20 with R*C <= 2^32 and G*R*C <= 2^39.  No step but
  * the last may leave a singular value above 15 (the range of fp16; such a matrix becomes
- * infinite or NaN).  A matrix of zeros gives zeros; an infinity or NaN makes its own matrix
+ * infinite or NaN); the last may leave any.  A matrix of zeros gives zeros; an infinity or NaN makes its own matrix
  * NaN and no other.  The scale of a matrix has no effect, down to subnormal entries.  A
  * matrix's bits depend on its values and on G, R and C, not on the other matrices. */
 int moe_orthogonalize(int G, int R, int C, int dtype, const moe_newton* n, const float* g, void* out,

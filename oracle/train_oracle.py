@@ -99,7 +99,8 @@ def newton_model(u, exact, coef=COEF):
     """The iteration as the products round it.  X has two fp16 parts, of which the lower one is dropped from
     the step on whose |a|, with those of the later steps, make at most 12 (never in the exact form, always
     for the last step otherwise).  a is part of B's diagonal; a times the lower part is added.  Factors have one
-    part (exact: two)."""
+    part (exact: two).  A and B are stored times 256, the last step's B, which may be of any size, times a power of two
+    that keeps it inside fp16."""
     x = np.asarray(u, np.float64)
     tall = x.shape[0] > x.shape[1]
     if tall:
@@ -118,7 +119,10 @@ def newton_model(u, exact, coef=COEF):
         A = _parts(mul(xs, (xs[0].T, xs[1].T)), 256)
         whole = A[0] + A[1] if exact else A[0]
         B = f(b) * whole + f(c) * mul(A, A) + f(a) * np.eye(len(A[0]), dtype=f)
-        x = mul(_parts(B, 256), xs)
+        scale = 256.0
+        while k + 1 == len(coef) and np.isfinite(B).all() and np.abs(B).max() * scale > 32768:
+            scale /= 2
+        x = mul(_parts(B, scale), xs)
         if low and not exact:
             x = f(a) * xs[1] + x
     return x.T if tall else x

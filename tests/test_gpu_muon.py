@@ -369,3 +369,63 @@ def test_a_training_step_of_a_layer(dtype):
     for n in ("w1", "w3", "w2"):
         kept = old[n][5].double() * (1 - 0.01 * 0.5) ** 2
         assert torch.allclose(m.master[n][5].double(), kept, rtol=4 * 2.0 ** -24, atol=0)
+
+
+def _large_last_step(G, R, C, seed):
+    """One row that is not zero, rank one, full rank, in turn."""
+    g = np.random.default_rng(seed)
+    x = g.standard_normal((G, R, C)).astype(np.float32)
+    for i in range(0, G, 3):
+        x[i] = 0
+        x[i, R // 3] = g.standard_normal(C)
+        if i + 1 < G:
+            x[i + 1] = np.outer(g.standard_normal(R), g.standard_normal(C))
+    return x
+
+
+def _check_result(got, x, dtype, coef, what):
+    """As _check, with half a step of a result in bf16 (2^-8) for each element."""
+    ref, model = TO.newton(x, coef), TO.newton_model(x, _exact(x, dtype), coef)
+    rounding = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -20
+    allowed = 2 * np.linalg.norm(model - ref) + rounding * np.linalg.norm(ref)
+    assert np.linalg.norm(got - ref) <= allowed, (what, np.linalg.norm(got - ref), allowed)
+
+
+LARGE_LAST = (((2.0, 0.0, 0.0), (1.0, 0.0, 20.0)), ((15.0, 0.0, 0.0), TO.COEF[0]), ((15.0, 0.0, 0.0), (32.0, 32.0, 32.0)),
+              ((15.0, 0.0, 0.0), (-32.0, 32.0, -32.0)), ((3.0, -1.0, 0.0), (4.0, 0.75, 0.0), (2.0, 32.0, 32.0)), ((32.0, 32.0, 32.0),))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,R,C", [(3, 90, 150), (3, 150, 90), (40, 520, 264)])
+def test_last_step_may_leave_any_singular_value(G, R, C, dtype):
+    """Steps that leave singular values of 2 to 15, and last ones whose B = a + b s^2 + c s^4 is 321 to 1.6e6: beyond what
+    fp16 holds at the scale of the other steps' B.  Small and large tiles, both orientations."""
+    print(f"case large last step G={G} R={R} C={C} {dtype}", flush=True)
+    x = _large_last_step(G, R, C, R)
+    for coef in LARGE_LAST:
+        got = _ortho(x, dtype, coef)
+        assert np.isfinite(got).all(), coef
+        for g in range(3):
+            _check_result(got[g], x[g], dtype, coef, f"matrix {g} of {coef}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_update_by_a_last_step_that_leaves_large_singular_values(dtype):
+    """As above, into the weights: master is off by lr scale times the update's error (bounded as in _check_result, without the
+    result's rounding) and three roundings of its own."""
+    G, R, C = 3, 90, 150
+    x, coef = _large_last_step(G, R, C, 5), LARGE_LAST[1]
+    w0 = (0.02 * np.random.default_rng(6).standard_normal((G, R, C))).astype(np.float32)
+    mom, master, ws = torch.zeros(G, R, C, device="cuda"), _dev(w0), _ws(G, R, C, dtype)
+    w = torch.empty(G, R, C, dtype=torch.bfloat16, device="cuda") if dtype == "bf16" else None
+    hyper = dict(lr=1e-4, momentum=0.0, weight_decay=0.1, scale=1.0)
+    M.moe_muon(G, R, C, _dev(x), mom, master, w, ws, nesterov=False, coef=coef, **hyper)
+    torch.cuda.synchronize()
+    assert torch.isfinite(master).all()
+    _, want, o = TO.muon(x, np.zeros_like(x), w0, nesterov=False, coef=coef, **hyper)
+    for g in range(G):
+        off = np.linalg.norm(TO.newton_model(x[g], dtype == "f32", coef) - o[g])
+        allowed = 1e-4 * (2 * off + 2.0 ** -20 * np.linalg.norm(o[g])) + 3 * 2.0 ** -24 * np.linalg.norm(want[g])
+        assert np.linalg.norm(host(master[g]).astype(np.float64) - want[g]) <= allowed, g
+    if w is not None:
+        assert torch.equal(w, master.to(torch.bfloat16))
