@@ -1048,15 +1048,17 @@ double mid_rounds(int64_t tiles) { return tiles <= 256 ? 0.75 : 1.25 * rounds(ti
 // Tiles by their number.  A and B of 1 [1024, 8192] (us; 256 x 256, 128 x 128 and small tiles): 405, 213, 60 and
 // 66, 34, 15 (f32); of 20 [300, 2000] 38, 23, 16 and 15, 9, 8; of 4 [1000, 1000] 26, 15, 17; of 6 [1100, 1100] 30, 21,
 // 28; of 1 [4096, 4096] the whole call 1476 with 256 x 256, 1800 with 128 x 128.  X of 8 [512, 1024] 17, 10, 16; of
-// 20 [300, 2000] 28, 20, 39; of 3 [700, 5000] f32 56, 60, 113.
+// 20 [300, 2000] 28, 20, 39; of 3 [700, 5000] f32 56, 60, 113.  By those of `part` matrices, a whole part of the
+// stack, also where the last part holds fewer: small tiles sum in another order, and a matrix's bits may not depend
+// on its place in the stack.
 template <int KIND, bool EXACT>
-hipError_t product(const Product& p, bool small, int batch, hipStream_t st) {
+hipError_t product(const Product& p, bool small, int part, int batch, hipStream_t st) {
   constexpr bool kMn = KIND != kGram && KIND != kPoly;
   using Big = NsCfg<256, 256, 2, 4, 64, 2, kMn>;
   using Mid = NsCfg<128, 128, 2, 2, 64, 2, kMn>;
   auto tiles = [&](int t) {
     const int64_t mt = (p.m_len + t - 1) / t, nt = (p.n_len + t - 1) / t;
-    return batch * (kMn ? mt * nt : mt * (mt + 1) / 2);
+    return part * (kMn ? mt * nt : mt * (mt + 1) / 2);
   };
   if (!kMn) small = tiles(64) <= kSmallTiles;   // both operands lie along k in any case
   // 32 x 32 tiles until there are two for each CU: whole calls of [512, 512] 95 us with them and 148
@@ -1075,9 +1077,9 @@ hipError_t product(const Product& p, bool small, int batch, hipStream_t st) {
 template <int KIND>
 hipError_t product(const Product& q, const NewtonPlan& p, int batch, hipStream_t st) {
   if constexpr (KIND != kAdd) {   // the exact form has a in B's diagonal
-    if (p.exact) return product<KIND, true>(q, p.small, batch, st);
+    if (p.exact) return product<KIND, true>(q, p.small, p.batch, batch, st);
   }
-  return product<KIND, false>(q, p.small, batch, st);
+  return product<KIND, false>(q, p.small, p.batch, batch, st);
 }
 
 // Whether X keeps its lower part for step k: a rounding of X (2^-12 of an element) has null

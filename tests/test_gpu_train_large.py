@@ -106,3 +106,21 @@ def test_stack_of_many_elements_and_rows(dtype):
         off = float((out[i].double() - x).norm() / x.norm())
         # as above
         assert off <= (2.0 ** -9 + 3e-3 if dtype == "bf16" else 5 * 4 * (1 << 16) ** 0.5 * EPS), (i, off)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bits_do_not_depend_on_the_place_in_the_stack(dtype):
+    """9 matrices are worked on as 5 and 4, whose numbers of tiles lie on either side of where the products
+    change to smaller ones: the first matrix once more as the last one gives the same bits."""
+    _room(40)
+    G, R, C = 9, 960, 1 << 17
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    g = torch.randn(G, R, C, generator=gen, device="cuda")
+    g[G - 1] = g[0]
+    dt, code = (torch.bfloat16, M.BF16) if dtype == "bf16" else (torch.float32, M.F32)
+    out = torch.empty(G, R, C, dtype=dt, device="cuda")
+    ws = torch.empty(M.moe_muon_workspace_bytes(G, R, C, code), dtype=torch.uint8, device="cuda")
+    print(f"case orthogonalize G={G} R={R} C={C} {dtype}", flush=True)
+    M.moe_orthogonalize(G, R, C, g, out, ws)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out[0]).all() and torch.equal(out[0], out[G - 1])
