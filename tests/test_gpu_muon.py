@@ -429,3 +429,38 @@ def test_update_by_a_last_step_that_leaves_large_singular_values(dtype):
         assert np.linalg.norm(host(master[g]).astype(np.float64) - want[g]) <= allowed, g
     if w is not None:
         assert torch.equal(w, master.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,R,C", [(2049, 50, 60), (2049, 60, 50)])
+def test_orthogonalize_by_products_part_by_part(G, R, C, dtype):
+    """1025 and 1024 matrices at a time through the chain of products, which stacks of fewer rows do not take: the
+    ends of both parts."""
+    print(f"case orthogonalize G={G} R={R} C={C} {dtype}", flush=True)
+    x = _grad(G, R, C, R)
+    got = _ortho(x, dtype)
+    for g in (0, 1024, 1025, G - 1):
+        _check_result(got[g], x[g], dtype, TO.COEF, f"matrix {g}")
+
+
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,R,C", [(2049, 50, 60), (2049, 60, 50), (2049, 50, 61)])
+def test_muon_steps_by_products_part_by_part(G, R, C, dtype, nesterov):
+    """Two steps, as in test_muon_steps: momentum, master and w of the second part, which finds the first one's
+    workspace."""
+    print(f"case muon G={G} R={R} C={C} {dtype} nesterov={nesterov}", flush=True)
+    grads, mom0, w0, mom, master, w = _muon(G, R, C, dtype, nesterov)
+    for g in (0, 1024, 1025, G - 1):
+        mg, xg, allowed = mom0[g:g + 1].astype(np.float64), w0[g:g + 1].astype(np.float64), 0.0
+        big = np.abs(mom0[g]) + sum(np.abs(gr[g]) for gr in grads)
+        for gr in grads:
+            mg, xg, o = TO.muon(gr[g:g + 1], mg, xg, **HYPER, nesterov=nesterov)
+            u = gr[g].astype(np.float64) + HYPER["momentum"] * mg[0] if nesterov else mg[0]
+            model = TO.newton_model(u, dtype == "f32")
+            allowed += HYPER["lr"] * HYPER["scale"] * (2 * np.linalg.norm(model - o[0]) + 2.0 ** -20 * np.linalg.norm(o[0]))
+            allowed += 3 * 2.0 ** -24 * np.linalg.norm(xg)
+        assert np.all(np.abs(host(mom[g]).astype(np.float64) - mg[0]) <= 4 * 2.0 ** -24 * big)
+        assert np.linalg.norm(host(master[g]).astype(np.float64) - xg[0]) <= allowed, g
+    if w is not None:
+        assert torch.equal(w, master.to(torch.bfloat16))
