@@ -13,9 +13,9 @@
 // added in f32.  The roundings of a product then act on X
 // from the left only, inside its row space, while a rounding of X itself has null directions, which
 // every later step makes |a| times larger.  So X drops its lower part when what the steps left
-// can make of it is small (kDropLow).  That is 1e-3 to 3e-3 of the result's norm for any rank (no lower parts
-// at all: 2e-2 for rank 64 of 352, 7e-2 for rank 4; everything in bf16: 1e-2 for a full rank and 0.2,
-// 0.6 for those), with 40 % fewer bytes for X than two parts all the way.
+// can make of it is small (kDropLow).  That is 1e-3 (full rank) to 4e-3 (rank 1) of the result's norm with the
+// default steps, and with others what they make of changes of 2^-12 (no lower parts at all: 2e-2 for rank 64 of 352,
+// 7e-2 for rank 4; everything in bf16: 1e-2 for a full rank and 0.2, 0.6 for those), with 40 % fewer bytes for X than two parts all the way.
 // The exact form takes three products, lo hi + hi lo + hi hi, of X, A and a I + B in two parts each.
 //
 // Matrices of few rows (or columns) have a form of their own, on [s, s] in 64 bits: see newton_few_gram_kernel.
@@ -1084,8 +1084,8 @@ hipError_t product(const Product& q, const NewtonPlan& p, int batch, hipStream_t
 
 // Whether X keeps its lower part for step k: a rounding of X (2^-12 of an element) has null
 // directions, which the steps from k on make up to |a_k a_k+1 ...| times larger.  Up to
-// kDropLow that stays at 3e-3 of the norm, next to 1e-3 to 2e-3 of the products' own roundings; for the
-// last step it is only its own |a|.
+// kDropLow that stays at 3e-3 of the norm, next to 1e-3 to 3e-3 of the products' own roundings (default steps); for
+// the last step it is only its own |a|.
 constexpr float kDropLow = 12.f;
 bool keeps_low(const NewtonCall& c, int k) {
   if (c.p.exact) return true;

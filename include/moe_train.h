@@ -77,10 +77,15 @@ size_t moe_muon_workspace_bytes(int G, int R, int C, int dtype);
  *  n: the iteration (host memory, read during the call), or NULL: 5 steps of
  *           (3.4445, -4.7750, 2.0315)
  * dtype MOE_BF16: products of 11-bit (fp16) factors with f32 sums, X itself in 22
- * bits as long as later steps would enlarge its roundings: the result is off by
- * 1e-3 to 3e-3 of its norm, low ranks included (before its rounding to bf16).
- * MOE_F32, and matrices with fewer than 32 rows or columns: factors of 22 bits, as
- * exact as f32 arithmetic.  Up to 48 rows or columns (64 if the other side has 2048 or more),
+ * bits as long as later steps would enlarge its roundings.  With the default steps the
+ * result is off by 1e-3 (full rank) to 4e-3 (rank 1) of its norm, before its rounding to
+ * bf16.  With others by what they make of changes of 2^-12: rank 1 loses 6e-3 for
+ * (4, -6.8, 2.9), (3.9, -6.3, 2.6), (3.7, -5.6, 2.3), (2.9, -3.1, 1.2), (2.8, -3, 1.2), low
+ * ranks 1e-2 to 3e-2 where the first step has a = 8, and steps close to where the
+ * iteration no longer settles (which f32 arithmetic shows by an error of 1e-3) lose the
+ * result: such ones need MOE_F32.
+ * MOE_F32, and matrices with fewer than 32 rows or columns: factors of 22 bits, about as
+ * exact as f32 arithmetic (default steps: 1e-6 for a full rank, 1e-4 for rank 1).  Up to 48 rows or columns (64 if the other side has 2048 or more),
  * where the magnitudes above 1 of the steps' a multiply to at most 4096: 64 bits
  * up to the result.
  * Any G from 1 to 2^30 and R, C from 1 to 2^20 with R*C <= 2^32 and G*R*C <= 2^39.  No step but
@@ -99,7 +104,9 @@ int moe_orthogonalize(int G, int R, int C, int dtype, const moe_newton* n, const
  *           [G, R, C] f32 in and out
  *  w [G, R, C] bf16 out; NULL for MOE_F32, where master is the weight itself
  *  lr: device f32[1], or NULL: p->lr (a captured step follows a schedule by it)
- * Precision and sizes as above (O is not rounded to dtype). */
+ * Precision and sizes as above (O is not rounded to dtype).  MOE_BF16 stands for both the
+ * type of w and the products' factors; bf16 weights by the exact products: MOE_F32 on
+ * master, then a copy of it. */
 typedef struct {
   float lr, momentum, weight_decay, scale;
   int32_t nesterov;

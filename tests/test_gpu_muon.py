@@ -464,3 +464,18 @@ def test_muon_steps_by_products_part_by_part(G, R, C, dtype, nesterov):
         assert np.linalg.norm(host(master[g]).astype(np.float64) - xg[0]) <= allowed, g
     if w is not None:
         assert torch.equal(w, master.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("coef,bound", [
+    (((4.0, -6.8, 2.9), (3.9, -6.3, 2.6), (3.7, -5.6, 2.3), (2.9, -3.1, 1.2), (2.8, -3.0, 1.2)), 1.8e-2),
+    (((8.2, -22.9, 16.5), (4.0, -2.9, 0.52), (3.9, -2.8, 0.52), (3.3, -2.4, 0.49), (2.3, -1.6, 0.4)), 5.6e-2)])
+def test_low_rank_of_steps_that_differ(coef, bound):
+    """Coefficients of its own for every step, low ranks, bf16.  The documented arithmetic (newton_model) is off by at most
+    6.8e-3 and 2.6e-2 of the norm over a dozen draws; twice that, and half a step of the result."""
+    g = np.random.default_rng(3)
+    for R, C in ((200, 300), (300, 200)):
+        x = np.stack([(g.standard_normal((R, r)) @ g.standard_normal((r, C))).astype(np.float32) for r in (1, 4, 16)])
+        got = _ortho(x, "bf16", coef)
+        for i in range(3):
+            ref = TO.newton(x[i], coef)
+            assert np.linalg.norm(got[i] - ref) <= bound * np.linalg.norm(ref), (R, C, i)
