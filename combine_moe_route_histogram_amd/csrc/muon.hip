@@ -1151,7 +1151,9 @@ hipError_t launch_few(const NewtonCall& c, Source u, hipStream_t st) {
   results(c, q);
   for (int g0 = 0; g0 < p.G; g0 += p.few_batch) {
     const int batch = p.G - g0 < p.few_batch ? p.G - g0 : p.few_batch;
-    const int64_t want = (p.l + 63) / 64, most = 1024 / batch + 1;   // about four blocks of 64 columns to a CU
+    // Blocks of 64 columns, about 1024 in all.  By their registers a CU holds eight of them at a time for 16 rows, four for
+    // 32, three for 48 and two for 64.
+    const int64_t want = (p.l + 63) / 64, most = 1024 / batch + 1;
     const int blocks = (int)(want < most ? want : most);
     u.g0 = q.g0 = g0;
     f.u = u;

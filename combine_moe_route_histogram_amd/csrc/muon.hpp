@@ -15,7 +15,10 @@ constexpr int kNewtonPad = 64;       // of both sides of a stored matrix: whole 
 // Fewer rows (or columns) than this take factors of two parts whatever the type: their roundings do
 // not average out (up to 4e-3 of the norm), and the call's time is that of its launches.
 constexpr int kNewtonFewRows = 32;
-constexpr int kNewtonFewBatch = 2048;   // matrices of few rows worked on at a time: at most 60 MB of workspace
+// Matrices of few rows worked on at a time: 63 MB of sums and polynomials for 48 rows, 109 MB for 64.  The workspace also
+// holds what the chain of products would take for them (2.2 GB for 2048 [64, 2048]), as its size is asked for without
+// the coefficients, which decide between the two.
+constexpr int kNewtonFewBatch = 2048;
 constexpr int kNormParts = 256;      // partial sums of a matrix's squares
 
 // Sizes of one call.  A matrix is worked on as X [s, l] with s <= l (the

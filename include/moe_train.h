@@ -68,7 +68,8 @@ typedef struct {
 } moe_newton;
 
 /* Workspace of the two calls below for G matrices [R, C] (0 for sizes that they
- * refuse): at most a few copies of a part of the stack, which is worked on part by part.
+ * refuse): at most a few copies of a part of the stack, which is worked on part by part,
+ * with sides rounded up to 64; for any coefficients.
  * 256-byte aligned, in any state; one for calls that overlap in time each. */
 size_t moe_muon_workspace_bytes(int G, int R, int C, int dtype);
 
