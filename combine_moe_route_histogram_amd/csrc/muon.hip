@@ -761,7 +761,7 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Source s, Start d) {
 // own does by a, but nothing keeps it from turning negative: hence 64 bits throughout, and only as long as
 // the product of a^2 leaves 1e-8 of that (kFewGrow).  |U|^2 is the trace.  Bound by the matrix cores' rate in
 // 64 bits (a [64, 64] product 3 us on its CU) and, for fewer rows, by the chain of loads, barriers and launches: of
-// 64 [32, 1000] 8.5 + 15.7 + 9.0 us, of 1 [12, 14336] 5.4 + 11.4 + 4.0, of 64 [64, 14336] 158 + 53 + 317.
+// 64 [32, 1000] 8.2 + 14.9 + 9.0 us, of 1 [12, 14336] 5.2 + 11.1 + 4.0, of 64 [64, 14336] 150 + 52 + 303.
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
