@@ -24,7 +24,7 @@ __all__ = [
     "moe_expert_ffn_bwd", "moe_sync_status", "moe_route_noalloc", "Tuning", "moe_get_tuning",
     "moe_tuning_predict", "moe_decode_workspace_bytes", "moe_decode", "moe_decode_mx", "moe_mx_bytes",
     "moe_mx_quantize", "moe_mx_dequantize", "moe_balance_workspace_bytes", "moe_balance", "moe_balance_bwd",
-    "Newton", "MuonParams", "NEWTON_COEF", "moe_muon_workspace_bytes", "moe_orthogonalize", "moe_muon",
+    "EXACT", "Newton", "MuonParams", "NEWTON_COEF", "moe_muon_workspace_bytes", "moe_orthogonalize", "moe_muon",
 ]
 
 F32, BF16 = 0, 1
@@ -580,6 +580,7 @@ def moe_balance_bwd(d: Dims, seq_len: int, logits, mask, counts, tokens, dloss, 
 
 # ---------------------------------------------------------------- update by Newton-Schulz products
 
+EXACT = 16   # MOE_EXACT
 NEWTON_COEF = ((3.4445, -4.7750, 2.0315),) * 5
 _NEWTON_MAX_STEPS = 16
 
@@ -629,11 +630,13 @@ def _newton(coef):
     return None if coef is None else ctypes.byref(Newton(coef))
 
 
-def moe_orthogonalize(G: int, R: int, C: int, g, out, ws, coef=None, stream=None):
-    """g [G, R, C] float32 -> out [G, R, C], float32 or bf16 (which sets the precision of the products).
-    coef: (a, b, c) of each step, or None: NEWTON_COEF."""
+def moe_orthogonalize(G: int, R: int, C: int, g, out, ws, coef=None, stream=None, exact=False):
+    """g [G, R, C] float32 -> out [G, R, C], float32 or bf16.  bf16 stands for products of 11-bit factors, too,
+    unless exact (EXACT in the workspace's dtype).  coef: (a, b, c) of each step, or None: NEWTON_COEF."""
     _check_stack(G, R, C)
     code, dt = _stack_dtype(out, "out")
+    if exact:
+        code |= EXACT
     n = G * R * C
     _launch("moe_orthogonalize", stream, (G, R, C, code, _newton(coef)),
             ((g, "g", torch.float32, n), (out, "out", dt, n), (ws, "ws", torch.uint8, 0)),
@@ -652,17 +655,18 @@ def _stack_dtype(t, name):
 
 
 def moe_muon(G: int, R: int, C: int, grad, mom, master, w, ws, *, lr, momentum=0.95, weight_decay=0.0, scale=1.0,
-             nesterov=True, coef=None, stream=None):
+             nesterov=True, coef=None, stream=None, exact=False):
     """One step on a stack of weights, in place: mom and master [G, R, C] float32, w their bf16 copy or
-    None (float32 weights: the products are as exact as float32's).  lr: a number, or a float32
-    tensor of one element on the GPU."""
+    None (float32 weights: the products are as exact as float32's; with w, only if exact, with EXACT in the
+    workspace's dtype).  lr: a number, or a float32 tensor of one element on the GPU."""
     _check_stack(G, R, C)
     if w is not None and not isinstance(w, torch.Tensor):
         raise TypeError("w must be a torch.Tensor or None")
     n, f32 = G * R * C, torch.float32
     on_device = isinstance(lr, torch.Tensor)
     p = MuonParams(0.0 if on_device else lr, momentum, weight_decay, scale, int(bool(nesterov)))
-    _launch("moe_muon", stream, (G, R, C, F32 if w is None else BF16, _newton(coef), ctypes.byref(p)),
+    _launch("moe_muon", stream, (G, R, C, (F32 if w is None else BF16) | (EXACT if exact else 0), _newton(coef),
+                                ctypes.byref(p)),
             ((lr if on_device else None, "lr", f32, 1), (grad, "grad", f32, n), (mom, "mom", f32, n),
              (master, "master", f32, n), (w, "w", torch.bfloat16, n), (ws, "ws", torch.uint8, 0)),
             (_numel(ws),))

@@ -1167,7 +1167,7 @@ hipError_t launch_few(const NewtonCall& c, Source u, hipStream_t st) {
 
 }  // namespace
 
-NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
+NewtonPlan newton_plan(int G, int R, int C, bool exact) {
   NewtonPlan p{};
   p.G = G; p.R = R; p.C = C;
   p.tall = R > C;
@@ -1175,7 +1175,7 @@ NewtonPlan newton_plan(int G, int R, int C, bool bf16) {
   p.l = p.tall ? R : C;
   p.sp = up(p.s, kNewtonPad);
   p.lp = up(p.l, kNewtonPad);
-  p.exact = !bf16 || p.s < kNewtonFewRows;
+  p.exact = exact || p.s < kNewtonFewRows;
   p.small = (int64_t)G * (p.sp / 64) * (p.lp / 64) <= kSmallTiles;
   // About 2048 tiles of 256 x 256 to a launch: 8 rounds over the 256 CUs, of which the last one
   // is partly empty; more would only take memory (at most 2^30 elements of X, or one matrix).

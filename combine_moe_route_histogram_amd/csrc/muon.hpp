@@ -36,7 +36,7 @@ struct NewtonPlan {
   // workspace sections (byte offsets)
   size_t parts, xh[2], xl[2], th[2], tl[2], ah, al, bh, bl, total;
 };
-NewtonPlan newton_plan(int G, int R, int C, bool bf16);
+NewtonPlan newton_plan(int G, int R, int C, bool exact);
 
 struct NewtonCall {
   NewtonPlan p;

@@ -96,10 +96,12 @@ int check_stack(int G, int R, int C, int dtype) {
     return fail(MOE_EUNSUPPORTED, "R*C must be at most 2^32 (R=%d, C=%d)", R, C);
   if ((double)G * R * C > 549755813888.0)
     return fail(MOE_EUNSUPPORTED, "G*R*C must be at most 2^39 (G=%d, R=%d, C=%d)", G, R, C);
-  if (dtype != MOE_F32 && dtype != MOE_BF16)
-    return fail(MOE_EUNSUPPORTED, "dtype must be MOE_F32 or MOE_BF16 (got %d)", dtype);
+  if ((dtype & ~MOE_EXACT) != MOE_F32 && (dtype & ~MOE_EXACT) != MOE_BF16)
+    return fail(MOE_EUNSUPPORTED, "dtype must be MOE_F32 or MOE_BF16, with or without MOE_EXACT (got %d)", dtype);
   return MOE_OK;
 }
+bool is_bf16(int dtype) { return (dtype & ~MOE_EXACT) == MOE_BF16; }
+bool is_exact(int dtype) { return dtype != MOE_BF16; }
 
 // The iteration's coefficients: the caller's, or the default ones in `own`.
 int check_newton(const moe_newton* n, moe_newton* own, const moe_newton** out) {
@@ -184,7 +186,7 @@ int moe_balance_bwd(const moe_dims* d, int seq_len, const float* logits, const u
 
 size_t moe_muon_workspace_bytes(int G, int R, int C, int dtype) {
   if (check_stack(G, R, C, dtype) != MOE_OK) return 0;
-  return newton_plan(G, R, C, dtype == MOE_BF16).total;
+  return newton_plan(G, R, C, is_exact(dtype)).total;
 }
 
 int moe_orthogonalize(int G, int R, int C, int dtype, const moe_newton* n, const float* g, void* out,
@@ -195,12 +197,12 @@ int moe_orthogonalize(int G, int R, int C, int dtype, const moe_newton* n, const
   MOE_TRY(check_ptr(g, "g"));
   MOE_TRY(check_ptr(out, "out"));
   NewtonCall c{};
-  c.p = newton_plan(G, R, C, dtype == MOE_BF16);
+  c.p = newton_plan(G, R, C, is_exact(dtype));
   MOE_TRY(check_ws_bytes(ws, ws_bytes, c.p.total));
   c.ws = ws;
   c.steps = n->steps;
   c.coef = n->coef;
-  c.bf16 = dtype == MOE_BF16;
+  c.bf16 = is_bf16(dtype);
   c.g = g;
   c.out = out;
   return hip_status(launch_newton(c, as_stream(stream)), "moe_orthogonalize");
@@ -217,15 +219,15 @@ int moe_muon(int G, int R, int C, int dtype, const moe_newton* n, const moe_muon
   MOE_TRY(check_ptr(grad, "grad"));
   MOE_TRY(check_ptr(mom, "mom"));
   MOE_TRY(check_ptr(master, "master"));
-  if (dtype == MOE_BF16) MOE_TRY(check_ptr(w, "w"));
+  if (is_bf16(dtype)) MOE_TRY(check_ptr(w, "w"));
   else if (w) return fail(MOE_EINVAL, "w must be NULL for MOE_F32: master is the weight itself");
   NewtonCall c{};
-  c.p = newton_plan(G, R, C, dtype == MOE_BF16);
+  c.p = newton_plan(G, R, C, is_exact(dtype));
   MOE_TRY(check_ws_bytes(ws, ws_bytes, c.p.total));
   c.ws = ws;
   c.steps = n->steps;
   c.coef = n->coef;
-  c.bf16 = dtype == MOE_BF16;
+  c.bf16 = is_bf16(dtype);
   c.g = grad;
   c.mom = mom;
   c.master = master;

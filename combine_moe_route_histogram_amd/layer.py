@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (BF16, F32, Dims, moe_balance, moe_balance_bwd, moe_balance_workspace_bytes, moe_combine,
+from . import (BF16, EXACT, F32, Dims, moe_balance, moe_balance_bwd, moe_balance_workspace_bytes, moe_combine,
                moe_combine_bwd, moe_decode, moe_decode_mx, moe_decode_workspace_bytes, moe_dispatch,
                moe_dispatch_bwd, moe_dispatch_ffn, moe_expert_ffn_bwd, moe_expert_ffn_bwd_data,
                moe_expert_ffn_bwd_weight, moe_expert_ffn_down, moe_expert_ffn_up, moe_ffn_combine,
@@ -175,15 +175,18 @@ WEIGHTS = ("w1", "w3", "w2", "ws1", "ws3", "ws2")
 
 class MuonState:
     """Momentum, float32 weights and the shared workspace of the optimizer for the weights in p (made on
-    the current stream).  float32 weights are updated in place, bf16 ones are copies of `master`."""
+    the current stream).  float32 weights are updated in place, bf16 ones are copies of `master`.  exact: bf16
+    weights, too, are updated by products as exact as float32's, in about 2.5 times the time."""
 
-    def __init__(self, p: dict):
+    def __init__(self, p: dict, exact: bool = False):
+        self.exact = exact
         self.names = [n for n in WEIGHTS if p.get(n) is not None]
         self.mom = {n: torch.zeros(p[n].shape, dtype=torch.float32, device=p[n].device) for n in self.names}
         self.master = {n: p[n].float() for n in self.names}      # float32 weights: p[n] itself
         need = 256
         for n in self.names:
-            need = max(need, moe_muon_workspace_bytes(*p[n].shape, BF16 if p[n].dtype == torch.bfloat16 else F32))
+            dtype = (BF16 if p[n].dtype == torch.bfloat16 else F32) | (EXACT if exact else 0)
+            need = max(need, moe_muon_workspace_bytes(*p[n].shape, dtype))
         self.ws = torch.empty(need, dtype=torch.uint8, device=p[self.names[0]].device)
 
 
@@ -196,4 +199,4 @@ def muon_step(m: MuonState, p: dict, b: Buffers, lr, momentum=0.95, weight_decay
         G, R, C = w.shape
         moe_muon(G, R, C, getattr(b, "d" + n), m.mom[n], m.master[n], w if w.dtype == torch.bfloat16 else None, m.ws,
                  lr=lr, momentum=momentum, weight_decay=weight_decay, scale=0.2 * max(R, C) ** 0.5, nesterov=nesterov,
-                 coef=coef, stream=stream)
+                 coef=coef, stream=stream, exact=m.exact)

@@ -479,3 +479,49 @@ def test_low_rank_of_steps_that_differ(coef, bound):
         for i in range(3):
             ref = TO.newton(x[i], coef)
             assert np.linalg.norm(got[i] - ref) <= bound * np.linalg.norm(ref), (R, C, i)
+
+
+@pytest.mark.parametrize("G,R,C", [(2, 65, 63), (1, 130, 257), (3, 257, 130), (40, 520, 264), (40, 264, 520), (3, 20, 90)])
+def test_exact_products_of_bf16_results(G, R, C):
+    """The float32 call's bits, rounded: results of both types, small and large tiles, both orientations."""
+    print(f"case exact G={G} R={R} C={C}", flush=True)
+    x = _dev(_grad(G, R, C, R))
+    f32, out = torch.empty(G, R, C, device="cuda"), torch.empty(G, R, C, dtype=torch.bfloat16, device="cuda")
+    ws = [torch.full((M.moe_muon_workspace_bytes(G, R, C, dt),), 0xFF, dtype=torch.uint8, device="cuda")
+          for dt in (M.F32, M.BF16 | M.EXACT)]
+    M.moe_orthogonalize(G, R, C, x, f32, ws[0])
+    M.moe_orthogonalize(G, R, C, x, out, ws[1], exact=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out, f32.to(torch.bfloat16))
+    again = torch.empty_like(f32)
+    M.moe_orthogonalize(G, R, C, x, again, ws[0], exact=True)       # float32 is exact with or without
+    assert torch.equal(again, f32)
+
+
+@pytest.mark.parametrize("G,R,C", [(2, 130, 70), (40, 520, 264), (40, 264, 522), (3, 20, 90)])
+def test_exact_steps_of_bf16_weights(G, R, C):
+    print(f"case exact muon G={G} R={R} C={C}", flush=True)
+    grads, mom0, w0, mom, master, _ = _muon(G, R, C, "f32", True)
+    m, x, w = _dev(mom0), _dev(w0), torch.full((G, R, C), 9.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((M.moe_muon_workspace_bytes(G, R, C, M.BF16 | M.EXACT),), 0xFF, dtype=torch.uint8, device="cuda")
+    for g in grads:
+        M.moe_muon(G, R, C, _dev(g), m, x, w, ws, nesterov=True, exact=True, **HYPER)
+    torch.cuda.synchronize()
+    assert torch.equal(m, mom) and torch.equal(x, master) and torch.equal(w, master.to(torch.bfloat16))
+
+
+def test_exact_step_of_a_layer():
+    """The layer's own call: a state made for exact products updates bf16 weights by them."""
+    cfg = custom_config(64, 64, 6, 2, 96)
+    p = device_inputs(synth.make_inputs(cfg))
+    d = L.make_dims(cfg.T, cfg.H, cfg.E, cfg.K, cfg.I)
+    b = L.Buffers(d)
+    L.forward(b, p, fused=True)
+    L.backward(b, p, fused=True)
+    q = {n: p[n].float() for n in ("w1", "w3", "w2")}              # the same weights in float32
+    exact, f32 = L.MuonState(p, exact=True), L.MuonState(q)
+    L.muon_step(exact, p, b, lr=0.01)
+    L.muon_step(f32, q, b, lr=0.01)
+    L.check()
+    for n in exact.names:
+        assert torch.equal(exact.master[n], q[n]) and torch.equal(p[n], q[n].to(torch.bfloat16))

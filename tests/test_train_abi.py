@@ -244,3 +244,15 @@ def test_model_of_the_arithmetic():
         ref = TO.newton(u)
         err = lambda v: np.linalg.norm(v - ref) / np.linalg.norm(ref)
         assert err(TO.newton_model(u, True)) < 1e-4 and err(TO.newton_model(u, False)) < 4e-3
+
+
+def test_exact_is_a_flag_of_either_type(lib):
+    assert M.EXACT & (M.F32 | M.BF16) == 0
+    need = {dt: lib.moe_muon_workspace_bytes(64, 256, 512, dt) for dt in (0, 1, M.EXACT, 1 | M.EXACT)}
+    assert need[1 | M.EXACT] == need[M.EXACT] == need[0] > need[1] > 0
+    assert _ortho(lib, 64, 256, 512, 1 | M.EXACT, ws_bytes=need[1]) == 3       # the exact form's workspace
+    for bad in (2 | M.EXACT, 1 | 2 * M.EXACT, -M.EXACT):
+        assert _ortho(lib, dtype=bad) == 2 and _muon(lib, dtype=bad) == 2
+        assert lib.moe_muon_workspace_bytes(2, 8, 16, bad) == 0
+    assert _muon(lib, dtype=1 | M.EXACT, w=None) == 1 and "w" in M.moe_last_error()
+    assert _muon(lib, dtype=M.EXACT) == 1 and "w must be NULL" in M.moe_last_error()
